@@ -405,6 +405,119 @@ int w4a4_linear_plan(int64_t M, int64_t N, int64_t K, int32_t fmt, int32_t with_
  * use for (M, N, K, fmt); 0 when the shape runs without one. */
 size_t w4a4_workspace_size(int64_t M, int64_t N, int64_t K, int32_t fmt);
 
+/* ---------------------------------------------------------------------------
+ * 16-bit operators beside the quantized linears
+ *
+ * One step of a world-action model needs more than its low-bit linears: the
+ * attention of an action chunk over the observation, the products of the
+ * layers that stay in 16 bits, and the normalisation of the autoencoder's
+ * features.  The conventions at the top of this file hold for these calls
+ * too, with two additions: an operand that a mask or a length excludes is
+ * never read into the result, whatever bits it holds (NaN included), and a
+ * workspace is optional (NULL runs an unsplit plan with the same semantics;
+ * the order of its sums, and so the last bits, may differ).  For a given plan
+ * results do not depend on timing: no atomics are used.
+ * ------------------------------------------------------------------------- */
+
+/* w4a4_prefix_attention -- softmax attention of B sequences of T queries over
+ * one prefix of P keys that all of them share, joined with S keys of each
+ * sequence's own:
+ *   out[b,t,h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q[b,t,h] . k_j)
+ * over the prefix keys j with prefix_keep[j] != 0 and the own keys
+ * j < own_len[b] (causal = 0) or j <= own_len[b] - T + t (causal = 1: the T
+ * queries are the sequence's last T positions).  Query head h reads KV head
+ * h / (Hq / Hkv).  A row that sees no key is zero.  Scores, softmax sums and
+ * outputs accumulate in fp32; the probabilities enter the second product
+ * as bf16; one rounding to bf16 at the end.
+ *  q, out    bf16 [B, T, Hq, D];  k_prefix, v_prefix  bf16 [P, Hkv, D];
+ *            k_own, v_own  bf16 [B, S, Hkv, D].  The last dimension is
+ *            contiguous; the other strides are in elements, multiples of 8,
+ *            at most 2^24 (batch strides: any).  Pointers 16-byte aligned.
+ *            out overlaps no input.
+ *  own_len   device int32[B], clamped to [0, S]; NULL: S for every sequence.
+ *  prefix_keep  device uint8[P], or NULL: all kept.
+ * Shape rules: D is 64, 128 or 256; Hq a multiple of Hkv; P, S >= 0 (their
+ * pointers may be NULL when 0).  An own value row holding NaN or Inf makes
+ * every row that sees it NaN, and no other row. */
+typedef struct w4a4_attn {
+  int64_t B, T, Hq, Hkv, D, P, S;
+  float scale;
+  int32_t causal;
+  const void* q;
+  int64_t q_sb, q_st, q_sh;
+  const void* k_prefix;
+  int64_t kp_sp, kp_sh;
+  const void* v_prefix;
+  int64_t vp_sp, vp_sh;
+  const void* k_own;
+  int64_t ko_sb, ko_ss, ko_sh;
+  const void* v_own;
+  int64_t vo_sb, vo_ss, vo_sh;
+  const int32_t* own_len;
+  const uint8_t* prefix_keep;
+  void* out;
+  int64_t o_sb, o_st, o_sh;
+} w4a4_attn;
+int w4a4_prefix_attention(const w4a4_attn* a, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace w4a4_prefix_attention uses for these sizes (0: none). */
+size_t w4a4_prefix_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t P, int64_t S);
+
+/* bf16_linear -- the 16-bit sibling of the quantized linears, with bias,
+ * activation and residual in its epilogue:
+ *   y = act(x W^T + bias) + residual
+ * (QuantWAMs sec. 4.2: layers kept out of quantization run in BF16.)
+ *  x   bf16 M x K, row stride ldx;  w  bf16 NW x K, row stride ldw, with
+ *      NW = N, or 2 N for W4A4_ACT_SWIGLU: rows [0, N) are the gate's and
+ *      [N, 2N) the up projection's, y = silu(gate) * up + residual.
+ *  ep  NULL (no bias, activation or residual) or:
+ *      act       W4A4_ACT_*; GELU is x Phi(x) (erf), GELU_TANH its tanh form.
+ *      bias      [NW], bias_dtype F32 or BF16, or NULL.
+ *      residual  M x N of y_dtype, row stride ldr, or NULL; may be y itself
+ *                (same ldr), otherwise y overlaps no input.
+ *  y   M x N, F32 or BF16, row stride ldy.
+ * The sum, bias, activation and residual are fp32; one rounding to y_dtype.
+ * Shape rules: K % 8 == 0, K <= 2^24; M, N <= 2^30; ldx, ldw % 8 == 0 and
+ * <= 2^22; ldy, ldr <= 2^22.  x, w 16-byte aligned; bias, residual and y by
+ * their element size. */
+enum { W4A4_ACT_NONE = 0, W4A4_ACT_RELU = 1, W4A4_ACT_GELU = 2, W4A4_ACT_GELU_TANH = 3, W4A4_ACT_SILU = 4,
+       W4A4_ACT_SWIGLU = 5 };
+typedef struct w4a4_epilogue {
+  int32_t act;
+  int32_t bias_dtype;
+  const void* bias;
+  const void* residual;
+  int64_t ldr;
+} w4a4_epilogue;
+int bf16_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t M, int64_t N, int64_t K,
+                const w4a4_epilogue* ep, void* y, int32_t y_dtype, int64_t ldy,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace bf16_linear uses for (M, N, K, act); 0: none. */
+size_t w4a4_bf16_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act);
+
+/* w4a4_group_norm_act -- group normalisation with an activation on
+ * channels-last features (N samples of S positions x C channels; video
+ * features flatten frames, rows and columns into S):
+ *   y = act((x - mean) / sqrt(var + eps) * weight[c] + bias[c])
+ * with mean and (biased) variance over the S * (C / groups) elements of a
+ * sample's group.  Statistics in fp32 from differences to a per-channel
+ * shift, joined pairwise, so that a large mean costs no accuracy.
+ *  x, y    dtype F32 or BF16; channels contiguous; position stride x_ss /
+ *          y_ss >= C, sample stride x_sn / y_sn (elements).  y may be x
+ *          itself (same strides), otherwise it overlaps no input.
+ *  weight, bias  fp32[C] or NULL (1 and 0).
+ *  act     W4A4_ACT_NONE, RELU, GELU, GELU_TANH or SILU.
+ * Shape rules: C a multiple of groups, C <= 65536; S * C <= 2^40; eps >= 0.
+ * N == 0 or S == 0 is a no-op. */
+int w4a4_group_norm_act(const void* x, int32_t dtype, int64_t N, int64_t S, int64_t C, int64_t groups,
+                        int64_t x_sn, int64_t x_ss, const float* weight, const float* bias, float eps,
+                        int32_t act, void* y, int64_t y_sn, int64_t y_ss,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace w4a4_group_norm_act uses for these sizes; 0: none. */
+size_t w4a4_group_norm_workspace(int64_t N, int64_t S, int64_t C, int64_t groups);
+
 const char* w4a4_status_string(int status);
 const char* w4a4_last_error(void);
 int w4a4_abi_version(void);

@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw4a4.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
-SOURCES = ["quantize.hip", "gemm_int.hip", "gemm_wide.hip", "branch.hip", "gptq.hip", "abi.cpp"]
+SOURCES = ["quantize.hip", "gemm_int.hip", "gemm_wide.hip", "branch.hip", "gptq.hip", "attention.hip",
+           "gemm_bf16.hip", "group_norm.hip", "abi.cpp", "abi_dense.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-ffp-contract=off",

@@ -6,37 +6,33 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
-#include <string>
 
 #include "../../include/w4a4.h"
+#include "abi_util.h"
 #include "launch.h"
 
 static_assert(w4a4::kNoAllocScratchBytes == W4A4_NOALLOC_SCRATCH_BYTES, "one size for the static split-K buffer");
 
 namespace {
+thread_local char g_last_error[512];
+}  // namespace
 
-thread_local std::string g_last_error;
-
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace w4a4 {
 int fail(int status, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return status;
 }
+}  // namespace w4a4
 
-int ok() { return W4A4_OK; }
+namespace {
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int launch_status(hipError_t e, const char* what) {
-  if (e != hipSuccess)
-    return fail(W4A4_ERR_LAUNCH_FAILED, "%s: %s", what, hipGetErrorString(e));
-  return ok();
-}
+using w4a4::aligned;
+using w4a4::fail;
+using w4a4::launch_status;
+using w4a4::ok;
 
 size_t dt_size(int32_t dt) { return dt == W4A4_DT_BF16 ? 2 : 4; }
 
@@ -448,7 +444,7 @@ const char* w4a4_status_string(int status) {
   }
 }
 
-const char* w4a4_last_error(void) { return g_last_error.c_str(); }
+const char* w4a4_last_error(void) { return g_last_error; }
 
 int w4a4_abi_version(void) { return W4A4_ABI_VERSION; }
 

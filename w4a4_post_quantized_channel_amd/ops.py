@@ -24,12 +24,16 @@ BRANCH_NONE, BRANCH_BF16 = 0, 1
 FMTS = {"int4": FMT_INT4, "int8": FMT_INT8, "nvfp4": FMT_NVFP4, "w4a8": FMT_W4A8, "fp8": FMT_FP8}
 ORDERS = {"smooth_then_rotate": ORDER_SMOOTH_THEN_ROTATE,
           "rotate_then_smooth": ORDER_ROTATE_THEN_SMOOTH}
+# activations of the 16-bit operators (swiglu: bf16_linear only)
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
 ABI_VERSION = 3
 MAX_BRANCH = 128   # W4A4_MAX_BRANCH: largest branch width (rank or kept channels)
 
 EXPORTS = ["quantize_act", "quantize_act_gather", "quantize_act_lowrank", "quantize_act_project", "pack_weights", "pack_weights_gptq", "w4a4_gptq_workspace_size", "w4a4_linear", "w4a4_linear_noalloc", "w8a8_linear", "w4a8_linear", "fp8_linear", "lowrank_add",
            "w4a4_lowrank_project", "w4a4_lowrank_width", "w4a4_transform_amax", "w4a4_linear_plan",
            "w4a4_workspace_size", "w4a4_status_string",
+           "w4a4_prefix_attention", "w4a4_prefix_attention_workspace", "bf16_linear", "w4a4_bf16_workspace_size",
+           "w4a4_group_norm_act", "w4a4_group_norm_workspace",
            "w4a4_last_error", "w4a4_abi_version"]
 
 
@@ -42,6 +46,26 @@ class BranchDesc(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("r", ctypes.c_int32), ("ra", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("a", ctypes.c_void_p), ("lda", ctypes.c_int64),
                 ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64)]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "T", "Hq", "Hkv", "D", "P", "S")] +
+                [("scale", ctypes.c_float), ("causal", ctypes.c_int32)] +
+                [("q", ctypes.c_void_p), ("q_sb", ctypes.c_int64), ("q_st", ctypes.c_int64), ("q_sh", ctypes.c_int64),
+                 ("k_prefix", ctypes.c_void_p), ("kp_sp", ctypes.c_int64), ("kp_sh", ctypes.c_int64),
+                 ("v_prefix", ctypes.c_void_p), ("vp_sp", ctypes.c_int64), ("vp_sh", ctypes.c_int64),
+                 ("k_own", ctypes.c_void_p), ("ko_sb", ctypes.c_int64), ("ko_ss", ctypes.c_int64),
+                 ("ko_sh", ctypes.c_int64),
+                 ("v_own", ctypes.c_void_p), ("vo_sb", ctypes.c_int64), ("vo_ss", ctypes.c_int64),
+                 ("vo_sh", ctypes.c_int64),
+                 ("own_len", ctypes.c_void_p), ("prefix_keep", ctypes.c_void_p),
+                 ("out", ctypes.c_void_p), ("o_sb", ctypes.c_int64), ("o_st", ctypes.c_int64),
+                 ("o_sh", ctypes.c_int64)])
+
+
+class EpilogueDesc(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("bias_dtype", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64)]
 
 
 class W4A4Error(RuntimeError):
@@ -76,6 +100,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "w4a4_linear_plan": [i64, i64, i64, i32, i32, ctypes.POINTER(ctypes.c_int32)],
         "w4a4_lowrank_width": [i64, i64, i64],
         "w4a4_transform_amax": [vp, i32, i64, i64, i64, vp, qd, vp, vp],
+        "w4a4_prefix_attention": [ctypes.POINTER(AttnDesc), vp, sz, vp],
+        "w4a4_prefix_attention_workspace": [i64] * 7,
+        "bf16_linear": [vp, i64, vp, i64, i64, i64, i64, ctypes.POINTER(EpilogueDesc), vp, i32, i64, vp, sz, vp],
+        "w4a4_bf16_workspace_size": [i64, i64, i64, i32],
+        "w4a4_group_norm_act": [vp, i32, i64, i64, i64, i64, i64, i64, vp, vp, f32, i32, vp, i64, i64, vp, sz, vp],
+        "w4a4_group_norm_workspace": [i64] * 4,
         "w4a4_status_string": [ctypes.c_int],
         "w4a4_last_error": [],
         "w4a4_abi_version": [],
@@ -86,6 +116,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn.restype = ctypes.c_int
     lib.w4a4_workspace_size.restype = ctypes.c_size_t
     lib.w4a4_gptq_workspace_size.restype = ctypes.c_size_t
+    lib.w4a4_prefix_attention_workspace.restype = ctypes.c_size_t
+    lib.w4a4_bf16_workspace_size.restype = ctypes.c_size_t
+    lib.w4a4_group_norm_workspace.restype = ctypes.c_size_t
     lib.w4a4_lowrank_width.restype = ctypes.c_int64
     lib.w4a4_status_string.restype = ctypes.c_char_p
     lib.w4a4_last_error.restype = ctypes.c_char_p
@@ -399,3 +432,144 @@ def lowrank_project(x: torch.Tensor, *, l1t: Optional[torch.Tensor] = None, idx:
     _check("w4a4_lowrank_project", LIB.w4a4_lowrank_project(_ptr(x), _dtype_code(x), M, K, ldx, _ptr(l1t), _ptr(idx),
                                                             r, _ptr(out), out.stride(0), _stream(stream)))
     return out[:, :2 * r] if l1t is not None else out
+
+
+# ---------------------------------------------------------------------------
+# 16-bit operators beside the quantized linears
+# ---------------------------------------------------------------------------
+def _ld(rows: int, cols: int, ld: int) -> int:
+    """A row stride; that of a single row is not used and may be anything."""
+    return ld if rows > 1 else cols
+
+
+def _act_code(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}: one of {sorted(ACTS)}")
+    return ACTS[act]
+
+
+def _ws(nbytes: int, device) -> Optional[torch.Tensor]:
+    return None if nbytes == 0 else torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _ws_args(workspace):
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def _attn_operand(name: str, t: torch.Tensor, shape):
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bf16")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return [s if n > 1 else 0 for n, s in zip(t.shape, t.stride())]   # a dimension of one is never stepped
+
+
+def make_prefix_attention_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, P: int, S: int,
+                                    device="cuda") -> Optional[torch.Tensor]:
+    return _ws(int(LIB.w4a4_prefix_attention_workspace(B, T, Hq, Hkv, D, P, S)), device)
+
+
+def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, k_own: torch.Tensor,
+                     v_own: torch.Tensor, *, own_len: Optional[torch.Tensor] = None,
+                     prefix_keep: Optional[torch.Tensor] = None, causal: bool = False,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None, workspace=None,
+                     stream=None) -> torch.Tensor:
+    """Attention of a batch over one shared prefix and each sequence's own keys.
+
+    q [B, T, Hq, D]; k_prefix, v_prefix [P, Hkv, D]; k_own, v_own [B, S, Hkv, D]
+    (all bf16, any strides that are multiples of 8, last dimension contiguous);
+    own_len int32[B] or None; prefix_keep bool / uint8 [P] or None; scale
+    defaults to 1 / sqrt(D).  See include/w4a4.h for the formula and the masks.
+    """
+    B, T, Hq, D = q.shape
+    P, Hkv = k_prefix.shape[:2]
+    S = k_own.shape[1]
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    qs, os_ = _attn_operand("q", q, (B, T, Hq, D)), _attn_operand("out", out, (B, T, Hq, D))
+    kps, vps = _attn_operand("k_prefix", k_prefix, (P, Hkv, D)), _attn_operand("v_prefix", v_prefix, (P, Hkv, D))
+    kos, vos = _attn_operand("k_own", k_own, (B, S, Hkv, D)), _attn_operand("v_own", v_own, (B, S, Hkv, D))
+    if own_len is not None and (own_len.dtype != torch.int32 or own_len.shape != (B,) or not own_len.is_contiguous()):
+        raise TypeError("own_len must be a contiguous int32[B] tensor")
+    if prefix_keep is not None and (prefix_keep.dtype not in (torch.bool, torch.uint8) or prefix_keep.shape != (P,)
+                                    or not prefix_keep.is_contiguous()):
+        raise TypeError("prefix_keep must be a contiguous bool or uint8 [P] tensor")
+    d = AttnDesc(B, T, Hq, Hkv, D, P, S, D ** -0.5 if scale is None else scale, int(causal),
+                 q.data_ptr(), qs[0], qs[1], qs[2], k_prefix.data_ptr(), kps[0], kps[1],
+                 v_prefix.data_ptr(), vps[0], vps[1], k_own.data_ptr(), kos[0], kos[1], kos[2],
+                 v_own.data_ptr(), vos[0], vos[1], vos[2], None if own_len is None else own_len.data_ptr(),
+                 None if prefix_keep is None else prefix_keep.data_ptr(), out.data_ptr(), os_[0], os_[1], os_[2])
+    st = LIB.w4a4_prefix_attention(ctypes.byref(d), *_ws_args(workspace), _stream(stream))
+    _check("w4a4_prefix_attention", st)
+    return out
+
+
+def make_bf16_linear_workspace(M: int, N: int, K: int, act: str = "none", device="cuda") -> Optional[torch.Tensor]:
+    return _ws(int(LIB.w4a4_bf16_workspace_size(M, N, K, _act_code(act))), device)
+
+
+def bf16_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = None, act: str = "none",
+                residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, y_dtype=torch.bfloat16,
+                workspace=None, stream=None) -> torch.Tensor:
+    """y = act(x w^T + bias) + residual in bf16 with fp32 sums (see include/w4a4.h).
+
+    w holds N rows, or 2 N for act="swiglu" (gate rows, then up rows); bias is
+    fp32 or bf16 with one entry per row of w; residual has y's shape and type
+    and may be y itself.
+    """
+    M, K, ldx = _rowmajor(x)
+    NW, Kw, ldw = _rowmajor(w)
+    code = _act_code(act)
+    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+        raise TypeError("bf16_linear takes bf16 x and w")
+    if Kw != K or (code == 5 and NW % 2):
+        raise ValueError(f"w of shape {tuple(w.shape)} does not fit x of shape {tuple(x.shape)} with act={act!r}")
+    N = NW // 2 if code == 5 else NW
+    if y is None:
+        y = torch.empty((M, N), dtype=y_dtype, device=x.device)
+    My, Ny, ldy = _rowmajor(y)
+    if (My, Ny) != (M, N):
+        raise ValueError(f"y has shape {tuple(y.shape)}, expected {(M, N)}")
+    ep = EpilogueDesc(code, DT_F32, None, None, 0)
+    if bias is not None:
+        if bias.shape != (NW,) or not bias.is_contiguous():
+            raise ValueError("bias must be contiguous, one entry per row of w")
+        ep.bias_dtype, ep.bias = _dtype_code(bias), bias.data_ptr()
+    if residual is not None:
+        Mr, Nr, ldr = _rowmajor(residual)
+        if residual.dtype != y.dtype or (Mr, Nr) != (M, N):
+            raise TypeError("residual must have y's shape and dtype")
+        ep.residual, ep.ldr = residual.data_ptr(), _ld(M, N, ldr)
+    st = LIB.bf16_linear(x.data_ptr(), _ld(M, K, ldx), w.data_ptr(), _ld(NW, K, ldw), M, N, K, ctypes.byref(ep),
+                         y.data_ptr(), _dtype_code(y), _ld(M, N, ldy), *_ws_args(workspace), _stream(stream))
+    _check("bf16_linear", st)
+    return y
+
+
+def make_group_norm_workspace(N: int, S: int, C: int, groups: int, device="cuda") -> Optional[torch.Tensor]:
+    return _ws(int(LIB.w4a4_group_norm_workspace(N, S, C, groups)), device)
+
+
+def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+                   bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5, act: str = "silu",
+                   out: Optional[torch.Tensor] = None, workspace=None, stream=None) -> torch.Tensor:
+    """Group normalisation with an activation on channels-last features x [N, S, C]
+    (fp32 or bf16, channels contiguous; weight, bias fp32[C] or None; out may be x)."""
+    if x.dim() != 3 or x.stride(2) != 1 or x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("x must be an fp32 or bf16 [N, S, C] tensor with contiguous channels")
+    N, S, C = x.shape
+    if out is None:
+        out = torch.empty((N, S, C), dtype=x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype != x.dtype or out.stride(2) != 1:
+        raise TypeError("out must have x's shape and dtype, with contiguous channels")
+    for name, v in (("weight", weight), ("bias", bias)):
+        if v is not None and (v.dtype != torch.float32 or v.shape != (C,) or not v.is_contiguous()):
+            raise TypeError(f"{name} must be a contiguous fp32[C] tensor")
+    st = LIB.w4a4_group_norm_act(x.data_ptr(), _dtype_code(x), N, S, C, groups, x.stride(0),
+                                 _ld(S, C, x.stride(1)), _ptr(weight), _ptr(bias), float(eps), _act_code(act),
+                                 out.data_ptr(), out.stride(0), _ld(S, C, out.stride(1)), *_ws_args(workspace),
+                                 _stream(stream))
+    _check("w4a4_group_norm_act", st)
+    return out
