@@ -432,13 +432,14 @@ size_t w4a4_workspace_size(int64_t M, int64_t N, int64_t K, int32_t fmt);
  *  q, out    bf16 [B, T, Hq, D];  k_prefix, v_prefix  bf16 [P, Hkv, D];
  *            k_own, v_own  bf16 [B, S, Hkv, D].  The last dimension is
  *            contiguous; the other strides are in elements, multiples of 8,
- *            at most 2^24 (batch strides: any).  Pointers 16-byte aligned.
+ *            at most 2^22 (batch strides: any).  Pointers 16-byte aligned.
  *            out overlaps no input.
  *  own_len   device int32[B], clamped to [0, S]; NULL: S for every sequence.
  *  prefix_keep  device uint8[P], or NULL: all kept.
  * Shape rules: D is 64, 128 or 256; Hq a multiple of Hkv; P, S >= 0 (their
- * pointers may be NULL when 0).  An own value row holding NaN or Inf makes
- * every row that sees it NaN, and no other row. */
+ * pointers may be NULL when 0).  NaN or Inf among a sequence's own values
+ * reaches the rows that see them, as NaN or Inf in part or all of the row,
+ * and no other row. */
 typedef struct w4a4_attn {
   int64_t B, T, Hq, Hkv, D, P, S;
   float scale;

@@ -26,7 +26,7 @@ int check_workspace(const char* fn, const void* ws, size_t bytes, size_t need) {
 int check_stride(const char* fn, const char* what, int64_t s) {
   if (s < 0) return fail(W4A4_ERR_INVALID_ARG, "%s: negative %s stride", fn, what);
   if (s % 8 != 0) return fail(W4A4_ERR_MISALIGNED, "%s: %s stride %lld not a multiple of 8", fn, what, (long long)s);
-  if (s > (1LL << 24)) return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: %s stride above 2^24 elements", fn, what);
+  if (s > (1LL << 22)) return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: %s stride above 2^22 elements", fn, what);
   return ok();
 }
 
@@ -123,7 +123,7 @@ int bf16_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t 
     return fail(W4A4_ERR_INVALID_ARG, "%s: row stride below the row length", fn);
   if (ldx % 8 != 0 || ldw % 8 != 0) return fail(W4A4_ERR_MISALIGNED, "%s: ldx / ldw not a multiple of 8", fn);
   const int64_t top = 1LL << 22;
-  if ((M > 1 && ldx > top) || ldw > (1LL << 24) || ldy > top || (ep->residual && ep->ldr > top))
+  if ((M > 1 && ldx > top) || ldw > top || ldy > top || (ep->residual && ep->ldr > top))
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: row stride above 2^22 elements", fn);
   if (M == 0 || N == 0) return ok();
   const size_t ysz = y_dtype == W4A4_DT_BF16 ? 2 : 4;
