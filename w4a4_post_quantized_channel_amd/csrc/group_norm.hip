@@ -1,7 +1,25 @@
 // Group normalisation with an activation on channels-last features.
 //
-// One workgroup per (sample, group): the mean, then the mean square
-// difference to it, then the output, three passes over the group.
+// Memory bound: the features are read once for the statistics and once for
+// the output; the second read comes from the 256 MB last-level cache where
+// the features fit it.
+//
+// Statistics.  A thread keeps V adjacent channels and walks down the
+// positions of its slab, so loads are whole lines and a lane's groups are
+// fixed.  It sums d and d^2 of differences d = x - x0 to the channel's first
+// value in the slab (exact to an ulp, so a large mean costs no accuracy).
+// Sums become (count, mean, M2) and are joined by
+//   mean = mean_a + (mean_b - mean_a) n_b / n,
+//   M2 = M2_a + M2_b + (mean_b - mean_a)^2 n_a n_b / n,
+// over the threads of a channel, over the channels of a group, and over the
+// slabs of a sample, always in the same order: no atomics, the same bits
+// every time.
+//
+// With a workspace the positions of a sample are cut into slabs that fill the
+// card; one kernel takes the moments of each (slab, group), one writes the
+// output.  The output kernel joins the slabs itself when they are few;
+// otherwise a third kernel does.  Without a workspace, or when a sample is
+// small, one workgroup does a run of groups of a sample by itself.
 #include "activation.h"
 #include "dense.h"
 #include "device_common.h"
@@ -10,52 +28,330 @@ namespace w4a4 {
 
 namespace {
 
-__device__ __forceinline__ float norm_load(const void* p, int64_t i, int bf16) {
-  return bf16 ? bf16_bits_to_f32(((const uint16_t*)p)[i]) : ((const float*)p)[i];
+constexpr int kThreads = 256;
+constexpr int kMaxSlabs = 2048;
+constexpr int kJoinInline = 96;    // slabs the output kernel joins by itself
+constexpr int64_t kSlabElems = 8192;
+
+struct Moments {
+  float n, mean, m2;
+};
+
+__device__ __forceinline__ Moments join(const Moments& a, const Moments& b) {
+  const float n = a.n + b.n;
+  const float w = n > 0.f ? b.n * __builtin_amdgcn_rcpf(n) : 0.f;
+  const float d = b.mean - a.mean;
+  return {n, a.mean + d * w, a.m2 + b.m2 + d * d * (a.n * w)};
 }
 
-__device__ float block_sum(float v, float* red) {
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) s += red[w];
-  return s;
+// Joins over the L = 2^k <= 64 adjacent lanes that share a result.
+__device__ __forceinline__ Moments join_lanes(Moments m, int L) {
+  for (int o = 1; o < L; o <<= 1) {
+    const Moments x = {__shfl_xor(m.n, o), __shfl_xor(m.mean, o), __shfl_xor(m.m2, o)};
+    m = (threadIdx.x & o) ? join(x, m) : join(m, x);
+  }
+  return m;
 }
 
-__global__ void __launch_bounds__(256) group_norm_kernel(NormArgs g) {
-  __shared__ float red[4];
+// Lanes for each of `items` results of a workgroup.
+__device__ __forceinline__ int lanes_per(int items) {
+  int L = 1;
+  while (L < 64 && items * L * 2 <= kThreads) L *= 2;
+  return L;
+}
+
+__device__ __forceinline__ float2 mean_rstd(const Moments& m, float eps) {
+  return make_float2(m.mean, 1.f / sqrtf(m.m2 / m.n + eps));
+}
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T v[V];
+};
+
+__device__ __forceinline__ float to_f32(uint16_t b) { return bf16_bits_to_f32(b); }
+__device__ __forceinline__ float to_f32(float f) { return f; }
+__device__ __forceinline__ void from_f32(uint16_t& o, float f) { o = __builtin_bit_cast(uint16_t, (__bf16)f); }
+__device__ __forceinline__ void from_f32(float& o, float f) { o = f; }
+
+// SiLU on the way to bf16 takes the hardware exp2 (a few parts in 10^6,
+// against 2^-9 of the output); fp32 output takes expf.
+__device__ __forceinline__ float activate_for(uint16_t, float z, int act) {
+  if (act == W4A4_ACT_SILU) return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+  return activate(z, act);
+}
+__device__ __forceinline__ float activate_for(float, float z, int act) { return activate(z, act); }
+
+// How a sample is cut.  A workgroup covers `gpb` whole groups, `cols` threads
+// across their channels and kThreads / cols positions deep.
+struct Split {
+  int gpb, cols, blocks;
+  int slabs;
+  int64_t len;     // positions of a slab
+};
+
+// Moments of the channels [c, c + V) of each thread over positions [s0, s1),
+// joined over the threads of a channel into mom[0 .. cols * V).
+template <typename T, int V>
+__device__ __forceinline__ void channel_moments(const NormArgs& g, const T* x, int64_t s0, int64_t s1, int c, int cend,
+                                                int cols, Moments* mom) {
+  const int rows = kThreads / cols, col = threadIdx.x % cols, depth = threadIdx.x / cols;
+  float sh[V], s[V], q[V];
+  float n = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) sh[e] = s[e] = q[e] = 0.f;
+  if (c < cend && depth < rows && s0 + depth < s1) {
+    const T* p = x + (s0 + depth) * g.x_ss + c;
+    const int64_t step = (int64_t)rows * g.x_ss;
+    const Vec<T, V> f = *reinterpret_cast<const Vec<T, V>*>(p);
+#pragma unroll
+    for (int e = 0; e < V; ++e) sh[e] = to_f32(f.v[e]);
+    int64_t left = (s1 - s0 - depth + rows - 1) / rows;
+    n = (float)left;
+    auto add = [&](const Vec<T, V>& u) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = to_f32(u.v[e]) - sh[e];
+        s[e] += d;
+        q[e] = __builtin_fmaf(d, d, q[e]);
+      }
+    };
+    for (; left >= 4; left -= 4, p += 4 * step) {   // four loads in flight
+      Vec<T, V> u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = *reinterpret_cast<const Vec<T, V>*>(p + k * step);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) add(u[k]);
+    }
+    for (; left > 0; --left, p += step) add(*reinterpret_cast<const Vec<T, V>*>(p));
+  }
+  const int width = cols * V;
+  const float inv = n > 0.f ? 1.f / n : 0.f;
+  if (depth < rows) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float ms = s[e] * inv;
+      mom[depth * width + col * V + e] = {n, sh[e] + ms, fmaxf(q[e] - s[e] * ms, 0.f)};
+    }
+  }
+  __syncthreads();
+  const int L = lanes_per(width);
+  for (int ch = threadIdx.x / L; ch < width; ch += kThreads / L) {
+    Moments m = {0.f, 0.f, 0.f};
+    for (int r = threadIdx.x % L; r < rows; r += L) m = join(m, mom[r * width + ch]);
+    m = join_lanes(m, L);
+    if (threadIdx.x % L == 0) mom[ch] = m;   // the column's other rows have been read by this wave
+  }
+  __syncthreads();
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void apply(const NormArgs& g, const T* x, T* y, int64_t s0, int64_t s1, int c, int cols,
+                                      const float (&mu)[V], const float (&rs)[V]) {
+  const int rows = kThreads / cols, depth = threadIdx.x / cols;
+  if (depth >= rows || s0 + depth >= s1) return;
+  float k[V], b[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    k[e] = rs[e] * (g.weight ? g.weight[c + e] : 1.f);
+    b[e] = g.bias ? g.bias[c + e] : 0.f;
+  }
+  const int64_t xs = (int64_t)rows * g.x_ss, ys = (int64_t)rows * g.y_ss;
+  const T* p = x + (s0 + depth) * g.x_ss + c;
+  T* o = y + (s0 + depth) * g.y_ss + c;
+  int64_t left = (s1 - s0 - depth + rows - 1) / rows;
+  auto one = [&](const Vec<T, V>& u, T* to) {
+    Vec<T, V> r;
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      from_f32(r.v[e], activate_for(T(), __builtin_fmaf(to_f32(u.v[e]) - mu[e], k[e], b[e]), g.act));
+    *reinterpret_cast<Vec<T, V>*>(to) = r;
+  };
+  for (; left >= 4; left -= 4, p += 4 * xs, o += 4 * ys) {   // in place: all four are read before any is written
+    Vec<T, V> u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const Vec<T, V>*>(p + i * xs);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) one(u[i], o + i * ys);
+  }
+  for (; left > 0; --left, p += xs, o += ys) one(*reinterpret_cast<const Vec<T, V>*>(p), o);
+}
+
+// Moments of (sample, slab, group).
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) norm_moments_kernel(NormArgs g, Split sp, Moments* ws) {
+  __shared__ Moments mom[kThreads * V];
+  const int cg = g.C / g.groups;
+  const int g0 = blockIdx.y * sp.gpb, ng = min(sp.gpb, g.groups - g0);
+  const int64_t n = blockIdx.z;
+  const int64_t s0 = blockIdx.x * sp.len, s1 = min(g.S, s0 + sp.len);
+  channel_moments<T, V>(g, (const T*)g.x + n * g.x_sn, s0, s1, g0 * cg + (threadIdx.x % sp.cols) * V, (g0 + ng) * cg,
+                        sp.cols, mom);
+  const int L = lanes_per(ng);
+  for (int i = threadIdx.x / L; i < ng; i += kThreads / L) {
+    Moments m = {0.f, 0.f, 0.f};
+    for (int c = threadIdx.x % L; c < cg; c += L) m = join(m, mom[i * cg + c]);
+    m = join_lanes(m, L);
+    if (threadIdx.x % L == 0) ws[(n * sp.slabs + blockIdx.x) * g.groups + g0 + i] = m;
+  }
+}
+
+// (mean, 1 / deviation) of a (sample, group) from its slabs.
+__global__ void __launch_bounds__(64) norm_join_kernel(NormArgs g, int slabs, const Moments* ws, float2* stat) {
   const int64_t n = blockIdx.x / g.groups;
-  const int cg = g.C / g.groups, c0 = (int)(blockIdx.x % g.groups) * cg;
-  const int64_t cnt = g.S * cg;
-  auto at = [&](int64_t i) { return n * g.x_sn + i / cg * g.x_ss + c0 + i % cg; };
-  float s = 0.f;
-  for (int64_t i = threadIdx.x; i < cnt; i += 256) s += norm_load(g.x, at(i), g.bf16);
-  const float mean = block_sum(s, red) / (float)cnt;
-  s = 0.f;
-  for (int64_t i = threadIdx.x; i < cnt; i += 256) {
-    const float d = norm_load(g.x, at(i), g.bf16) - mean;
-    s += d * d;
+  const int grp = blockIdx.x % g.groups;
+  Moments m = {0.f, 0.f, 0.f};
+  for (int i = threadIdx.x; i < slabs; i += 64) m = join(m, ws[(n * slabs + i) * g.groups + grp]);
+  m = join_lanes(m, 64);
+  if (threadIdx.x == 0) stat[blockIdx.x] = mean_rstd(m, g.eps);
+}
+
+// The output of a slab; stat null: the slabs' moments are joined here.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) norm_apply_kernel(NormArgs g, Split sp, const Moments* ws, const float2* stat) {
+  __shared__ float2 st[kThreads * V];
+  const int cg = g.C / g.groups;
+  const int g0 = blockIdx.y * sp.gpb, ng = min(sp.gpb, g.groups - g0);
+  const int64_t n = blockIdx.z;
+  if (stat) {
+    for (int i = threadIdx.x; i < ng; i += kThreads) st[i] = stat[n * g.groups + g0 + i];
+  } else {
+    const int L = lanes_per(ng);
+    for (int i = threadIdx.x / L; i < ng; i += kThreads / L) {
+      Moments m = {0.f, 0.f, 0.f};
+      for (int k = threadIdx.x % L; k < sp.slabs; k += L) m = join(m, ws[(n * sp.slabs + k) * g.groups + g0 + i]);
+      m = join_lanes(m, L);
+      if (threadIdx.x % L == 0) st[i] = mean_rstd(m, g.eps);
+    }
   }
-  const float rstd = 1.f / sqrtf(block_sum(s, red) / (float)cnt + g.eps);
-  for (int64_t i = threadIdx.x; i < cnt; i += 256) {
-    const int c = c0 + (int)(i % cg);
-    float v = (norm_load(g.x, at(i), g.bf16) - mean) * rstd;
-    v = activate(v * (g.weight ? g.weight[c] : 1.f) + (g.bias ? g.bias[c] : 0.f), g.act);
-    const int64_t o = n * g.y_sn + i / cg * g.y_ss + c;
-    if (g.bf16) ((uint16_t*)g.y)[o] = (uint16_t)f32_to_bf16_bits(v);
-    else ((float*)g.y)[o] = v;
+  __syncthreads();
+  const int cl = (threadIdx.x % sp.cols) * V;   // channel within the block
+  if (cl >= ng * cg) return;
+  float mu[V], rs[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float2 v = st[(cl + e) / cg];
+    mu[e] = v.x;
+    rs[e] = v.y;
   }
+  // slabs last to first: what the moments kernel read last is still cached
+  const int64_t s0 = (sp.slabs - 1 - (int)blockIdx.x) * sp.len, s1 = min(g.S, s0 + sp.len);
+  apply<T, V>(g, (const T*)g.x + n * g.x_sn, (T*)g.y + n * g.y_sn, s0, s1, g0 * cg + cl, sp.cols, mu, rs);
+}
+
+// A run of whole groups of one sample, statistics and output.  A group wider
+// than the workgroup (run == 1 then) is taken in chunks of its channels.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) norm_whole_kernel(NormArgs g, int gpb, int cols) {
+  __shared__ Moments mom[kThreads * V];
+  __shared__ float2 st[kThreads * V];
+  const int cg = g.C / g.groups;
+  const int64_t n = blockIdx.y;
+  const int g0 = blockIdx.x * gpb, ng = min(gpb, g.groups - g0);
+  const int c0 = g0 * cg, cend = c0 + ng * cg, width = cols * V;
+  const T* x = (const T*)g.x + n * g.x_sn;
+  T* y = (T*)g.y + n * g.y_sn;
+  const int L = lanes_per(ng);
+  Moments tot = {0.f, 0.f, 0.f};
+  for (int cc = c0; cc < cend; cc += width) {
+    channel_moments<T, V>(g, x, 0, g.S, cc + (threadIdx.x % cols) * V, cend, cols, mom);
+    for (int i = threadIdx.x / L; i < ng; i += kThreads / L) {
+      Moments m = ng == 1 ? tot : Moments{0.f, 0.f, 0.f};
+      const int cnt = ng == 1 ? min(width, cend - cc) : cg;
+      for (int c = threadIdx.x % L; c < cnt; c += L) m = join(m, mom[i * cg + c]);
+      tot = m;
+      if (cc + width >= cend) {
+        m = join_lanes(m, L);
+        if (threadIdx.x % L == 0) st[i] = mean_rstd(m, g.eps);
+      }
+    }
+    __syncthreads();
+  }
+  for (int cc = c0; cc < cend; cc += width) {
+    const int c = cc + (threadIdx.x % cols) * V;
+    if (c >= cend) break;
+    float mu[V], rs[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float2 v = st[(c + e - c0) / cg];
+      mu[e] = v.x;
+      rs[e] = v.y;
+    }
+    apply<T, V>(g, x, y, 0, g.S, c, cols, mu, rs);
+  }
+}
+
+// Slabs of a sample: about eight workgroups a CU over all samples, at least
+// kSlabElems elements each.
+int slabs_for(int64_t N, int64_t S, int64_t C, int64_t groups) {
+  // a group wider than any workgroup's channels is not cut
+  if (C / groups > kThreads) return 1;
+  const int64_t elems = S * C;
+  int64_t want = kMaxSlabs / N;
+  if (want > elems / kSlabElems) want = elems / kSlabElems;
+  if (want > S) want = S;
+  return want < 2 ? 1 : (int)want;
+}
+
+size_t stat_bytes(int64_t N, int64_t groups) { return (size_t)(N * groups * 8 + 255) / 256 * 256; }
+
+template <typename T, int V>
+hipError_t run(const NormArgs& g, void* workspace, hipStream_t st) {
+  const int cg = g.C / g.groups;
+  const int slabs = slabs_for(g.N, g.S, g.C, g.groups);
+  // whole groups a workgroup can cover; vectors may straddle groups only
+  // where the workgroup covers all of them
+  int gpb = cg >= kThreads * V ? 1 : kThreads * V / cg;
+  if (gpb > g.groups) gpb = g.groups;
+  if (!workspace || slabs == 1) {
+    // small: few channels a workgroup, so that more of them share the sample
+    if (cg % V == 0)
+      while (gpb > 1 && gpb * cg > 16 * V) gpb = (gpb + 1) / 2;
+    const int w = (gpb * cg + V - 1) / V, cols = w < kThreads ? w : kThreads;
+    norm_whole_kernel<T, V><<<dim3((g.groups + gpb - 1) / gpb, (unsigned)g.N), kThreads, 0, st>>>(g, gpb, cols);
+    return hipGetLastError();
+  }
+  Split sp;
+  sp.gpb = gpb;
+  sp.cols = (gpb * cg + V - 1) / V;
+  sp.blocks = (g.groups + gpb - 1) / gpb;
+  sp.len = (g.S + slabs - 1) / slabs;
+  sp.slabs = (int)((g.S + sp.len - 1) / sp.len);
+  float2* stat = (float2*)workspace;
+  Moments* mom = (Moments*)((char*)workspace + stat_bytes(g.N, g.groups));
+  const dim3 grid(sp.slabs, sp.blocks, (unsigned)g.N);
+  norm_moments_kernel<T, V><<<grid, kThreads, 0, st>>>(g, sp, mom);
+  const bool inline_join = sp.slabs <= kJoinInline;
+  if (!inline_join) norm_join_kernel<<<(unsigned)(g.N * g.groups), 64, 0, st>>>(g, sp.slabs, mom, stat);
+  norm_apply_kernel<T, V><<<grid, kThreads, 0, st>>>(g, sp, mom, inline_join ? nullptr : stat);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t group_norm_workspace(int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t group_norm_workspace(int64_t N, int64_t S, int64_t C, int64_t groups) {
+  const int slabs = slabs_for(N, S, C, groups);
+  return slabs == 1 ? 0 : stat_bytes(N, groups) + (size_t)N * slabs * groups * sizeof(Moments);
+}
 
-hipError_t launch_group_norm(const NormArgs& g, void*, hipStream_t st) {
-  group_norm_kernel<<<dim3((unsigned)(g.N * g.groups)), 256, 0, st>>>(g);
-  return hipGetLastError();
+hipError_t launch_group_norm(const NormArgs& g, void* workspace, hipStream_t st) {
+  // Widest vector that the channel count, the strides and the pointers allow.
+  const int esz = g.bf16 ? 2 : 4;
+  auto fits = [&](int V) {
+    const int64_t b = V * esz;
+    if (g.C % V || g.x_ss % V || g.y_ss % V || (g.N > 1 && (g.x_sn % V || g.y_sn % V))) return false;
+    if ((uintptr_t)g.x % b || (uintptr_t)g.y % b) return false;
+    return (g.C / g.groups) % V == 0 || g.C <= kThreads * V;   // straddling vectors: all groups in one workgroup
+  };
+  if (g.bf16) {
+    if (fits(8)) return run<uint16_t, 8>(g, workspace, st);
+    if (fits(4)) return run<uint16_t, 4>(g, workspace, st);
+    if (fits(2)) return run<uint16_t, 2>(g, workspace, st);
+    return run<uint16_t, 1>(g, workspace, st);
+  }
+  if (fits(4)) return run<float, 4>(g, workspace, st);
+  if (fits(2)) return run<float, 2>(g, workspace, st);
+  return run<float, 1>(g, workspace, st);
 }
 
 }  // namespace w4a4
