@@ -100,7 +100,7 @@ size_t w4a4_prefix_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t
 static int check_dense_sizes(const char* fn, int64_t M, int64_t N, int64_t K, int32_t act) {
   if (M < 0 || N < 0 || K <= 0) return fail(W4A4_ERR_INVALID_ARG, "%s: bad sizes", fn);
   if (K % 8 != 0) return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: K=%lld not a multiple of 8", fn, (long long)K);
-  if (K > (1LL << 24) || M > (1LL << 30) || N > (1LL << 30))
+  if (K > (1LL << 21) || M > (1LL << 30) || N > (1LL << 30))
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: sizes too large", fn);
   if (act < W4A4_ACT_NONE || act > W4A4_ACT_SWIGLU)
     return fail(W4A4_ERR_UNSUPPORTED_FORMAT, "%s: unknown activation %d", fn, act);
@@ -123,8 +123,8 @@ int bf16_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t 
     return fail(W4A4_ERR_INVALID_ARG, "%s: row stride below the row length", fn);
   if (ldx % 8 != 0 || ldw % 8 != 0) return fail(W4A4_ERR_MISALIGNED, "%s: ldx / ldw not a multiple of 8", fn);
   const int64_t top = 1LL << 22;
-  if ((M > 1 && ldx > top) || ldw > top || ldy > top || (ep->residual && ep->ldr > top))
-    return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: row stride above 2^22 elements", fn);
+  if (ldx > top / 2 || ldw > top / 2 || ldy > top || (ep->residual && ep->ldr > top))
+    return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: row stride too large", fn);
   if (M == 0 || N == 0) return ok();
   const size_t ysz = y_dtype == W4A4_DT_BF16 ? 2 : 4;
   if ((st = check_pointer(fn, "x", x, 16)) != W4A4_OK) return st;

@@ -1,55 +1,412 @@
-// bf16 product with bias, activation and residual: y = act(x W^T + bias) + residual.
+// bf16 product with bias, activation and residual:
+//   y = act(x W^T + bias) + residual.
 //
-// One wave per 16 x 16 output tile, operands straight from global memory
-// into v_mfma_f32_16x16x32_bf16; for SwiGLU the wave holds the gate's and the
-// up projection's tile of the same columns.
+// Tiles of BM x BN outputs, K in stages of 64 (a 128-byte line per row).
+// Stages are copied global -> LDS with 16-byte copies (XOR-swizzled 16-byte
+// slots, see swz128) into NBUF buffers, NBUF - 1 stages ahead, and multiplied
+// with v_mfma_f32_16x16x32_bf16.  W is the first operand and x the second,
+// so that a lane's four accumulators are four adjacent columns of one output
+// row.  The epilogue passes 16 rows at a time through LDS as fp32, so that
+// bias, activation and residual work on whole row segments and every store
+// is 16 bytes of a row.
+//
+// SwiGLU: 16-row fragments of a W tile alternate between the gate's rows and
+// the up projection's, so one wave holds both factors of its outputs.
+//
+// Few output tiles: K is split over workgroups; fp32 partial sums go to the
+// workspace and a second kernel adds them in order and runs the epilogue.
 #include "activation.h"
 #include "dense.h"
 #include "device_common.h"
-#include "epilogue.h"
+#include "lds_dma.h"
 
 namespace w4a4 {
 
 namespace {
 
-__device__ __forceinline__ float bias_at(const DenseArgs& g, int n) {
-  if (!g.bias) return 0.f;
-  return g.bias_bf16 ? bf16_bits_to_f32(((const uint16_t*)g.bias)[n]) : ((const float*)g.bias)[n];
+// Slot swizzle of a 128-byte LDS row: the 16 rows of a fragment read land on
+// distinct banks in each of the read's four cycles.
+__device__ __forceinline__ int swz128(int row) {
+  return ((row >> 1) & 1) ^ (row & 4) ^ (((row >> 3) & 1) * 6);
 }
 
-__global__ void __launch_bounds__(64) gemm_bf16_tile_kernel(DenseArgs g) {
-  const int lane = threadIdx.x, lr = lane & 15, lk = (lane >> 4) * 8;
-  const int m0 = blockIdx.y * 16, n0 = blockIdx.x * 16;
-  const bool gated = g.act == W4A4_ACT_SWIGLU;
-  v4f acc = {0, 0, 0, 0}, up = {0, 0, 0, 0};
-  for (int k = 0; k < g.K; k += 32) {
-    const v8bf a = load_bf16x8(g.x, g.ldx, m0 + lr, g.M, k + lk, g.K);
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, load_bf16x8(g.w, g.ldw, n0 + lr, g.N, k + lk, g.K), acc, 0, 0, 0);
-    if (gated)
-      up = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-          a, load_bf16x8(g.w + g.N * g.ldw, g.ldw, n0 + lr, g.N, k + lk, g.K), up, 0, 0, 0);
+// Eight adjacent outputs of row m from column n: z (and for SwiGLU the up
+// projection's u) plus bias, activation, residual, one rounding, store.
+// vec: 16-byte accesses to y and the residual are aligned.
+template <int KIND, bool GATED>
+__device__ __forceinline__ void finish8(const DenseArgs& g, float (&z)[8], const float (&u)[8], int m, int n, bool vec) {
+  if (m >= g.M || n >= g.N) return;
+  const bool whole = n + 8 <= g.N;
+  const int cnt = min(8, g.N - n);
+  float res[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) res[e] = 0.f;
+  const int64_t ro = m * g.ldr + n, yo = m * g.ldy + n;
+  if (g.residual) {
+    if (g.y_bf16) {
+      const uint16_t* r = (const uint16_t*)g.residual + ro;
+      if (whole && vec) {
+        const uint4 v = *reinterpret_cast<const uint4*>(r);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) res[e] = e & 1 ? __uint_as_float(w[e >> 1] & 0xFFFF0000u) : __uint_as_float(w[e >> 1] << 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < cnt) res[e] = bf16_bits_to_f32(r[e]);
+      }
+    } else {
+      const float* r = (const float*)g.residual + ro;
+      if (whole && vec) {
+        const v4f a = *reinterpret_cast<const v4f*>(r), b = *reinterpret_cast<const v4f*>(r + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) res[e] = a[e], res[e + 4] = b[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < cnt) res[e] = r[e];
+      }
+    }
   }
-  const int n = n0 + lr;
-  if (n >= g.N) return;
-  for (int r = 0; r < 4; ++r) {
-    const int m = m0 + (lane >> 4) * 4 + r;
-    if (m >= g.M) return;
-    float z = acc[r] + bias_at(g, n);
-    z = gated ? times_sigmoid(z, z) * (up[r] + bias_at(g, g.N + n)) : activate(z, g.act);
-    if (g.residual)
-      z += g.y_bf16 ? bf16_bits_to_f32(((const uint16_t*)g.residual)[m * g.ldr + n])
-                    : ((const float*)g.residual)[m * g.ldr + n];
-    if (g.y_bf16) ((uint16_t*)g.y)[m * g.ldy + n] = (uint16_t)f32_to_bf16_bits(z);
-    else ((float*)g.y)[m * g.ldy + n] = z;
+  auto bias = [&](int i) {
+    return g.bias_bf16 ? bf16_bits_to_f32(((const uint16_t*)g.bias)[i]) : ((const float*)g.bias)[i];
+  };
+  float b[8], bu[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    b[e] = g.bias && e < cnt ? bias(n + e) : 0.f;
+    bu[e] = GATED && g.bias && e < cnt ? bias(g.N + n + e) : 0.f;
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float v = z[e] + b[e];
+    if constexpr (GATED) v = times_sigmoid(v, v) * (u[e] + bu[e]);
+    else v = activate_kind<KIND>(v, g.act);
+    z[e] = v + res[e];
+  }
+  if (g.y_bf16) {
+    uint16_t* y = (uint16_t*)g.y + yo;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      typedef float v2f __attribute__((ext_vector_type(2)));
+      w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){z[2 * e], z[2 * e + 1]}, v2bf));
+    }
+    if (whole && vec) {
+      *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < cnt) y[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+  } else {
+    float* y = (float*)g.y + yo;
+    if (whole && vec) {
+      *reinterpret_cast<v4f*>(y) = (v4f){z[0], z[1], z[2], z[3]};
+      *reinterpret_cast<v4f*>(y + 4) = (v4f){z[4], z[5], z[6], z[7]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < cnt) y[e] = z[e];
+    }
+  }
+}
+
+__host__ __device__ inline bool vec_ok(const DenseArgs& g) {
+  const uintptr_t esz = g.y_bf16 ? 2 : 4;
+  uintptr_t bits = (uintptr_t)g.y | (uintptr_t)g.ldy * esz;
+  if (g.residual) bits |= (uintptr_t)g.residual | (uintptr_t)g.ldr * esz;
+  return bits % 16 == 0;
+}
+
+struct GemmPlanArgs {
+  DenseArgs g;
+  int tiles_m, tiles_n, splits;
+  int stages;        // K stages in all
+  float* part;       // splits > 1: [split][m][W row], row length pn
+  int pn;
+};
+
+template <int TI_, int TJ_, int WR_, int WC_, int NBUF_>
+struct GCfg {
+  static constexpr int TI = TI_, TJ = TJ_, WR = WR_, WC = WC_, NBUF = NBUF_;
+  static constexpr int NW = WR * WC;
+  static constexpr int BM = WR * TI * 16, BN = WC * TJ * 16;   // BN: rows of W
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
+  static constexpr int NA = BM / 8, NB = BN / 8;               // copy instructions of a stage
+  static constexpr int PA = (NA + NW - 1) / NW, PB = (NB + NW - 1) / NW, DPS = PA + PB;
+  static constexpr int PITCH = TJ * 16 + 4;                    // floats of an epilogue row
+  static constexpr int PIPE = NBUF * STAGE + 1024;             // + the target of padding copies
+  static constexpr int EPI = NW * 16 * PITCH * 4;
+  static constexpr int LDS = PIPE > EPI ? PIPE : EPI;
+  static_assert(LDS <= 160 * 1024 && DPS * (NBUF - 2) <= 63, "limits");
+};
+
+template <typename C, int KIND, bool GATED>
+__global__ void __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu((C::NW + 3) / 4, 8)))
+gemm_bf16_kernel(GemmPlanArgs p) {
+  constexpr int TI = C::TI, TJ = C::TJ, NW = C::NW;
+  static_assert(!GATED || TJ % 2 == 0, "gate and up fragments in pairs");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
+  const DenseArgs& g = p.g;
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WC * TI * 16, wn = wave % C::WC * TJ * 16;
+
+  // Workgroup -> tile: contiguous runs per XCD, groups of four row tiles
+  // walked column by column, K splits outermost.
+  const int nwg = gridDim.x, wid = blockIdx.x;
+  int t = nwg % 8 == 0 ? (wid % 8) * (nwg / 8) + wid / 8 : wid;
+  const int per = p.tiles_m * p.tiles_n, split = t / per;
+  t %= per;
+  constexpr int GM = 4;
+  const int grp = t / (GM * p.tiles_n), gm0 = grp * GM, gh = min(GM, p.tiles_m - gm0);
+  const int tm = gm0 + t % (GM * p.tiles_n) % gh, tn = t % (GM * p.tiles_n) / gh;
+  const int m0 = tm * C::BM, n0 = tn * (GATED ? C::BN / 2 : C::BN);
+  const int s0 = (int)((int64_t)p.stages * split / p.splits), s1 = (int)((int64_t)p.stages * (split + 1) / p.splits);
+
+  // Copies: instruction n of an operand covers 8 rows; lane l chunk slot
+  // l % 8 of row l / 8.  Rows past the end and columns past K take an
+  // out-of-range offset and arrive as zeros.
+  const uint32_t lds0 = lds_addr(smem);
+  const v4u rsA = rsrc_words(g.x + (int64_t)m0 * g.ldx, 0x7FFFFFFFu);
+  const v4u rsB = rsrc_words(g.w + (int64_t)n0 * g.ldw, 0x7FFFFFFFu);
+  const v4u rsU = GATED ? rsrc_words(g.w + ((int64_t)g.N + n0) * g.ldw, 0x7FFFFFFFu) : rsB;
+  const int crow = lane >> 3, cslot = lane & 7;
+  uint32_t offA[C::PA], offB[C::PB];
+  int colA[C::PA], colB[C::PB];
+#pragma unroll
+  for (int k = 0; k < C::PA; ++k) {
+    const int n = k * NW + wave, row = n * 8 + crow;
+    colA[k] = (cslot ^ swz128(row)) * 16;
+    offA[k] = n < C::NA && m0 + row < g.M ? (uint32_t)(row * g.ldx * 2) + colA[k] : kOOB;
+  }
+#pragma unroll
+  for (int k = 0; k < C::PB; ++k) {
+    const int n = k * NW + wave, row = n * 8 + crow;
+    const int nl = GATED ? (row >> 5) * 16 + (row & 15) : row;   // output column within the tile
+    colB[k] = (cslot ^ swz128(row)) * 16;
+    offB[k] = n < C::NB && n0 + nl < g.N ? (uint32_t)(nl * g.ldw * 2) + colB[k] : kOOB;
+  }
+  const int kbytes = g.K * 2;
+  auto copy_stage = [&](int s) {
+    const uint32_t base = lds0 + (uint32_t)((s - s0) % C::NBUF) * C::STAGE;
+    const uint32_t pad = lds0 + C::NBUF * C::STAGE;
+    const int left = s < s1 ? kbytes - s * 128 : 0;   // bytes of this stage's rows
+    const uint32_t k0 = left > 0 ? s * 128u : 0;
+#pragma unroll
+    for (int k = 0; k < C::PA; ++k) {
+      const int n = k * NW + wave;
+      dma16_at(rsA, (C::NA % NW == 0 || n < C::NA) ? base + n * 1024 : pad, colA[k] < left ? offA[k] : kOOB, k0);
+    }
+#pragma unroll
+    for (int k = 0; k < C::PB; ++k) {
+      const int n = k * NW + wave;
+      dma16_at(GATED && (n & 2) ? rsU : rsB, (C::NB % NW == 0 || n < C::NB) ? base + C::A_BYTES + n * 1024 : pad,
+               colB[k] < left ? offB[k] : kOOB, k0);
+    }
+  };
+
+  v4f acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+
+  int aoff[2], boff[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    aoff[k] = (wm + lr) * 128 + (((4 * k + lq) ^ swz128(lr)) << 4);
+    boff[k] = C::A_BYTES + (wn + lr) * 128 + (((4 * k + lq) ^ swz128(lr)) << 4);
+  }
+
+#pragma unroll
+  for (int b = 0; b < C::NBUF - 1; ++b) copy_stage(s0 + b);
+  for (int s = s0; s < s1; ++s) {
+    wait_vmcnt<C::DPS * (C::NBUF - 2)>();   // stage s has landed, later ones may be in flight
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();           // for every wave; and stage s - 1 is no longer read
+    asm volatile("" ::: "memory");
+    copy_stage(s + C::NBUF - 1);
+    const uint8_t* base = smem + (s - s0) % C::NBUF * C::STAGE;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      v8bf a[TI], b[TJ];
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) b[j] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(base + boff[k] + j * 2048));
+#pragma unroll
+      for (int i = 0; i < TI; ++i) a[i] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(base + aoff[k] + i * 2048));
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+    }
+  }
+  wait_vmcnt<0>();
+  __syncthreads();   // no copy in flight, no stage being read: LDS is free for the epilogue
+
+  if (p.splits > 1) {
+    // partial sums: a lane's four values are adjacent W rows
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int m = m0 + wm + i * 16 + lr;
+      float* row = p.part + ((int64_t)split * g.M + m) * p.pn + tn * C::BN + wn + lq * 4;
+      if (m < g.M)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) *reinterpret_cast<v4f*>(row + j * 16) = acc[i][j];
+    }
+    return;
+  }
+  const bool vec = vec_ok(g);
+  float* buf = reinterpret_cast<float*>(smem) + wave * 16 * C::PITCH;
+  constexpr int OC = (GATED ? TJ / 2 : TJ) * 2;   // 8-column chunks of an output row of this wave
+  const int nb = n0 + (GATED ? wn / 2 : wn);
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) *reinterpret_cast<v4f*>(buf + lr * C::PITCH + j * 16 + lq * 4) = acc[i][j];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int c0 = 0; c0 < 16 * OC; c0 += 64) {
+      const int c = c0 + lane;
+      if (16 * OC % 64 != 0 && c >= 16 * OC) continue;
+      const int row = c / OC, ch = c % OC;
+      const float* src = buf + row * C::PITCH + (GATED ? (ch >> 1) * 32 + (ch & 1) * 8 : ch * 8);
+      float z[8], u[8];
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const v4f v = *reinterpret_cast<const v4f*>(src + e);
+        const v4f w = GATED ? *reinterpret_cast<const v4f*>(src + 16 + e) : v4f{0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z[e + q] = v[q], u[e + q] = w[q];
+      }
+      finish8<KIND, GATED>(g, z, u, m0 + wm + i * 16 + row, nb + ch * 8, vec);
+      __builtin_amdgcn_sched_barrier(0);   // one chunk's registers at a time
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Adds the K splits in order and runs the epilogue: 8 columns a thread.
+template <int KIND, bool GATED>
+__global__ void __launch_bounds__(256) gemm_bf16_join_kernel(GemmPlanArgs p) {
+  const DenseArgs& g = p.g;
+  const int chunks = (g.N + 7) / 8;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= (int64_t)g.M * chunks) return;
+  const int m = (int)(id / chunks), n = (int)(id % chunks) * 8;
+  // column n of the partial rows: SwiGLU rows hold 16 gate then 16 up values
+  const int col = GATED ? (n >> 4) * 32 + (n & 15) : n;
+  const float* src = p.part + (int64_t)m * p.pn + col;
+  const int64_t step = (int64_t)g.M * p.pn;
+  v4f z0 = {0, 0, 0, 0}, z1 = z0, u0 = z0, u1 = z0;
+  for (int s = 0; s < p.splits; ++s, src += step) {
+    z0 += *reinterpret_cast<const v4f*>(src);
+    z1 += *reinterpret_cast<const v4f*>(src + 4);
+    if constexpr (GATED) {
+      u0 += *reinterpret_cast<const v4f*>(src + 16);
+      u1 += *reinterpret_cast<const v4f*>(src + 20);
+    }
+  }
+  float z[8], u[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) z[e] = z0[e], z[e + 4] = z1[e], u[e] = u0[e], u[e + 4] = u1[e];
+  finish8<KIND, GATED>(g, z, u, m, n, vec_ok(g));
+}
+
+// Tiles, largest first.
+using T256x320 = GCfg<8, 5, 2, 4, 2>;   // not for SwiGLU (odd fragment count)
+using T256x256 = GCfg<8, 4, 2, 4, 2>;
+using T128x256 = GCfg<4, 4, 2, 4, 3>;
+using T128x128 = GCfg<4, 2, 2, 4, 4>;
+using T64x128 = GCfg<2, 2, 2, 4, 5>;
+using T32x128 = GCfg<2, 2, 1, 4, 6>;
+using T16x128 = GCfg<1, 2, 1, 4, 6>;
+struct TileInfo {
+  int bm, bn, wgs;   // wgs: workgroups a CU holds
+  double us;         // measured time of a stage of one workgroup on a busy card
+  bool gated;
+};
+constexpr TileInfo kTiles[] = {{256, 320, 1, 1.9, false}, {256, 256, 1, 1.55, true}, {128, 256, 1, 0.85, true},
+                               {128, 128, 1, 0.55, true}, {64, 128, 1, 0.40, true},  {32, 128, 1, 0.30, true},
+                               {16, 128, 1, 0.28, true}};
+constexpr int kNumTiles = 7, kCUs = 256;
+
+struct GemmPlan {
+  int tile, tiles_m, tiles_n, splits, pn;
+};
+
+GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int act, bool split) {
+  const bool gated = act == W4A4_ACT_SWIGLU;
+  const int64_t stages = (K + 63) / 64;
+  GemmPlan best{};
+  double best_cost = 1e300;
+  for (int i = 0; i < kNumTiles; ++i) {
+    const TileInfo& ti = kTiles[i];
+    if (gated && !ti.gated) continue;
+    const int64_t bn = gated ? ti.bn / 2 : ti.bn;
+    const int64_t tm = (M + ti.bm - 1) / ti.bm, tn = (N + bn - 1) / bn, tiles = tm * tn;
+    for (int64_t sp = 1; sp <= 64; sp *= 2) {
+      if (sp > 1 && (!split || tiles * sp > 2 * kCUs || stages / sp < 2)) break;
+      const int64_t rounds = (tiles * sp + kCUs - 1) / kCUs;
+      double cost = rounds * ((stages + sp - 1) / sp * ti.us + 1.5 + ti.bm * ti.bn * 4e-5);
+      if (sp > 1) cost += 3.0 + 2.0 * sp * M * tn * ti.bn * 4.0 / 4e6;
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {i, (int)tm, (int)tn, (int)sp, (int)(tn * ti.bn)};
+      }
+    }
+  }
+  return best;
+}
+
+template <typename C, bool GATED>
+void launch_kind(const GemmPlanArgs& p, hipStream_t st) {
+  const unsigned grid = (unsigned)(p.tiles_m * p.tiles_n * p.splits);
+  const int kind = act_kind(p.g.act);
+  if (GATED || (kind == ACT_KIND_SIGMOID && p.splits == 1))
+    gemm_bf16_kernel<C, ACT_KIND_SIGMOID, GATED><<<grid, 64 * C::NW, 0, st>>>(p);
+  else if constexpr (!GATED) {
+    if (kind == ACT_KIND_ERF && p.splits == 1) gemm_bf16_kernel<C, ACT_KIND_ERF, false><<<grid, 64 * C::NW, 0, st>>>(p);
+    else gemm_bf16_kernel<C, ACT_KIND_PLAIN, false><<<grid, 64 * C::NW, 0, st>>>(p);   // a split stores plain sums
+  }
+}
+
+template <typename C>
+void launch_tile(const GemmPlanArgs& p, hipStream_t st) {
+  if (p.g.act != W4A4_ACT_SWIGLU) launch_kind<C, false>(p, st);
+  else if constexpr (C::TJ % 2 == 0) launch_kind<C, true>(p, st);
 }
 
 }  // namespace
 
-size_t gemm_bf16_workspace(int64_t, int64_t, int64_t, int) { return 0; }
+size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int act) {
+  const GemmPlan pl = plan_gemm(M, N, K, act, true);
+  return pl.splits > 1 ? (size_t)pl.splits * M * pl.pn * 4 : 0;
+}
 
-hipError_t launch_gemm_bf16(const DenseArgs& g, void*, hipStream_t st) {
-  gemm_bf16_tile_kernel<<<dim3((g.N + 15) / 16, (g.M + 15) / 16), 64, 0, st>>>(g);
+hipError_t launch_gemm_bf16(const DenseArgs& g, void* workspace, hipStream_t st) {
+
+  const GemmPlan pl = plan_gemm(g.M, g.N, g.K, g.act, workspace != nullptr);
+  GemmPlanArgs p{g, pl.tiles_m, pl.tiles_n, pl.splits, (g.K + 63) / 64, (float*)workspace, pl.pn};
+  switch (pl.tile) {
+    case 0: launch_tile<T256x320>(p, st); break;
+    case 1: launch_tile<T256x256>(p, st); break;
+    case 2: launch_tile<T128x256>(p, st); break;
+    case 3: launch_tile<T128x128>(p, st); break;
+    case 4: launch_tile<T64x128>(p, st); break;
+    case 5: launch_tile<T32x128>(p, st); break;
+    default: launch_tile<T16x128>(p, st); break;
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || pl.splits == 1) return e;
+  const int64_t items = (int64_t)g.M * ((g.N + 7) / 8);
+  const unsigned grid = (unsigned)((items + 255) / 256);
+  const int kind = act_kind(g.act);
+  if (g.act == W4A4_ACT_SWIGLU) gemm_bf16_join_kernel<ACT_KIND_SIGMOID, true><<<grid, 256, 0, st>>>(p);
+  else if (kind == ACT_KIND_SIGMOID) gemm_bf16_join_kernel<ACT_KIND_SIGMOID, false><<<grid, 256, 0, st>>>(p);
+  else if (kind == ACT_KIND_ERF) gemm_bf16_join_kernel<ACT_KIND_ERF, false><<<grid, 256, 0, st>>>(p);
+  else gemm_bf16_join_kernel<ACT_KIND_PLAIN, false><<<grid, 256, 0, st>>>(p);
   return hipGetLastError();
 }
 
