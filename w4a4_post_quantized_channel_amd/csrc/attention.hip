@@ -43,13 +43,33 @@ typedef const __attribute__((address_space(3))) v4i lds_v4i;
 constexpr float kLazy = 8.f;
 constexpr int kNoBad = 1 << 30;
 
+// Division by a number fixed for a launch: m = floor(2^32 / d) + 1 gives the
+// quotient or one more (2^32 - 1 for d = 1: or one less).
+struct Divisor {
+  uint32_t d, m;
+};
+inline Divisor divisor(int64_t d) {
+  return {(uint32_t)d, d == 1 ? 0xFFFFFFFFu : (uint32_t)((1ull << 32) / (uint64_t)d + 1)};
+}
+__device__ __forceinline__ int div_by(int x, const Divisor& v, int& rem) {
+  int q = (int)__umulhi((uint32_t)x, v.m), r = x - q * (int)v.d;
+  if (r < 0) --q, r += (int)v.d;
+  if (r >= (int)v.d) ++q, r -= (int)v.d;
+  rem = r;
+  return q;
+}
+
 struct AttnArgs {
   w4a4_attn a;
   int rows;         // B T G rows of a KV head
   int rpt;          // rows of a tile
-  int tg, g;        // T G, G
-  int tiles, parts;
-  int np, ns;       // prefix blocks; own blocks of a sequence
+  Divisor tg, g;    // T G, G
+  Divisor tiles, heads;
+  int parts;
+  int np;           // prefix blocks
+  Divisor ns;       // own blocks of a sequence (1 if none)
+  int own;          // 0: no own keys
+  int per;          // blocks of a part
   float c2;         // |scale| log2 e
   uint32_t qflip;   // sign bits flipped in q when scale < 0
   float* po;        // parts > 1: [part][head][row][D], else null
@@ -60,11 +80,13 @@ template <int D_, int WQ_, int WK_, int BN_, int NBUF_>
 struct ACfg {
   static constexpr int D = D_, WQ = WQ_, WK = WK_, BN = BN_, NBUF = NBUF_;
   static constexpr int NW = WQ * WK;
+  static constexpr bool PINGPONG = WQ == 8 && NBUF == 4;
   static constexpr int RB = 2 * D;                  // bytes of a key or value row
   static constexpr int MAT = BN * RB;               // bytes of a block of one of them
   static constexpr int STAGE = 2 * MAT;
   static constexpr int NI = MAT / 1024 / WQ;        // copy instructions per wave and matrix
   static constexpr int RPI = 1024 / RB;             // rows per copy instruction
+  static constexpr int AHEAD = D == 256 ? 3 : WQ == 1 ? 4 : 6;    // MFMA steps an operand is read ahead
   static constexpr int KC = D / 16, DB = D / 32, SB = BN / 32;
   static constexpr int PITCH = D + 4;               // floats of a row in the joining of key groups
   static constexpr int PIPE = WK * NBUF * STAGE;
@@ -114,97 +136,63 @@ __global__ void __launch_bounds__(64 * C::NW) __attribute__((amdgpu_waves_per_eu
 attn_tile_kernel(AttnArgs p) {
   constexpr int D = C::D, BN = C::BN, WQ = C::WQ, WK = C::WK;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
-  __shared__ int sbad[WK][2];
+  __shared__ int sbad[WK][3], slen[32 * C::WQ];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wq = wave % WQ, wk = wave / WQ;
   const int h = lane >> 5, lr = lane & 31;
 
-  // Workgroup -> (head, part, tile), tiles fastest, in contiguous runs per
-  // XCD: the tiles that read the same keys share an L2.
+  // Workgroup -> (part, tile, head), heads fastest, in contiguous runs per
+  // XCD.  An XCD thus reads the same few key rows for all heads: where the
+  // heads of a key lie side by side, one head alone is 2 D bytes in every
+  // 2 D Hkv and would use few of the L2's channels.
   const int nwg = gridDim.x, wid = blockIdx.x;
   const int u = nwg % 8 == 0 ? (wid % 8) * (nwg / 8) + wid / 8 : wid;
-  const int tile = u % p.tiles, part = u / p.tiles % p.parts, hk = u / p.tiles / p.parts;
+  int tile, hk;
+  const int part = div_by(div_by(u, p.heads, hk), p.tiles, tile);
   const w4a4_attn& a = p.a;
 
   const int r0 = tile * p.rpt, nrows = min(p.rpt, p.rows - r0);
-  const int b0 = r0 / p.tg, nseq = (r0 + nrows - 1) / p.tg - b0 + 1;
-  const int64_t total = p.np + (int64_t)nseq * p.ns;
-  const int lo = (int)(total * part / p.parts), hi = (int)(total * (part + 1) / p.parts);
-  const int iters = (hi - lo + WK - 1) / WK;
+  int rem;
+  const int b0 = div_by(r0, p.tg, rem), nseq = div_by(r0 + nrows - 1, p.tg, rem) - b0 + 1;
+  const int64_t total = p.np + (p.own ? (int64_t)nseq * (int)p.ns.d : 0);
+  const int lo = (int)min((int64_t)part * p.per, total), hi = (int)min((int64_t)lo + p.per, total);
 
-  // this lane's row: query, sequence, and how many of its own keys it sees
-  const int rl = wq * 32 + lr, row = r0 + rl;
-  const bool live = rl < nrows;
-  const int rb = live ? row / p.tg : -1, rt = live ? (row % p.tg) / p.g : 0, rg = live ? row % p.g : 0;
-  auto own_length = [&](int b) {
-    return a.own_len ? max(0, min(a.own_len[b], (int)a.S)) : (int)a.S;
-  };
-  int rlim = live ? own_length(rb) : 0;
-  if (a.causal) rlim = max(0, min(rlim, rlim - (int)a.T + 1 + rt));
-  const int wb0 = (r0 + wq * 32) / p.tg, wb1 = (min(r0 + wq * 32 + 32, r0 + nrows) - 1) / p.tg;   // this wave's sequences
-  const bool wave_live = wq * 32 < nrows;
-  // own value rows are seen by some rows of a wave and not by others
-  const bool mixed = a.causal || nseq > 1;
-
-  v8bf qf[C::KC];
-  {
-    const uint16_t* q = (const uint16_t*)a.q + rb * a.q_sb + rt * a.q_st + (int64_t)(hk * p.g + rg) * a.q_sh + h * 8;
-#pragma unroll
-    for (int c = 0; c < C::KC; ++c) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (live) v = *reinterpret_cast<const uint4*>(q + c * 16);
-      v.x ^= p.qflip; v.y ^= p.qflip; v.z ^= p.qflip; v.w ^= p.qflip;
-      qf[c] = __builtin_bit_cast(v8bf, v);
-    }
-  }
-
-  auto slot_at = [&](int it) {
-    Slot s{-1, 0, 0};
-    const int i = lo + it * WK + wk;
-    if (i >= hi) return s;
-    if (i < p.np) {
-      s.j0 = i * BN;
-      s.valid = min(BN, (int)a.P - s.j0);
-    } else {
-      const int o = i - p.np;
-      s.b = b0 + o / p.ns;
-      s.j0 = o % p.ns * BN;
-      s.valid = max(0, min(BN, own_length(s.b) - s.j0));
-    }
-    return s;
-  };
-
-  // Copies.  Instruction n of a matrix covers rows n RPI + [0, RPI), lane l
-  // chunk l % (D / 8) of row l / (D / 8); excluded rows (past the end, or not
-  // kept) take an out-of-range offset and arrive as zeros, so whatever
-  // lies there never enters a product.
+  // A block on its way from global memory to LDS, 16 bytes a lane and piece:
+  // piece k of a matrix covers rows n RPI + [0, RPI), n = k WQ + wq, lane l
+  // chunk l % (D / 8) of row l / (D / 8).  Excluded rows (past the end, or not
+  // kept) take an out-of-range offset and arrive as zeros, so whatever lies
+  // there never enters a product.
   const uint32_t lds0 = lds_addr(smem);
   const int cr = lane / (D / 8), cc = lane % (D / 8);
-  auto copy = [&](const Slot& s, uint64_t mask, uint32_t dst, const void* base, int64_t stride, bool is_k) {
-    const v4u rs = rsrc_words((const uint16_t*)base + s.j0 * stride, 0x7FFFFFFFu);
-    const uint32_t st2 = (uint32_t)stride * 2;
-    const uint32_t voff = cr * st2;
+  v4i piece[2 * C::NI];
+  auto load_matrix = [&](const Slot& s, uint64_t mask, const uint16_t* base, int64_t stride, bool is_k) {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base + s.j0 * stride, 0x7FFFFFFFu);
+    const uint32_t st2 = (uint32_t)stride * 2, voff = cr * st2;
     const bool full = mask == low_bits<BN>(BN);
 #pragma unroll
     for (int k = 0; k < C::NI; ++k) {
-      const int n = k * WQ + wq, rw = n * C::RPI;
-      const int chunk = cc ^ (is_k ? swz_k<D>(rw + cr) : swz_v<D>(rw + cr));
-      uint32_t off = voff + chunk * 16;
+      const int rw = (k * WQ + wq) * C::RPI;
+      uint32_t off = voff + rw * st2 + (cc ^ (is_k ? swz_k<D>(rw + cr) : swz_v<D>(rw + cr))) * 16;
       if (!full) off = (mask >> (rw + cr)) & 1 ? off : kOOB;
-      dma16_at(rs, dst + n * 1024, off, rw * st2);
+      piece[is_k ? k : C::NI + k] = __builtin_bit_cast(v4i, buf_load16(rs, off));
     }
   };
-  auto issue = [&](const Slot& s, uint64_t mask, int buf) {
+  auto load_block = [&](const Slot& s, uint64_t mask) {
     if (mask == 0) return;
-    const uint32_t dst = lds0 + (wk * C::NBUF + buf) * C::STAGE;
     if (s.b < 0) {
-      copy(s, mask, dst, (const uint16_t*)a.k_prefix + hk * a.kp_sh, a.kp_sp, true);
-      copy(s, mask, dst + C::MAT, (const uint16_t*)a.v_prefix + hk * a.vp_sh, a.vp_sp, false);
+      load_matrix(s, mask, (const uint16_t*)a.k_prefix + hk * a.kp_sh, a.kp_sp, true);
+      load_matrix(s, mask, (const uint16_t*)a.v_prefix + hk * a.vp_sh, a.vp_sp, false);
     } else {
-      copy(s, mask, dst, (const uint16_t*)a.k_own + s.b * a.ko_sb + hk * a.ko_sh, a.ko_ss, true);
-      copy(s, mask, dst + C::MAT, (const uint16_t*)a.v_own + s.b * a.vo_sb + hk * a.vo_sh, a.vo_ss, false);
+      load_matrix(s, mask, (const uint16_t*)a.k_own + s.b * a.ko_sb + hk * a.ko_sh, a.ko_ss, true);
+      load_matrix(s, mask, (const uint16_t*)a.v_own + s.b * a.vo_sb + hk * a.vo_sh, a.vo_ss, false);
     }
+  };
+  auto store_block = [&](int buf) {
+    const uint32_t dst = lds0 + (wk * C::NBUF + buf) * C::STAGE + lane * 16;
+#pragma unroll
+    for (int k = 0; k < 2 * C::NI; ++k)
+      *(__attribute__((address_space(3))) v4i*)(dst + (k >= C::NI ? C::MAT : 0) + ((k % C::NI) * WQ + wq) * 1024) = piece[k];
   };
   // keep bytes of a block, one per lane, loaded an iteration before they are balloted
   auto load_keep = [&](const Slot& s) -> uint32_t {
@@ -215,11 +203,52 @@ attn_tile_kernel(AttnArgs p) {
     const uint64_t in = low_bits<BN>(s.valid);
     return a.prefix_keep && s.b < 0 ? in & __ballot(keep != 0) : in;
   };
+  auto prefix_slot = [&](int i) {
+    const int j0 = i * BN;
+    return Slot{-1, j0, min(BN, (int)a.P - j0)};
+  };
   auto group_sync = [&]() {
     asm volatile("" ::: "memory");
     if constexpr (WQ > 1) __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+
+  // The first prefix blocks are under way before anything else is loaded.
+  const int pend = min(hi, p.np);
+  Slot nxt{-1, 0, 0};
+  uint64_t nmask = 0;
+  const bool early = !C::PINGPONG && lo + wk < pend;
+  if (early) {
+    nxt = prefix_slot(lo + wk);
+    nmask = slot_mask(nxt, load_keep(nxt));
+    load_block(nxt, nmask);
+  }
+
+  // lengths of the tile's sequences
+  for (int i = tid; i < nseq; i += 64 * C::NW) slen[i] = a.own_len ? max(0, min(a.own_len[b0 + i], (int)a.S)) : (int)a.S;
+  if (tid < WK) sbad[tid][0] = sbad[tid][1] = sbad[tid][2] = kNoBad;
+
+  // this lane's row: query, sequence
+  const int rl = wq * 32 + lr, row = r0 + rl;
+  const bool live = rl < nrows;
+  int rt, rg, rb = div_by(live ? row : r0, p.tg, rem);
+  rt = div_by(rem, p.g, rg);
+  const bool wave_live = wq * 32 < nrows;
+  const int wb0 = div_by(r0 + (wave_live ? wq * 32 : 0), p.tg, rem);   // this wave's sequences
+  const int wb1 = div_by(min(r0 + wq * 32 + 32, r0 + nrows) - 1, p.tg, rem);
+  // own value rows are seen by some rows of a wave and not by others
+  const bool mixed = a.causal || nseq > 1;
+
+  v8bf qf[C::KC];
+  {
+    const uint16_t* q = (const uint16_t*)a.q + rb * a.q_sb + rt * a.q_st + (int64_t)(hk * (int)p.g.d + rg) * a.q_sh + h * 8;
+#pragma unroll
+    for (int c = 0; c < C::KC; ++c) {
+      uint4 v = *reinterpret_cast<const uint4*>(q + c * 16);   // rows past the end repeat the tile's first
+      v.x ^= p.qflip; v.y ^= p.qflip; v.z ^= p.qflip; v.w ^= p.qflip;
+      qf[c] = __builtin_bit_cast(v8bf, v);
+    }
+  }
 
   v16f o[C::DB];
 #pragma unroll
@@ -232,68 +261,308 @@ attn_tile_kernel(AttnArgs p) {
   // LDS addresses of the fragment reads, relative to a stage
   const uint32_t ka = lr * C::RB + ((h ^ swz_k<D>(lr)) << 4);
   const int vr = 4 * h + ((lane & 15) >> 2);
-  const uint32_t va = C::MAT + vr * C::RB + (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ swz_v<D>(vr)) << 4) + (lane & 1) * 8;
+  const uint32_t va = vr * C::RB + (((2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ swz_v<D>(vr)) << 4) + (lane & 1) * 8;
 
-  if (tid < WK) sbad[tid][0] = sbad[tid][1] = kNoBad;
-  __syncthreads();
+  // Scores of a block -> probabilities (bf16, in the order the second product
+  // takes them), with m, l and, when m moves, o brought up to date.
+  uint32_t pk[C::SB][8];
+  auto softmax = [&](v16f (&s)[C::SB]) {
+    float tm = s[0][0];
+#pragma unroll
+    for (int b = 0; b < C::SB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) tm = fmaxf(tm, s[b][i]);
+    tm = half_max(tm) * p.c2;
+    if (__any(tm > m + kLazy)) {
+      const float mn = fmaxf(m, tm);
+      const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < C::DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= f;
+    }
+    const float nm = m == -INFINITY ? 0.f : -m;
+    float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+    for (int b = 0; b < C::SB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], p.c2, nm));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i + 1], p.c2, nm));
+        l0 += e0;
+        l1 += e1;
+        pk[b][i >> 1] = pack_bf16(e0, e1);   // the second product takes p with 8 significant bits; l keeps 24
+      }
+    l += l0 + l1;
+  };
+  auto exclude = [&](v16f (&s)[C::SB], uint64_t mask) {
+#pragma unroll
+    for (int b = 0; b < C::SB; ++b) {
+      const uint32_t w = (uint32_t)(mask >> (32 * b)) >> (4 * h);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] = (w >> (8 * (i >> 2) + (i & 3))) & 1 ? s[b][i] : -INFINITY;
+    }
+  };
+  // LDS addresses of this lane's fragment reads in buffer 0; buffers, row
+  // blocks and key steps are constant offsets from them
+  uint32_t kad[C::KC], vad[C::DB];
+#pragma unroll
+  for (int c = 0; c < C::KC; ++c) kad[c] = lds0 + wk * C::NBUF * C::STAGE + (ka ^ (c << 5));
+#pragma unroll
+  for (int d = 0; d < C::DB; ++d) vad[d] = lds0 + wk * C::NBUF * C::STAGE + C::MAT + (va ^ (d << 6));
+  // The products of a block as a list of steps, one MFMA each, with the LDS
+  // reads kAhead steps in front of their MFMA (left to itself the compiler
+  // reads each operand right before its use and waits out the latency every
+  // time).  Both products have as many steps.  Together they start with
+  // kAhead steps of P V, whose operands can be read before the barrier in
+  // front, and then alternate.
+  constexpr int kSteps = C::KC * C::SB;
+  static_assert(kSteps == BN / 16 * C::DB, "products of equal length");
+  constexpr int kAhead = C::AHEAD;
+  static_assert(kAhead <= kSteps, "steps");
+  v4i frag[kAhead];
+  enum { QK = 1, PV = 2, BOTH = 3 };
+  auto step_is_k = [](int what, int t) {
+    return what == QK || (what == BOTH && (t >= 2 * kSteps - kAhead || (t >= kAhead && (t - kAhead) % 2 == 0)));
+  };
+  auto step_index = [](int what, int t) {
+    if (what != BOTH || t < kAhead) return t;
+    if (t >= 2 * kSteps - kAhead) return t - kSteps;
+    return (t - kAhead) / 2 + ((t - kAhead) % 2 == 0 ? 0 : kAhead);
+  };
+  auto fetch = [&](int what, int t, int koff, int voff) {
+    const int x = step_index(what, t);
+    if (step_is_k(what, t)) {
+      frag[t % kAhead] = *(lds_v4i*)(kad[x / C::SB] + koff + x % C::SB * 32 * C::RB);
+    } else {
+      const uint32_t ad = vad[x % C::DB] + voff + x / C::DB * 16 * C::RB;
+      const v4s v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)ad);
+      const v4s v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(ad + 8 * C::RB));
+      frag[t % kAhead] = __builtin_bit_cast(v4i, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  };
+  auto fetch_first = [&](int what, int koff, int voff) {
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) fetch(what, t, koff, voff);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto products = [&](v16f (&s)[C::SB], auto what_, int koff, int voff) {
+    constexpr int what = what_();
+    constexpr int n = what == BOTH ? 2 * kSteps : kSteps;
+#pragma unroll
+    for (int t = 0; t < n; ++t) {
+      const int x = step_index(what, t);
+      const v8bf op = __builtin_bit_cast(v8bf, frag[t % kAhead]);
+      if (step_is_k(what, t)) {
+        s[x % C::SB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op, qf[x / C::SB], s[x % C::SB], 0, 0, 0);
+      } else {
+        const uint32_t* w = &pk[x / C::DB >> 1][(x / C::DB & 1) * 4];
+        const v4i pv = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+        o[x % C::DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op, __builtin_bit_cast(v8bf, pv), o[x % C::DB], 0, 0, 0);
+      }
+      if (t + kAhead < n) fetch(what, t + kAhead, koff, voff);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  struct Qk { constexpr int operator()() const { return QK; } };
+  struct Pv { constexpr int operator()() const { return PV; } };
+  struct Both { constexpr int operator()() const { return BOTH; } };
+  auto clear = [&](v16f (&s)[C::SB]) {
+#pragma unroll
+    for (int b = 0; b < C::SB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+  };
 
-  Slot cur, nxt = slot_at(0);
-  uint64_t cmask, nmask = slot_mask(nxt, load_keep(nxt));
-  if (iters > 0) issue(nxt, nmask, 0);
+  // Prefix blocks with eight waves of rows: waves 0-3 and 4-7 (one of each on
+  // every SIMD) run half an iteration apart, so that one multiplies while the
+  // other does its softmax.  Phase 2 i: waves 0-3 take the products M(i)
+  // (block i - 1 times V, block i times K), waves 4-7 softmax S(i - 1); phase
+  // 2 i + 1: the other way round.  A barrier ends every phase.  Stage i (K and
+  // V of block i) is read in phases 2 i to 2 i + 3.  S(i) copies stage i + 2
+  // into the buffer of stage i - 2 (a copy takes about 100 cycles to issue,
+  // too long between the products of M); each wave waits for its copies of
+  // stage i + 1 in phase 2 i + 1, between M(i) and S(i).
+  int glo = lo;
+  if constexpr (C::PINGPONG) {
+    const int n = pend - lo;
+    glo = max(lo, p.np);
+    if (n > 0) {
+      const bool second = wave >= 4;
+      auto block_at = [&](int i) {
+        Slot b = prefix_slot(lo + i);
+        if (i >= n) b.valid = 0;
+        return b;
+      };
+      // stages are copied in order: the bases step by a block, the lanes'
+      // offsets stay
+      uint64_t kbase = (uint64_t)((const uint16_t*)a.k_prefix + hk * a.kp_sh + (int64_t)lo * BN * a.kp_sp);
+      uint64_t vbase = (uint64_t)((const uint16_t*)a.v_prefix + hk * a.vp_sh + (int64_t)lo * BN * a.vp_sp);
+      uint32_t off[2 * C::NI];
+#pragma unroll
+      for (int k = 0; k < C::NI; ++k) {
+        const int row = (k * WQ + wq) * C::RPI + cr;
+        off[k] = (uint32_t)(row * a.kp_sp * 2) + (cc ^ swz_k<D>(row)) * 16;
+        off[C::NI + k] = (uint32_t)(row * a.vp_sp * 2) + (cc ^ swz_v<D>(row)) * 16;
+      }
+      auto copy_one = [&](int i, int k, uint64_t mask) {   // copy k of 2 NI of stage i
+        const bool isv = k >= C::NI;
+        const int n_ = (isv ? k - C::NI : k) * WQ + wq;
+        const uint64_t b = isv ? vbase : kbase;
+        const v4u rs = {(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, 0x7FFFFFFFu, 0x00020000u};
+        const uint32_t dst = lds0 + (i & 3) * C::STAGE + (isv ? C::MAT : 0) + n_ * 1024;
+        if (mask == low_bits<BN>(BN)) dma16_v(rs, dst, off[k]);
+        else dma16_v(rs, dst, (mask >> (n_ * C::RPI + cr)) & 1 ? off[k] : kOOB);
+      };
+      auto next_stage = [&]() {
+        kbase += BN * a.kp_sp * 2;
+        vbase += BN * a.vp_sp * 2;
+      };
+      uint64_t m0, m1, m2 = 0;   // masks of blocks i, i + 1, i + 2
+      uint32_t keep;             // keep bytes of block i + 2
+      {
+        const Slot s0 = block_at(0), s1 = block_at(1);
+        const uint32_t k0 = load_keep(s0), k1 = load_keep(s1);
+        keep = load_keep(block_at(2));
+        m0 = slot_mask(s0, k0);
+        m1 = slot_mask(s1, k1);
+#pragma unroll
+        for (int k = 0; k < 2 * C::NI; ++k) copy_one(0, k, m0);
+        next_stage();
+        if (n > 1)
+#pragma unroll
+          for (int k = 0; k < 2 * C::NI; ++k) copy_one(1, k, m1);
+        next_stage();
+      }
+      // M(0) has no block before it: its V, in the buffer of stage -1, and P are zero
+#pragma unroll
+      for (int k = 0; k < C::NI; ++k)
+        *(__attribute__((address_space(3))) v4i*)(lds0 + 3 * C::STAGE + C::MAT + (k * WQ + wq) * 1024 + lane * 16) =
+            (v4i){0, 0, 0, 0};
+#pragma unroll
+      for (int b = 0; b < C::SB; ++b)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pk[b][i] = 0;
+#pragma unroll
+      for (int d = 0; d < C::DB; ++d) vad[d] += 3 * C::STAGE;
+      auto phase = [&]() {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+      };
+      v16f s[C::SB];
+      wait_vmcnt<0>();
+      phase();
+      if (second) phase();
+      fetch_first(BOTH, 0, 0);
+      for (int i = 0; i < n; ++i) {
+        __builtin_amdgcn_s_setprio(1);
+        clear(s);
+        products(s, Both(), 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+        const int kstep = (i & 3) == 3 ? -3 * C::STAGE : C::STAGE, vstep = (i & 3) == 0 ? -3 * C::STAGE : C::STAGE;
+#pragma unroll
+        for (int c = 0; c < C::KC; ++c) kad[c] += kstep;
+#pragma unroll
+        for (int d = 0; d < C::DB; ++d) vad[d] += vstep;
+        if (second) wait_vmcnt<0>();   // stage i + 1
+        phase();
+        if (!second) wait_vmcnt<0>();
+        asm volatile("" ::: "memory");
+        if (i + 2 < n) {
+          m2 = slot_mask(block_at(i + 2), keep);
+#pragma unroll
+          for (int k = 0; k < 2 * C::NI; ++k) copy_one(i + 2, k, m2);
+          next_stage();
+          keep = load_keep(block_at(i + 3));
+        }
+        fetch_first(PV, 0, 0);   // the first operands of M(i + 1)
+        if (m0 != low_bits<BN>(BN)) exclude(s, m0);
+        softmax(s);
+        m0 = m1;
+        m1 = m2;
+        phase();
+      }
+      products(s, Pv(), 0, 0);
+      if (!second) phase();
+#pragma unroll
+      for (int c = 0; c < C::KC; ++c) kad[c] -= (n & 3) * C::STAGE;
+#pragma unroll
+      for (int d = 0; d < C::DB; ++d) vad[d] -= ((n - 1) & 3) * C::STAGE;
+      __syncthreads();
+    }
+  }
+
+  // Everything else, block by block: own keys, and prefix keys with fewer waves.
+  __syncthreads();   // lengths and flags are set
+  int rlim = live ? slen[rb - b0] : 0;   // own keys this row sees
+  if (a.causal) rlim = max(0, min(rlim, rlim - (int)a.T + 1 + rt));
+  const int iters = (hi - glo + WK - 1) / WK;
+  auto slot_at = [&](int it) {
+    Slot s{-1, 0, 0};
+    const int i = glo + it * WK + wk;
+    if (i >= hi) return s;
+    if (i < p.np) return prefix_slot(i);
+    int blk;
+    const int sq = div_by(i - p.np, p.ns, blk);
+    s.b = b0 + sq;
+    s.j0 = blk * BN;
+    s.valid = max(0, min(BN, __builtin_amdgcn_readfirstlane(slen[sq]) - s.j0));
+    return s;
+  };
+  if (!early && iters > 0) {
+    nxt = slot_at(0);
+    nmask = slot_mask(nxt, load_keep(nxt));
+    load_block(nxt, nmask);
+  }
   Slot after = slot_at(1);
   uint32_t keep = load_keep(after);
 
-  for (int it = 0; it < iters; ++it) {
-    wait_vmcnt<0>();
-    group_sync();   // the block has landed and the other buffer is no longer read
-    cur = nxt;
-    cmask = nmask;
-    nxt = after;
-    nmask = slot_mask(nxt, keep);
-    if constexpr (C::NBUF > 1) {
-      if (it + 1 < iters) issue(nxt, nmask, (it + 1) & 1);
-      after = slot_at(it + 2);
-      keep = load_keep(after);
-    }
-    const uint32_t stage = lds0 + (wk * C::NBUF + (C::NBUF > 1 ? (it & 1) : 0)) * C::STAGE;
-
-    // Own values that some rows of the tile must not see: a chunk with a NaN
-    // or Inf is zeroed and the rows that do see its key are marked.
-    if (mixed && lo + it * WK + WK > p.np) {
-      if (cur.b >= 0 && cmask != 0) {
+  // Iteration `it` stores its block from registers to LDS, loads the next one
+  // into them, and multiplies.  With one wave per key group the wave's own
+  // order of LDS accesses is all the synchronisation there is, and one buffer
+  // is enough.
+  //
+  // Own values that some rows of the tile must not see: a piece with a NaN or
+  // Inf is stored as zeros, and the rows that do see its key are marked.  The
+  // lowest such key of iteration `it` is in sbad[][it % 3]; the next
+  // iteration's is cleared a barrier before it is written.
+  for (int it = 0, third = 0; it < iters; ++it, third = third == 2 ? 0 : third + 1) {
+    const Slot cur = nxt;
+    const uint64_t cmask = nmask;
+    const int buf = C::NBUF > 1 ? (it & 1) : 0;
+    if (mixed && cur.b >= 0 && cmask != 0) {
 #pragma unroll
-        for (int k = 0; k < C::NI; ++k) {
-          const int n = k * WQ + wq;
-          auto* ptr = (__attribute__((address_space(3))) v4i*)(stage + C::MAT + n * 1024 + lane * 16);
-          const v4i v = *ptr;
-          uint32_t bad = 0;
+      for (int k = C::NI; k < 2 * C::NI; ++k) {
+        uint32_t bad = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) bad |= (((uint32_t)v[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-          if (bad) {
-            *ptr = (v4i){0, 0, 0, 0};
-            atomicMin(&sbad[wk][it & 1], n * C::RPI + cr);
-          }
+        for (int e = 0; e < 4; ++e) bad |= (((uint32_t)piece[k][e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+        if (bad) {
+          piece[k] = (v4i){0, 0, 0, 0};
+          atomicMin(&sbad[wk][third], ((k - C::NI) * WQ + wq) * C::RPI + cr);
         }
       }
-      if (wq == 0 && lane == 0) sbad[wk][(it + 1) & 1] = kNoBad;
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      group_sync();
-      if (cur.b >= 0 && rb == cur.b && cur.j0 + sbad[wk][it & 1] < rlim) poisoned = true;
     }
+    if (cmask != 0) store_block(buf);
+    if (wq == 0 && lane == 0) sbad[wk][third == 2 ? 0 : third + 1] = kNoBad;
+    nxt = after;
+    nmask = it + 1 < iters ? slot_mask(nxt, keep) : 0;
+    load_block(nxt, nmask);
+    after = slot_at(it + 2);
+    keep = load_keep(after);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    group_sync();   // stored by all, and the other buffer is no longer read
+    const int boff = buf * C::STAGE;
+    if (mixed && cur.b >= 0 && live && rb == cur.b && cur.j0 + sbad[wk][third] < rlim) poisoned = true;
 
     const bool mine = cmask != 0 && wave_live && (cur.b < 0 || (cur.b >= wb0 && cur.b <= wb1));
     if (mine) {
       v16f s[C::SB];
-#pragma unroll
-      for (int b = 0; b < C::SB; ++b) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
-#pragma unroll
-        for (int c = 0; c < C::KC; ++c) {
-          const v4i kf = *(lds_v4i*)(stage + (ka ^ (c << 5)) + b * 32 * C::RB);
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, kf), qf[c], s[b], 0, 0, 0);
-        }
-      }
+      clear(s);
+      fetch_first(QK, boff, 0);
+      products(s, Qk(), boff, 0);
       if (cur.b >= 0) {
         const int vis = (rb == cur.b ? rlim - cur.j0 : 0) - 4 * h;
 #pragma unroll
@@ -301,63 +570,11 @@ attn_tile_kernel(AttnArgs p) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[b][i] = 32 * b + 8 * (i >> 2) + (i & 3) < vis ? s[b][i] : -INFINITY;
       } else if (cmask != low_bits<BN>(BN)) {
-#pragma unroll
-        for (int b = 0; b < C::SB; ++b) {
-          const uint32_t w = (uint32_t)(cmask >> (32 * b)) >> (4 * h);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[b][i] = (w >> (8 * (i >> 2) + (i & 3))) & 1 ? s[b][i] : -INFINITY;
-        }
+        exclude(s, cmask);
       }
-      float tm = s[0][0];
-#pragma unroll
-      for (int b = 0; b < C::SB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) tm = fmaxf(tm, s[b][i]);
-      tm = half_max(tm) * p.c2;
-      if (__any(tm > m + kLazy)) {
-        const float mn = fmaxf(m, tm);
-        const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int d = 0; d < C::DB; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[d][i] *= f;
-      }
-      const float nm = m == -INFINITY ? 0.f : -m;
-      uint32_t pk[C::SB][8];
-      float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-      for (int b = 0; b < C::SB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], p.c2, nm));
-          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i + 1], p.c2, nm));
-          l0 += e0;
-          l1 += e1;
-          pk[b][i >> 1] = pack_bf16(e0, e1);   // the second product takes p with 8 significant bits; l keeps 24
-        }
-      l += l0 + l1;
-#pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk) {
-        const uint32_t* w = &pk[kk >> 1][(kk & 1) * 4];
-        const v4i pv = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-#pragma unroll
-        for (int d = 0; d < C::DB; ++d) {
-          const uint32_t ad = stage + (va ^ (d << 6)) + kk * 16 * C::RB;
-          const v4s v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)ad);
-          const v4s v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(ad + 8 * C::RB));
-          const auto vv = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, vv), __builtin_bit_cast(v8bf, pv), o[d],
-                                                         0, 0, 0);
-        }
-      }
-    }
-    if constexpr (C::NBUF == 1) {
-      group_sync();
-      if (it + 1 < iters) issue(nxt, nmask, 0);
-      after = slot_at(it + 2);
-      keep = load_keep(after);
+      softmax(s);
+      fetch_first(PV, 0, boff);
+      products(s, Pv(), 0, boff);
     }
   }
   wait_vmcnt<0>();   // no copy may land in memory that is used differently below
@@ -407,8 +624,8 @@ attn_tile_kernel(AttnArgs p) {
         if (d == 0) *reinterpret_cast<v2f*>(p.pml + x * 2) = (v2f){M, L};
       } else {
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        uint16_t* out = (uint16_t*)a.out + gr / p.tg * a.o_sb + gr % p.tg / p.g * a.o_st +
-                        (int64_t)(hk * p.g + gr % p.g) * a.o_sh + d;
+        int og, ob = div_by(gr, p.tg, rem), ot = div_by(rem, p.g, og);
+        uint16_t* out = (uint16_t*)a.out + ob * a.o_sb + ot * a.o_st + (int64_t)(hk * (int)p.g.d + og) * a.o_sh + d;
         *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
       }
     }
@@ -425,7 +642,7 @@ attn_tile_kernel(AttnArgs p) {
       if (h == 0) *reinterpret_cast<v2f*>(p.pml + x * 2) = (v2f){m, l};
     } else {
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint16_t* out = (uint16_t*)a.out + rb * a.o_sb + rt * a.o_st + (int64_t)(hk * p.g + rg) * a.o_sh;
+      uint16_t* out = (uint16_t*)a.out + rb * a.o_sb + rt * a.o_st + (int64_t)(hk * (int)p.g.d + rg) * a.o_sh;
 #pragma unroll
       for (int d = 0; d < C::DB; ++d)
 #pragma unroll
@@ -447,9 +664,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs p) {
   const int64_t all = (int64_t)a.Hkv * p.rows;
   if (gr >= all) return;
   float M = -INFINITY, L = 0.f;
+#pragma unroll 4
   for (int k = 0; k < p.parts; ++k) M = fmaxf(M, p.pml[(k * all + gr) * 2]);
   const float ms = M == -INFINITY ? 0.f : M;
   v4f acc = {0, 0, 0, 0};
+#pragma unroll 4
   for (int k = 0; k < p.parts; ++k) {
     const v2f ml = *reinterpret_cast<const v2f*>(p.pml + (k * all + gr) * 2);
     const float f = __builtin_amdgcn_exp2f(ml[0] - ms);
@@ -457,23 +676,27 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs p) {
     acc += *reinterpret_cast<const v4f*>(p.po + (k * all + gr) * D + d) * f;
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int hk = (int)(gr / p.rows), row = (int)(gr % p.rows);
-  uint16_t* out = (uint16_t*)a.out + row / p.tg * a.o_sb + row % p.tg / p.g * a.o_st + (int64_t)(hk * p.g + row % p.g) * a.o_sh + d;
+  const int hk = (int)gr / p.rows, row = (int)gr % p.rows;
+  int rem, g, b = div_by(row, p.tg, rem), t = div_by(rem, p.g, g);
+  uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * (int)p.g.d + g) * a.o_sh + d;
   *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
 }
 
 struct AttnPlan {
   int cfg;     // index of the (WQ, WK) pair
   int rpt, tiles, parts, np, ns;
+  int per;     // blocks of a part
 };
 
 struct Shape {
   int wq, wk, bn;
+  double us;   // an iteration of a workgroup, all CUs busy
 };
 // (WQ, WK, BN) per head width; the kernels below are instantiated from it.
-constexpr Shape kShapes[3][4] = {{{1, 4, 64}, {2, 4, 64}, {4, 2, 64}, {8, 1, 64}},     // D = 64
-                                 {{1, 4, 32}, {2, 4, 32}, {4, 2, 64}, {8, 1, 64}},     // D = 128
-                                 {{1, 4, 32}, {2, 2, 32}, {4, 1, 32}, {4, 1, 32}}};    // D = 256
+constexpr Shape kShapes[3][4] = {
+    {{1, 8, 64, 2.0}, {2, 4, 64, 1.8}, {4, 2, 64, 2.0}, {8, 1, 64, 1.5}},      // D = 64
+    {{1, 8, 32, 3.05}, {2, 4, 32, 2.3}, {4, 2, 64, 3.0}, {8, 1, 64, 2.0}},     // D = 128
+    {{2, 2, 32, 3.0}, {4, 1, 32, 2.6}, {0, 0, 0, 0.0}, {0, 0, 0, 0.0}}};       // D = 256
 constexpr int kCUs = 256;
 
 AttnPlan plan_attention(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t P, int64_t S, bool split) {
@@ -482,7 +705,7 @@ AttnPlan plan_attention(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D
   AttnPlan best{};
   double best_cost = 1e300;
   for (int c = 0; c < 4; ++c) {
-    if (D == 256 && c == 3) break;
+    if (sh[c].wq == 0) break;
     const int64_t R = 32 * sh[c].wq;
     const int64_t rpt = tg <= R ? R / tg * tg : R;
     const int64_t tiles = (rows + rpt - 1) / rpt;
@@ -490,20 +713,25 @@ AttnPlan plan_attention(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D
     const int64_t nseq = tg <= R ? rpt / tg : (R + tg - 1) / tg + (R % tg != 0);
     const int64_t total = np + (nseq < B ? nseq : B) * ns;
     const int64_t units = Hkv * tiles;
-    // parts: one round of the card's CUs, with at least one block per key group
-    int64_t parts = 1;
-    if (split && units < kCUs) parts = kCUs / units;
+    // Parts: up to one round of the card's CUs, with at least one block per
+    // key group, halved as long as that is cheaper.
     const int64_t cap = (total + sh[c].wk - 1) / sh[c].wk;
-    if (parts > cap) parts = cap < 1 ? 1 : cap;
-    const int64_t per = (total + parts * sh[c].wk - 1) / (parts * sh[c].wk);    // iterations of a workgroup
-    const int64_t rounds = (units * parts + kCUs - 1) / kCUs;
-    // microseconds: an iteration, and the join's launch and traffic
-    const double iter = (sh[c].bn / 64.0) * (D / 128.0) * (sh[c].wq * sh[c].wk > 4 ? 1.5 : 1.0);
-    double cost = rounds * (per * iter + 2.0);
-    if (parts > 1) cost += 3.0 + parts * Hkv * rows * (double)D * 8.0 / 4e6;
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = {c, (int)rpt, (int)tiles, (int)parts, (int)np, (int)ns};
+    int64_t most = split && units < kCUs ? kCUs / units : 1;
+    if (most > cap) most = cap < 1 ? 1 : cap;
+    for (int64_t want = most; want >= 1; want /= 2) {
+      const int64_t blocks = total < 1 ? 1 : (total + want - 1) / want;
+      const int64_t parts = total < 1 ? 1 : (total + blocks - 1) / blocks;
+      const int64_t iters = (blocks + sh[c].wk - 1) / sh[c].wk, rounds = (units * parts + kCUs - 1) / kCUs;
+      // Microseconds, fitted to measurements (D = 128: a decoding batch of 64
+      // over 8192 keys 40 us as planned, 46 with 32-row tiles; a chunk of 8 x
+      // 50 over 2040 keys 26 as planned, 29 with 64-row tiles): iterations,
+      // start and end of a workgroup, and the join's launch, parts and bytes.
+      double cost = rounds * (iters * sh[c].us + 5.0);
+      if (parts > 1) cost += 3.5 + 0.1 * parts + parts * Hkv * rows * (double)D * 8.0 / 4e6;
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {c, (int)rpt, (int)tiles, (int)parts, (int)np, (int)ns, (int)blocks};
+      }
     }
   }
   return best;
@@ -511,7 +739,7 @@ AttnPlan plan_attention(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D
 
 template <typename C>
 void launch_tiles(const AttnArgs& p, hipStream_t st) {
-  attn_tile_kernel<C><<<(unsigned)(p.a.Hkv * p.tiles * p.parts), 64 * C::NW, 0, st>>>(p);
+  attn_tile_kernel<C><<<(unsigned)(p.a.Hkv * p.tiles.d * p.parts), 64 * C::NW, 0, st>>>(p);
 }
 
 }  // namespace
@@ -525,14 +753,18 @@ hipError_t launch_prefix_attention(const w4a4_attn& a, void* workspace, hipStrea
   const AttnPlan pl = plan_attention(a.B, a.T, a.Hq, a.Hkv, a.D, a.P, a.S, workspace != nullptr);
   AttnArgs p{};
   p.a = a;
-  p.g = (int)(a.Hq / a.Hkv);
-  p.tg = (int)a.T * p.g;
-  p.rows = (int)(a.B * p.tg);
+  const int64_t g = a.Hq / a.Hkv;
+  p.g = divisor(g);
+  p.tg = divisor(a.T * g);
+  p.rows = (int)(a.B * a.T * g);
   p.rpt = pl.rpt;
-  p.tiles = pl.tiles;
+  p.tiles = divisor(pl.tiles);
   p.parts = pl.parts;
+  p.heads = divisor(a.Hkv);
   p.np = pl.np;
-  p.ns = pl.ns;
+  p.ns = divisor(pl.ns > 0 ? pl.ns : 1);
+  p.own = pl.ns > 0;
+  p.per = pl.per;
   // A scale of zero weighs all keys alike; the tiny positive factor keeps
   // -inf (excluded) times the scale at -inf.
   const float c2 = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
@@ -543,18 +775,17 @@ hipError_t launch_prefix_attention(const w4a4_attn& a, void* workspace, hipStrea
     p.pml = p.po + (size_t)pl.parts * a.Hkv * p.rows * a.D;
   }
   if (a.D == 64) {
-    if (pl.cfg == 0) launch_tiles<ACfg<64, 1, 4, 64, 2>>(p, st);
+    if (pl.cfg == 0) launch_tiles<ACfg<64, 1, 8, 64, 1>>(p, st);
     else if (pl.cfg == 1) launch_tiles<ACfg<64, 2, 4, 64, 2>>(p, st);
     else if (pl.cfg == 2) launch_tiles<ACfg<64, 4, 2, 64, 2>>(p, st);
-    else launch_tiles<ACfg<64, 8, 1, 64, 2>>(p, st);
+    else launch_tiles<ACfg<64, 8, 1, 64, 4>>(p, st);
   } else if (a.D == 128) {
-    if (pl.cfg == 0) launch_tiles<ACfg<128, 1, 4, 32, 2>>(p, st);
+    if (pl.cfg == 0) launch_tiles<ACfg<128, 1, 8, 32, 1>>(p, st);
     else if (pl.cfg == 1) launch_tiles<ACfg<128, 2, 4, 32, 2>>(p, st);
     else if (pl.cfg == 2) launch_tiles<ACfg<128, 4, 2, 64, 2>>(p, st);
-    else launch_tiles<ACfg<128, 8, 1, 64, 2>>(p, st);
+    else launch_tiles<ACfg<128, 8, 1, 64, 4>>(p, st);
   } else {
-    if (pl.cfg == 0) launch_tiles<ACfg<256, 1, 4, 32, 1>>(p, st);
-    else if (pl.cfg == 1) launch_tiles<ACfg<256, 2, 2, 32, 2>>(p, st);
+    if (pl.cfg == 0) launch_tiles<ACfg<256, 2, 2, 32, 2>>(p, st);
     else launch_tiles<ACfg<256, 4, 1, 32, 2>>(p, st);
   }
   hipError_t e = hipGetLastError();

@@ -223,7 +223,7 @@ gemm_bf16_kernel(GemmPlanArgs p) {
 #pragma unroll
   for (int b = 0; b < C::NBUF - 1; ++b) copy_stage(s0 + b);
   for (int s = s0; s < s1; ++s) {
-    wait_vmcnt<C::DPS * (C::NBUF - 2)>();   // stage s has landed, later ones may be in flight
+    wait_vmcnt_lds<C::DPS * (C::NBUF - 2)>();   // stage s has landed (later ones may be in flight), s - 1 is read
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();           // for every wave; and stage s - 1 is no longer read
     asm volatile("" ::: "memory");
