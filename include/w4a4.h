@@ -432,7 +432,8 @@ size_t w4a4_workspace_size(int64_t M, int64_t N, int64_t K, int32_t fmt);
  *  q, out    bf16 [B, T, Hq, D];  k_prefix, v_prefix  bf16 [P, Hkv, D];
  *            k_own, v_own  bf16 [B, S, Hkv, D].  The last dimension is
  *            contiguous; the other strides are in elements, multiples of 8,
- *            at most 2^22 (batch strides: any).  Pointers 16-byte aligned.
+ *            at most 2^22 (batch strides: any); those of a dimension of
+ *            one are not used.  Pointers 16-byte aligned.
  *            out overlaps no input.
  *  own_len   device int32[B], clamped to [0, S]; NULL: S for every sequence.
  *  prefix_keep  device uint8[P], or NULL: all kept.

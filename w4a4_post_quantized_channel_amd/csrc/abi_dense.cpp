@@ -60,9 +60,18 @@ int check_attn_sizes(const char* fn, int64_t B, int64_t T, int64_t Hq, int64_t H
 
 extern "C" {
 
-int w4a4_prefix_attention(const w4a4_attn* a, void* workspace, size_t workspace_bytes, void* stream) {
+int w4a4_prefix_attention(const w4a4_attn* desc, void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "w4a4_prefix_attention";
-  if (!a) return fail(W4A4_ERR_INVALID_ARG, "%s: NULL descriptor", fn);
+  if (!desc) return fail(W4A4_ERR_INVALID_ARG, "%s: NULL descriptor", fn);
+  w4a4_attn copy = *desc;
+  w4a4_attn* a = &copy;
+  // the stride of a dimension of one is not used and may be anything
+  if (a->B == 1) a->q_sb = a->o_sb = a->ko_sb = a->vo_sb = 0;
+  if (a->T == 1) a->q_st = a->o_st = 0;
+  if (a->Hq == 1) a->q_sh = a->o_sh = 0;
+  if (a->Hkv == 1) a->kp_sh = a->vp_sh = a->ko_sh = a->vo_sh = 0;
+  if (a->P == 1) a->kp_sp = a->vp_sp = 0;
+  if (a->S == 1) a->ko_ss = a->vo_ss = 0;
   int st = check_attn_sizes(fn, a->B, a->T, a->Hq, a->Hkv, a->D, a->P, a->S);
   if (st != W4A4_OK) return st;
   if (!std::isfinite(a->scale)) return fail(W4A4_ERR_INVALID_ARG, "%s: scale not finite", fn);

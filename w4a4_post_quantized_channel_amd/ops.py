@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -48,24 +49,11 @@ class BranchDesc(ctypes.Structure):
                 ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64)]
 
 
-class AttnDesc(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "T", "Hq", "Hkv", "D", "P", "S")] +
-                [("scale", ctypes.c_float), ("causal", ctypes.c_int32)] +
-                [("q", ctypes.c_void_p), ("q_sb", ctypes.c_int64), ("q_st", ctypes.c_int64), ("q_sh", ctypes.c_int64),
-                 ("k_prefix", ctypes.c_void_p), ("kp_sp", ctypes.c_int64), ("kp_sh", ctypes.c_int64),
-                 ("v_prefix", ctypes.c_void_p), ("vp_sp", ctypes.c_int64), ("vp_sh", ctypes.c_int64),
-                 ("k_own", ctypes.c_void_p), ("ko_sb", ctypes.c_int64), ("ko_ss", ctypes.c_int64),
-                 ("ko_sh", ctypes.c_int64),
-                 ("v_own", ctypes.c_void_p), ("vo_sb", ctypes.c_int64), ("vo_ss", ctypes.c_int64),
-                 ("vo_sh", ctypes.c_int64),
-                 ("own_len", ctypes.c_void_p), ("prefix_keep", ctypes.c_void_p),
-                 ("out", ctypes.c_void_p), ("o_sb", ctypes.c_int64), ("o_st", ctypes.c_int64),
-                 ("o_sh", ctypes.c_int64)])
+# w4a4_attn, packed (filling a ctypes structure of 36 fields takes longer than a short kernel)
+_ATTN = struct.Struct("7qfi" + "4q" + "3q3q" + "4q4q" + "2q" + "4q")
 
 
-class EpilogueDesc(ctypes.Structure):
-    _fields_ = [("act", ctypes.c_int32), ("bias_dtype", ctypes.c_int32), ("bias", ctypes.c_void_p),
-                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64)]
+_EPILOGUE = struct.Struct("2i3q")   # w4a4_epilogue
 
 
 class W4A4Error(RuntimeError):
@@ -100,9 +88,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "w4a4_linear_plan": [i64, i64, i64, i32, i32, ctypes.POINTER(ctypes.c_int32)],
         "w4a4_lowrank_width": [i64, i64, i64],
         "w4a4_transform_amax": [vp, i32, i64, i64, i64, vp, qd, vp, vp],
-        "w4a4_prefix_attention": [ctypes.POINTER(AttnDesc), vp, sz, vp],
+        "w4a4_prefix_attention": [ctypes.c_char_p, vp, sz, vp],   # a packed w4a4_attn
         "w4a4_prefix_attention_workspace": [i64] * 7,
-        "bf16_linear": [vp, i64, vp, i64, i64, i64, i64, ctypes.POINTER(EpilogueDesc), vp, i32, i64, vp, sz, vp],
+        "bf16_linear": [vp, i64, vp, i64, i64, i64, i64, ctypes.c_char_p, vp, i32, i64, vp, sz, vp],
         "w4a4_bf16_workspace_size": [i64, i64, i64, i32],
         "w4a4_group_norm_act": [vp, i32, i64, i64, i64, i64, i64, i64, vp, vp, f32, i32, vp, i64, i64, vp, sz, vp],
         "w4a4_group_norm_workspace": [i64] * 4,
@@ -437,9 +425,12 @@ def lowrank_project(x: torch.Tensor, *, l1t: Optional[torch.Tensor] = None, idx:
 # ---------------------------------------------------------------------------
 # 16-bit operators beside the quantized linears
 # ---------------------------------------------------------------------------
-def _ld(rows: int, cols: int, ld: int) -> int:
-    """A row stride; that of a single row is not used and may be anything."""
-    return ld if rows > 1 else cols
+def _matrix(name: str, t: torch.Tensor):
+    """(rows, columns, row stride) of a row-major matrix; the stride of a single row is not used."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a 2-D row-major tensor")
+    rows, cols = t.shape
+    return rows, cols, t.stride(0) if rows > 1 else cols
 
 
 def _act_code(act: str) -> int:
@@ -453,17 +444,18 @@ def _ws(nbytes: int, device) -> Optional[torch.Tensor]:
 
 
 def _ws_args(workspace):
-    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
 
 
 def _attn_operand(name: str, t: torch.Tensor, shape):
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bf16")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.stride(-1) != 1:
+    st = t.stride()
+    if st[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return [s if n > 1 else 0 for n, s in zip(t.shape, t.stride())]   # a dimension of one is never stepped
+    return st
 
 
 def make_prefix_attention_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, P: int, S: int,
@@ -484,25 +476,30 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     defaults to 1 / sqrt(D).  See include/w4a4.h for the formula and the masks.
     """
     B, T, Hq, D = q.shape
-    P, Hkv = k_prefix.shape[:2]
+    P, Hkv, _ = k_prefix.shape
     S = k_own.shape[1]
     if out is None:
         out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    qs, os_ = _attn_operand("q", q, (B, T, Hq, D)), _attn_operand("out", out, (B, T, Hq, D))
-    kps, vps = _attn_operand("k_prefix", k_prefix, (P, Hkv, D)), _attn_operand("v_prefix", v_prefix, (P, Hkv, D))
-    kos, vos = _attn_operand("k_own", k_own, (B, S, Hkv, D)), _attn_operand("v_own", v_own, (B, S, Hkv, D))
-    if own_len is not None and (own_len.dtype != torch.int32 or own_len.shape != (B,) or not own_len.is_contiguous()):
+    qb, qt, qh, _ = _attn_operand("q", q, (B, T, Hq, D))
+    ob, ot, oh, _ = _attn_operand("out", out, (B, T, Hq, D))
+    kpp, kph, _ = _attn_operand("k_prefix", k_prefix, (P, Hkv, D))
+    vpp, vph, _ = _attn_operand("v_prefix", v_prefix, (P, Hkv, D))
+    kob, kos, koh, _ = _attn_operand("k_own", k_own, (B, S, Hkv, D))
+    vob, vos, voh, _ = _attn_operand("v_own", v_own, (B, S, Hkv, D))
+    if own_len is not None and (own_len.dtype is not torch.int32 or own_len.shape != (B,)
+                                or not own_len.is_contiguous()):
         raise TypeError("own_len must be a contiguous int32[B] tensor")
     if prefix_keep is not None and (prefix_keep.dtype not in (torch.bool, torch.uint8) or prefix_keep.shape != (P,)
                                     or not prefix_keep.is_contiguous()):
         raise TypeError("prefix_keep must be a contiguous bool or uint8 [P] tensor")
-    d = AttnDesc(B, T, Hq, Hkv, D, P, S, D ** -0.5 if scale is None else scale, int(causal),
-                 q.data_ptr(), qs[0], qs[1], qs[2], k_prefix.data_ptr(), kps[0], kps[1],
-                 v_prefix.data_ptr(), vps[0], vps[1], k_own.data_ptr(), kos[0], kos[1], kos[2],
-                 v_own.data_ptr(), vos[0], vos[1], vos[2], None if own_len is None else own_len.data_ptr(),
-                 None if prefix_keep is None else prefix_keep.data_ptr(), out.data_ptr(), os_[0], os_[1], os_[2])
-    st = LIB.w4a4_prefix_attention(ctypes.byref(d), *_ws_args(workspace), _stream(stream))
-    _check("w4a4_prefix_attention", st)
+    desc = _ATTN.pack(B, T, Hq, Hkv, D, P, S, D ** -0.5 if scale is None else scale, causal,
+                      q.data_ptr(), qb, qt, qh, k_prefix.data_ptr(), kpp, kph, v_prefix.data_ptr(), vpp, vph,
+                      k_own.data_ptr(), kob, kos, koh, v_own.data_ptr(), vob, vos, voh,
+                      0 if own_len is None else own_len.data_ptr(),
+                      0 if prefix_keep is None else prefix_keep.data_ptr(), out.data_ptr(), ob, ot, oh)
+    st = LIB.w4a4_prefix_attention(desc, *_ws_args(workspace), _stream(stream))
+    if st != 0:
+        _check("w4a4_prefix_attention", st)
     return out
 
 
@@ -519,32 +516,33 @@ def bf16_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor
     fp32 or bf16 with one entry per row of w; residual has y's shape and type
     and may be y itself.
     """
-    M, K, ldx = _rowmajor(x)
-    NW, Kw, ldw = _rowmajor(w)
+    M, K, ldx = _matrix("x", x)
+    NW, Kw, ldw = _matrix("w", w)
     code = _act_code(act)
-    if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+    if x.dtype is not torch.bfloat16 or w.dtype is not torch.bfloat16:
         raise TypeError("bf16_linear takes bf16 x and w")
     if Kw != K or (code == 5 and NW % 2):
         raise ValueError(f"w of shape {tuple(w.shape)} does not fit x of shape {tuple(x.shape)} with act={act!r}")
     N = NW // 2 if code == 5 else NW
     if y is None:
         y = torch.empty((M, N), dtype=y_dtype, device=x.device)
-    My, Ny, ldy = _rowmajor(y)
-    if (My, Ny) != (M, N):
+    My, Ny, ldy = _matrix("y", y)
+    if My != M or Ny != N:
         raise ValueError(f"y has shape {tuple(y.shape)}, expected {(M, N)}")
-    ep = EpilogueDesc(code, DT_F32, None, None, 0)
+    bdt, bp, rp, ldr = DT_F32, 0, 0, 0
     if bias is not None:
         if bias.shape != (NW,) or not bias.is_contiguous():
             raise ValueError("bias must be contiguous, one entry per row of w")
-        ep.bias_dtype, ep.bias = _dtype_code(bias), bias.data_ptr()
+        bdt, bp = _dtype_code(bias), bias.data_ptr()
     if residual is not None:
-        Mr, Nr, ldr = _rowmajor(residual)
-        if residual.dtype != y.dtype or (Mr, Nr) != (M, N):
+        Mr, Nr, ldr = _matrix("residual", residual)
+        if residual.dtype is not y.dtype or Mr != M or Nr != N:
             raise TypeError("residual must have y's shape and dtype")
-        ep.residual, ep.ldr = residual.data_ptr(), _ld(M, N, ldr)
-    st = LIB.bf16_linear(x.data_ptr(), _ld(M, K, ldx), w.data_ptr(), _ld(NW, K, ldw), M, N, K, ctypes.byref(ep),
-                         y.data_ptr(), _dtype_code(y), _ld(M, N, ldy), *_ws_args(workspace), _stream(stream))
-    _check("bf16_linear", st)
+        rp = residual.data_ptr()
+    st = LIB.bf16_linear(x.data_ptr(), ldx, w.data_ptr(), ldw, M, N, K, _EPILOGUE.pack(code, bdt, bp, rp, ldr),
+                         y.data_ptr(), _dtype_code(y), ldy, *_ws_args(workspace), _stream(stream))
+    if st != 0:
+        _check("bf16_linear", st)
     return y
 
 
@@ -568,8 +566,9 @@ def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
         if v is not None and (v.dtype != torch.float32 or v.shape != (C,) or not v.is_contiguous()):
             raise TypeError(f"{name} must be a contiguous fp32[C] tensor")
     st = LIB.w4a4_group_norm_act(x.data_ptr(), _dtype_code(x), N, S, C, groups, x.stride(0),
-                                 _ld(S, C, x.stride(1)), _ptr(weight), _ptr(bias), float(eps), _act_code(act),
-                                 out.data_ptr(), out.stride(0), _ld(S, C, out.stride(1)), *_ws_args(workspace),
+                                 x.stride(1) if S > 1 else C, _ptr(weight), _ptr(bias), float(eps), _act_code(act),
+                                 out.data_ptr(), out.stride(0), out.stride(1) if S > 1 else C, *_ws_args(workspace),
                                  _stream(stream))
-    _check("w4a4_group_norm_act", st)
+    if st != 0:
+        _check("w4a4_group_norm_act", st)
     return out
