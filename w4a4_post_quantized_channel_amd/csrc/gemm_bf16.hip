@@ -174,37 +174,31 @@ gemm_bf16_kernel(GemmPlanArgs p) {
   const v4u rsU = GATED ? rsrc_words(g.w + ((int64_t)g.N + n0) * g.ldw, 0x7FFFFFFFu) : rsB;
   const int crow = lane >> 3, cslot = lane & 7;
   uint32_t offA[C::PA], offB[C::PB];
-  int colA[C::PA], colB[C::PB];
+  // NW is even: the row's bits that the swizzle takes are the same in every instruction of a wave
+  const int col = (cslot ^ swz128((wave & 1) * 8 + crow)) * 16;
 #pragma unroll
   for (int k = 0; k < C::PA; ++k) {
     const int n = k * NW + wave, row = n * 8 + crow;
-    colA[k] = (cslot ^ swz128(row)) * 16;
-    offA[k] = n < C::NA && m0 + row < g.M ? (uint32_t)(row * g.ldx * 2) + colA[k] : kOOB;
+    offA[k] = n < C::NA && m0 + row < g.M ? (uint32_t)(row * g.ldx * 2) + col : kOOB;
   }
 #pragma unroll
   for (int k = 0; k < C::PB; ++k) {
     const int n = k * NW + wave, row = n * 8 + crow;
     const int nl = GATED ? (row >> 5) * 16 + (row & 15) : row;   // output column within the tile
-    colB[k] = (cslot ^ swz128(row)) * 16;
-    offB[k] = n < C::NB && n0 + nl < g.N ? (uint32_t)(nl * g.ldw * 2) + colB[k] : kOOB;
+    offB[k] = n < C::NB && n0 + nl < g.N ? (uint32_t)(nl * g.ldw * 2) + col : kOOB;
   }
   const int kbytes = g.K * 2;
-  auto copy_stage = [&](int s) {
+  // copy k of DPS of stage s
+  auto copy_one = [&](int s, int k) {
+    const bool isa = k < C::PA;
+    const int n = (isa ? k : k - C::PA) * NW + wave;
     const uint32_t base = lds0 + (uint32_t)((s - s0) % C::NBUF) * C::STAGE;
     const uint32_t pad = lds0 + C::NBUF * C::STAGE;
     const int left = s < s1 ? kbytes - s * 128 : 0;   // bytes of this stage's rows
     const uint32_t k0 = left > 0 ? s * 128u : 0;
-#pragma unroll
-    for (int k = 0; k < C::PA; ++k) {
-      const int n = k * NW + wave;
-      dma16_at(rsA, (C::NA % NW == 0 || n < C::NA) ? base + n * 1024 : pad, colA[k] < left ? offA[k] : kOOB, k0);
-    }
-#pragma unroll
-    for (int k = 0; k < C::PB; ++k) {
-      const int n = k * NW + wave;
-      dma16_at(GATED && (n & 2) ? rsU : rsB, (C::NB % NW == 0 || n < C::NB) ? base + C::A_BYTES + n * 1024 : pad,
-               colB[k] < left ? offB[k] : kOOB, k0);
-    }
+    const bool real = isa ? (C::NA % NW == 0 || n < C::NA) : (C::NB % NW == 0 || n < C::NB);
+    dma16_at(isa ? rsA : (GATED && (n & 2)) ? rsU : rsB, real ? base + (isa ? 0 : C::A_BYTES) + n * 1024 : pad,
+             col < left ? (isa ? offA[k < C::PA ? k : 0] : offB[k >= C::PA ? k - C::PA : 0]) : kOOB, k0);
   };
 
   v4f acc[TI][TJ];
@@ -220,26 +214,48 @@ gemm_bf16_kernel(GemmPlanArgs p) {
     boff[k] = C::A_BYTES + (wn + lr) * 128 + (((4 * k + lq) ^ swz128(lr)) << 4);
   }
 
+  // A stage is 2 TI steps of TJ products: step t multiplies fragment t % TI of
+  // x with all of W's fragments of K half t / TI.  x fragments are read two
+  // steps ahead, W's second half during the first, and the next stage's
+  // copies, which take about 100 cycles each to issue, go one to a step.
+  // The order is pinned: left to itself the compiler reads operands right
+  // before their use.
 #pragma unroll
-  for (int b = 0; b < C::NBUF - 1; ++b) copy_stage(s0 + b);
+  for (int b = 0; b < C::NBUF - 1; ++b)
+#pragma unroll
+    for (int k = 0; k < C::DPS; ++k) copy_one(s0 + b, k);
+  constexpr int RING = 3, STEPS = 2 * TI, CPS = (C::DPS + STEPS - 1) / STEPS, BPS = (TJ + TI - 1) / TI;
   for (int s = s0; s < s1; ++s) {
     wait_vmcnt_lds<C::DPS * (C::NBUF - 2)>();   // stage s has landed (later ones may be in flight), s - 1 is read
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();           // for every wave; and stage s - 1 is no longer read
+    __builtin_amdgcn_s_barrier();           // for every wave
     asm volatile("" ::: "memory");
-    copy_stage(s + C::NBUF - 1);
     const uint8_t* base = smem + (s - s0) % C::NBUF * C::STAGE;
+    v8bf a[RING], b[2][TJ];
+    auto read_a = [&](int t) {
+      a[t % RING] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(base + aoff[t / TI] + t % TI * 2048));
+    };
+    auto read_b = [&](int k, int j) {
+      b[k][j] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(base + boff[k] + j * 2048));
+    };
+    read_a(0);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      v8bf a[TI], b[TJ];
+    for (int j = 0; j < TJ; ++j) read_b(0, j);
+    read_a(1);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) b[j] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(base + boff[k] + j * 2048));
+    for (int t = 0; t < STEPS; ++t) {
+      if (t + 2 < STEPS) read_a(t + 2);
+      if (t < TI)
 #pragma unroll
-      for (int i = 0; i < TI; ++i) a[i] = __builtin_bit_cast(v8bf, *reinterpret_cast<const uint4*>(base + aoff[k] + i * 2048));
+        for (int j = t * BPS; j < (t + 1) * BPS && j < TJ; ++j) read_b(1, j);
 #pragma unroll
-      for (int i = 0; i < TI; ++i)
+      for (int j = 0; j < TJ; ++j)
+        acc[t % TI][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t / TI][j], a[t % RING], acc[t % TI][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+      for (int k = t * CPS; k < (t + 1) * CPS && k < C::DPS; ++k) copy_one(s + C::NBUF - 1, k);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   wait_vmcnt<0>();
@@ -289,10 +305,10 @@ gemm_bf16_kernel(GemmPlanArgs p) {
 
 // Adds the K splits in order and runs the epilogue: 8 columns a thread.
 template <int KIND, bool GATED>
-__global__ void __launch_bounds__(256) gemm_bf16_join_kernel(GemmPlanArgs p) {
+__global__ void __launch_bounds__(64) gemm_bf16_join_kernel(GemmPlanArgs p) {
   const DenseArgs& g = p.g;
   const int chunks = (g.N + 7) / 8;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t id = (int64_t)blockIdx.x * 64 + threadIdx.x;
   if (id >= (int64_t)g.M * chunks) return;
   const int m = (int)(id / chunks), n = (int)(id % chunks) * 8;
   // column n of the partial rows: SwiGLU rows hold 16 gate then 16 up values
@@ -300,6 +316,7 @@ __global__ void __launch_bounds__(256) gemm_bf16_join_kernel(GemmPlanArgs p) {
   const float* src = p.part + (int64_t)m * p.pn + col;
   const int64_t step = (int64_t)g.M * p.pn;
   v4f z0 = {0, 0, 0, 0}, z1 = z0, u0 = z0, u1 = z0;
+#pragma unroll 8
   for (int s = 0; s < p.splits; ++s, src += step) {
     z0 += *reinterpret_cast<const v4f*>(src);
     z1 += *reinterpret_cast<const v4f*>(src + 4);
@@ -401,12 +418,12 @@ hipError_t launch_gemm_bf16(const DenseArgs& g, void* workspace, hipStream_t st)
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.splits == 1) return e;
   const int64_t items = (int64_t)g.M * ((g.N + 7) / 8);
-  const unsigned grid = (unsigned)((items + 255) / 256);
+  const unsigned grid = (unsigned)((items + 63) / 64);
   const int kind = act_kind(g.act);
-  if (g.act == W4A4_ACT_SWIGLU) gemm_bf16_join_kernel<ACT_KIND_SIGMOID, true><<<grid, 256, 0, st>>>(p);
-  else if (kind == ACT_KIND_SIGMOID) gemm_bf16_join_kernel<ACT_KIND_SIGMOID, false><<<grid, 256, 0, st>>>(p);
-  else if (kind == ACT_KIND_ERF) gemm_bf16_join_kernel<ACT_KIND_ERF, false><<<grid, 256, 0, st>>>(p);
-  else gemm_bf16_join_kernel<ACT_KIND_PLAIN, false><<<grid, 256, 0, st>>>(p);
+  if (g.act == W4A4_ACT_SWIGLU) gemm_bf16_join_kernel<ACT_KIND_SIGMOID, true><<<grid, 64, 0, st>>>(p);
+  else if (kind == ACT_KIND_SIGMOID) gemm_bf16_join_kernel<ACT_KIND_SIGMOID, false><<<grid, 64, 0, st>>>(p);
+  else if (kind == ACT_KIND_ERF) gemm_bf16_join_kernel<ACT_KIND_ERF, false><<<grid, 64, 0, st>>>(p);
+  else gemm_bf16_join_kernel<ACT_KIND_PLAIN, false><<<grid, 64, 0, st>>>(p);
   return hipGetLastError();
 }
 
