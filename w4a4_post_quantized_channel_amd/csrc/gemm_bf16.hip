@@ -30,84 +30,102 @@ __device__ __forceinline__ int swz128(int row) {
   return ((row >> 1) & 1) ^ (row & 4) ^ (((row >> 3) & 1) * 6);
 }
 
-// Eight adjacent outputs of row m from column n: z (and for SwiGLU the up
-// projection's u) plus bias, activation, residual, one rounding, store.
-// vec: 16-byte accesses to y and the residual are aligned.
-template <int KIND, bool GATED>
-__device__ __forceinline__ void finish8(const DenseArgs& g, float (&z)[8], const float (&u)[8], int m, int n, bool vec) {
-  if (m >= g.M || n >= g.N) return;
-  const bool whole = n + 8 <= g.N;
-  const int cnt = min(8, g.N - n);
-  float res[8];
+// Eight adjacent columns of an output row, from column n.  Bias and residual
+// are read ahead of the sums they are added to.
+struct Bias8 {
+  float b[8], up[8];   // up: SwiGLU's second factor
+};
+template <bool GATED>
+__device__ __forceinline__ Bias8 load_bias8(const DenseArgs& g, int n) {
+  Bias8 r;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) res[e] = 0.f;
-  const int64_t ro = m * g.ldr + n, yo = m * g.ldy + n;
-  if (g.residual) {
-    if (g.y_bf16) {
-      const uint16_t* r = (const uint16_t*)g.residual + ro;
-      if (whole && vec) {
-        const uint4 v = *reinterpret_cast<const uint4*>(r);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) res[e] = e & 1 ? __uint_as_float(w[e >> 1] & 0xFFFF0000u) : __uint_as_float(w[e >> 1] << 16);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < cnt) res[e] = bf16_bits_to_f32(r[e]);
-      }
+  for (int e = 0; e < 8; ++e) {
+    const int i = min(n + e, g.N - 1);   // past the end: read but not used
+    r.b[e] = r.up[e] = 0.f;
+    if (!g.bias) continue;
+    if (g.bias_bf16) {
+      r.b[e] = bf16_bits_to_f32(((const uint16_t*)g.bias)[i]);
+      if (GATED) r.up[e] = bf16_bits_to_f32(((const uint16_t*)g.bias)[g.N + i]);
     } else {
-      const float* r = (const float*)g.residual + ro;
-      if (whole && vec) {
-        const v4f a = *reinterpret_cast<const v4f*>(r), b = *reinterpret_cast<const v4f*>(r + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) res[e] = a[e], res[e + 4] = b[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < cnt) res[e] = r[e];
-      }
+      r.b[e] = ((const float*)g.bias)[i];
+      if (GATED) r.up[e] = ((const float*)g.bias)[g.N + i];
     }
   }
-  auto bias = [&](int i) {
-    return g.bias_bf16 ? bf16_bits_to_f32(((const uint16_t*)g.bias)[i]) : ((const float*)g.bias)[i];
-  };
-  float b[8], bu[8];
+  return r;
+}
+
+// Residual of a chunk as its bits (bf16: four words, fp32: eight).
+// vec: 16-byte accesses to y and the residual are aligned.
+struct Res8 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Res8 load_res8(const DenseArgs& g, int m, int n, bool vec) {
+  Res8 r;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    b[e] = g.bias && e < cnt ? bias(n + e) : 0.f;
-    bu[e] = GATED && g.bias && e < cnt ? bias(g.N + n + e) : 0.f;
+  for (int e = 0; e < 8; ++e) r.w[e] = 0;
+  if (!g.residual || m >= g.M || n >= g.N) return r;
+  const int64_t at = m * g.ldr + n;
+  if (n + 8 <= g.N && vec) {
+    const uint4* p = reinterpret_cast<const uint4*>((const char*)g.residual + at * (g.y_bf16 ? 2 : 4));
+    const uint4 a = p[0];
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+    if (!g.y_bf16) {
+      const uint4 b = p[1];
+      r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (n + e < g.N) {
+        if (g.y_bf16) r.w[e >> 1] |= (uint32_t)((const uint16_t*)g.residual)[at + e] << (16 * (e & 1));
+        else r.w[e] = ((const uint32_t*)g.residual)[at + e];
+      }
   }
+  return r;
+}
+
+// act(z + bias) + residual (SwiGLU: silu(z + bias) (u + bias) + residual),
+// one rounding, store.
+template <int KIND, bool GATED>
+__device__ __forceinline__ void finish8(const DenseArgs& g, float (&z)[8], const float (&u)[8], const Bias8& b,
+                                        const Res8& res, int m, int n, bool vec) {
+  if (m >= g.M || n >= g.N) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    float v = z[e] + b[e];
-    if constexpr (GATED) v = times_sigmoid(v, v) * (u[e] + bu[e]);
+    float v = z[e] + b.b[e];
+    if constexpr (GATED) v = times_sigmoid(v, v) * (u[e] + b.up[e]);
     else v = activate_kind<KIND>(v, g.act);
-    z[e] = v + res[e];
+    const float r = !g.y_bf16 ? __uint_as_float(res.w[e])
+                              : __uint_as_float(e & 1 ? res.w[e >> 1] & 0xFFFF0000u : res.w[e >> 1] << 16);
+    z[e] = v + r;
   }
+  const bool whole = n + 8 <= g.N && vec;
+  const int64_t yo = m * g.ldy + n;
+  // non-temporal: the output is not read again here
   if (g.y_bf16) {
     uint16_t* y = (uint16_t*)g.y + yo;
-    uint32_t w[4];
+    v4i w;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       typedef float v2f __attribute__((ext_vector_type(2)));
-      w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){z[2 * e], z[2 * e + 1]}, v2bf));
+      w[e] = __builtin_bit_cast(int, __builtin_convertvector((v2f){z[2 * e], z[2 * e + 1]}, v2bf));
     }
-    if (whole && vec) {
-      *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (whole) {
+      __builtin_nontemporal_store(w, reinterpret_cast<v4i*>(y));
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < cnt) y[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        if (n + e < g.N) y[e] = (uint16_t)((uint32_t)w[e >> 1] >> (16 * (e & 1)));
     }
   } else {
     float* y = (float*)g.y + yo;
-    if (whole && vec) {
-      *reinterpret_cast<v4f*>(y) = (v4f){z[0], z[1], z[2], z[3]};
-      *reinterpret_cast<v4f*>(y + 4) = (v4f){z[4], z[5], z[6], z[7]};
+    if (whole) {
+      __builtin_nontemporal_store((v4f){z[0], z[1], z[2], z[3]}, reinterpret_cast<v4f*>(y));
+      __builtin_nontemporal_store((v4f){z[4], z[5], z[6], z[7]}, reinterpret_cast<v4f*>(y) + 1);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < cnt) y[e] = z[e];
+        if (n + e < g.N) y[e] = z[e];
     }
   }
 }
@@ -273,33 +291,42 @@ gemm_bf16_kernel(GemmPlanArgs p) {
     }
     return;
   }
+  // Epilogue: 16 rows at a time through this wave's slice of LDS.  A lane
+  // keeps its 8 columns, so that bias is read once; OC lanes share a row.
   const bool vec = vec_ok(g);
   float* buf = reinterpret_cast<float*>(smem) + wave * 16 * C::PITCH;
-  constexpr int OC = (GATED ? TJ / 2 : TJ) * 2;   // 8-column chunks of an output row of this wave
-  const int nb = n0 + (GATED ? wn / 2 : wn);
+  constexpr int OC = (GATED ? TJ / 2 : TJ) * 2;      // 8-column chunks of a row
+  constexpr int RPP = 64 / OC, PASSES = (16 + RPP - 1) / RPP;
+  const int ch = lane % OC, prow = lane / OC;
+  const int n = n0 + (GATED ? wn / 2 : wn) + ch * 8;
+  const float* src = buf + (GATED ? (ch >> 1) * 32 + (ch & 1) * 8 : ch * 8);
+  const Bias8 bias = load_bias8<GATED>(g, n);
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
+    const int mb = m0 + wm + i * 16;
+    Res8 res[PASSES];
+#pragma unroll
+    for (int q = 0; q < PASSES; ++q) res[q] = load_res8(g, prow < RPP && prow + q * RPP < 16 ? mb + prow + q * RPP : g.M, n, vec);
 #pragma unroll
     for (int j = 0; j < TJ; ++j) *reinterpret_cast<v4f*>(buf + lr * C::PITCH + j * 16 + lq * 4) = acc[i][j];
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int c0 = 0; c0 < 16 * OC; c0 += 64) {
-      const int c = c0 + lane;
-      if (16 * OC % 64 != 0 && c >= 16 * OC) continue;
-      const int row = c / OC, ch = c % OC;
-      const float* src = buf + row * C::PITCH + (GATED ? (ch >> 1) * 32 + (ch & 1) * 8 : ch * 8);
-      float z[8], u[8];
+    for (int q = 0; q < PASSES; ++q) {
+      const int row = prow + q * RPP;
+      if (prow < RPP && row < 16) {
+        float z[8], u[8];
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const v4f v = *reinterpret_cast<const v4f*>(src + e);
-        const v4f w = GATED ? *reinterpret_cast<const v4f*>(src + 16 + e) : v4f{0, 0, 0, 0};
+        for (int e = 0; e < 8; e += 4) {
+          const v4f v = *reinterpret_cast<const v4f*>(src + row * C::PITCH + e);
+          const v4f w = GATED ? *reinterpret_cast<const v4f*>(src + row * C::PITCH + 16 + e) : v4f{0, 0, 0, 0};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) z[e + q] = v[q], u[e + q] = w[q];
+          for (int x = 0; x < 4; ++x) z[e + x] = v[x], u[e + x] = w[x];
+        }
+        finish8<KIND, GATED>(g, z, u, bias, res[q], mb + row, n, vec);
       }
-      finish8<KIND, GATED>(g, z, u, m0 + wm + i * 16 + row, nb + ch * 8, vec);
-      __builtin_amdgcn_sched_barrier(0);   // one chunk's registers at a time
     }
     __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_sched_barrier(0);   // one row block's registers at a time
   }
 }
 
@@ -328,7 +355,7 @@ __global__ void __launch_bounds__(64) gemm_bf16_join_kernel(GemmPlanArgs p) {
   float z[8], u[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) z[e] = z0[e], z[e + 4] = z1[e], u[e] = u0[e], u[e + 4] = u1[e];
-  finish8<KIND, GATED>(g, z, u, m, n, vec_ok(g));
+  finish8<KIND, GATED>(g, z, u, load_bias8<GATED>(g, n), load_res8(g, m, n, vec_ok(g)), m, n, vec_ok(g));
 }
 
 // Tiles, largest first.
@@ -340,13 +367,13 @@ using T64x128 = GCfg<2, 2, 2, 4, 5>;
 using T32x128 = GCfg<2, 2, 1, 4, 6>;
 using T16x128 = GCfg<1, 2, 1, 4, 6>;
 struct TileInfo {
-  int bm, bn, wgs;   // wgs: workgroups a CU holds
-  double us;         // measured time of a stage of one workgroup on a busy card
+  int bm, bn;
+  double us;   // measured time of a K stage, every CU busy with one workgroup
   bool gated;
 };
-constexpr TileInfo kTiles[] = {{256, 320, 1, 1.9, false}, {256, 256, 1, 1.55, true}, {128, 256, 1, 0.85, true},
-                               {128, 128, 1, 0.55, true}, {64, 128, 1, 0.40, true},  {32, 128, 1, 0.30, true},
-                               {16, 128, 1, 0.28, true}};
+constexpr TileInfo kTiles[] = {{256, 320, 1.95, false}, {256, 256, 1.4, true}, {128, 256, 0.82, true},
+                               {128, 128, 0.53, true},  {64, 128, 0.40, true}, {32, 128, 0.30, true},
+                               {16, 128, 0.28, true}};
 constexpr int kNumTiles = 7, kCUs = 256;
 
 struct GemmPlan {
@@ -367,7 +394,7 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int act, bool split) {
       if (sp > 1 && (!split || tiles * sp > 2 * kCUs || stages / sp < 2)) break;
       const int64_t rounds = (tiles * sp + kCUs - 1) / kCUs;
       double cost = rounds * ((stages + sp - 1) / sp * ti.us + 1.5 + ti.bm * ti.bn * 4e-5);
-      if (sp > 1) cost += 3.0 + 2.0 * sp * M * tn * ti.bn * 4.0 / 4e6;
+      if (sp > 1) cost += 3.0 + 0.1 * sp + 2.0 * sp * M * tn * ti.bn * 4.0 / 4e6;
       if (cost < best_cost) {
         best_cost = cost;
         best = {i, (int)tm, (int)tn, (int)sp, (int)(tn * ti.bn)};

@@ -53,6 +53,23 @@ __device__ __forceinline__ Moments join_lanes(Moments m, int L) {
   return m;
 }
 
+// Moments first, first + step, ... of `slabs`, `stride` apart; eight loads in flight.
+__device__ __forceinline__ Moments join_slabs(const Moments* ws, int slabs, int stride, int first, int step) {
+  Moments m = {0.f, 0.f, 0.f};
+  for (int i = first; i < slabs; i += 8 * step) {
+    Moments x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[k] = ws[(int64_t)min(i + k * step, slabs - 1) * stride];
+      if (i + k * step >= slabs) x[k].n = 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (x[k].n > 0.f) m = join(m, x[k]);
+  }
+  return m;
+}
+
 // Lanes for each of `items` results of a workgroup.
 __device__ __forceinline__ int lanes_per(int items) {
   int L = 1;
@@ -68,6 +85,14 @@ template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
   T v[V];
 };
+
+// Output that nothing here reads again: a non-temporal store leaves the
+// features in the caches.
+template <typename T, int V>
+__device__ __forceinline__ void store_once(const Vec<T, V>& r, T* to) {
+  if constexpr (sizeof(r) == 16) __builtin_nontemporal_store(__builtin_bit_cast(v4i, r), reinterpret_cast<v4i*>(to));
+  else *reinterpret_cast<Vec<T, V>*>(to) = r;
+}
 
 __device__ __forceinline__ float to_f32(uint16_t b) { return bf16_bits_to_f32(b); }
 __device__ __forceinline__ float to_f32(float f) { return f; }
@@ -165,7 +190,7 @@ __device__ __forceinline__ void apply(const NormArgs& g, const T* x, T* y, int64
 #pragma unroll
     for (int e = 0; e < V; ++e)
       from_f32(r.v[e], activate_for(T(), __builtin_fmaf(to_f32(u.v[e]) - mu[e], k[e], b[e]), g.act));
-    *reinterpret_cast<Vec<T, V>*>(to) = r;
+    store_once<T, V>(r, to);
   };
   for (; left >= 4; left -= 4, p += 4 * xs, o += 4 * ys) {   // in place: all four are read before any is written
     Vec<T, V> u[4];
@@ -197,13 +222,16 @@ __global__ void __launch_bounds__(kThreads) norm_moments_kernel(NormArgs g, Spli
 }
 
 // (mean, 1 / deviation) of a (sample, group) from its slabs.
-__global__ void __launch_bounds__(64) norm_join_kernel(NormArgs g, int slabs, const Moments* ws, float2* stat) {
+__global__ void __launch_bounds__(kThreads) norm_join_kernel(NormArgs g, int slabs, const Moments* ws, float2* stat) {
+  __shared__ Moments part[kThreads / 64];
   const int64_t n = blockIdx.x / g.groups;
   const int grp = blockIdx.x % g.groups;
-  Moments m = {0.f, 0.f, 0.f};
-  for (int i = threadIdx.x; i < slabs; i += 64) m = join(m, ws[(n * slabs + i) * g.groups + grp]);
-  m = join_lanes(m, 64);
-  if (threadIdx.x == 0) stat[blockIdx.x] = mean_rstd(m, g.eps);
+  Moments m = join_lanes(join_slabs(ws + n * slabs * g.groups + grp, slabs, g.groups, threadIdx.x, kThreads), 64);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < kThreads / 64; ++w) m = join(m, part[w]);
+  stat[blockIdx.x] = mean_rstd(m, g.eps);
 }
 
 // The output of a slab; stat null: the slabs' moments are joined here.
@@ -218,8 +246,7 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(NormArgs g, Split 
   } else {
     const int L = lanes_per(ng);
     for (int i = threadIdx.x / L; i < ng; i += kThreads / L) {
-      Moments m = {0.f, 0.f, 0.f};
-      for (int k = threadIdx.x % L; k < sp.slabs; k += L) m = join(m, ws[(n * sp.slabs + k) * g.groups + g0 + i]);
+      Moments m = join_slabs(ws + n * sp.slabs * g.groups + g0 + i, sp.slabs, g.groups, threadIdx.x % L, L);
       m = join_lanes(m, L);
       if (threadIdx.x % L == 0) st[i] = mean_rstd(m, g.eps);
     }
@@ -322,7 +349,7 @@ hipError_t run(const NormArgs& g, void* workspace, hipStream_t st) {
   const dim3 grid(sp.slabs, sp.blocks, (unsigned)g.N);
   norm_moments_kernel<T, V><<<grid, kThreads, 0, st>>>(g, sp, mom);
   const bool inline_join = sp.slabs <= kJoinInline;
-  if (!inline_join) norm_join_kernel<<<(unsigned)(g.N * g.groups), 64, 0, st>>>(g, sp.slabs, mom, stat);
+  if (!inline_join) norm_join_kernel<<<(unsigned)(g.N * g.groups), kThreads, 0, st>>>(g, sp.slabs, mom, stat);
   norm_apply_kernel<T, V><<<grid, kThreads, 0, st>>>(g, sp, mom, inline_join ? nullptr : stat);
   return hipGetLastError();
 }
