@@ -100,12 +100,14 @@ __device__ __forceinline__ void from_f32(uint16_t& o, float f) { o = __builtin_b
 __device__ __forceinline__ void from_f32(float& o, float f) { o = f; }
 
 // SiLU on the way to bf16 takes the hardware exp2 (a few parts in 10^6,
-// against 2^-9 of the output); fp32 output takes expf.
-__device__ __forceinline__ float activate_for(uint16_t, float z, int act) {
-  if (act == W4A4_ACT_SILU) return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
-  return activate(z, act);
+// against 2^-8 of the output).
+template <typename T, int KIND>
+__device__ __forceinline__ float activate_for(float z, int act) {
+  if constexpr (sizeof(T) == 2 && KIND == ACT_KIND_SIGMOID) {
+    if (act == W4A4_ACT_SILU) return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+  }
+  return activate_kind<KIND>(z, act);
 }
-__device__ __forceinline__ float activate_for(float, float z, int act) { return activate(z, act); }
 
 // How a sample is cut.  A workgroup covers `gpb` whole groups, `cols` threads
 // across their channels and kThreads / cols positions deep.
@@ -170,37 +172,61 @@ __device__ __forceinline__ void channel_moments(const NormArgs& g, const T* x, i
   __syncthreads();
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void apply(const NormArgs& g, const T* x, T* y, int64_t s0, int64_t s1, int c, int cols,
-                                      const float (&mu)[V], const float (&rs)[V]) {
-  const int rows = kThreads / cols, depth = threadIdx.x / cols;
-  if (depth >= rows || s0 + depth >= s1) return;
-  float k[V], b[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    k[e] = rs[e] * (g.weight ? g.weight[c + e] : 1.f);
-    b[e] = g.bias ? g.bias[c + e] : 0.f;
+// The output of a thread's channels over positions [s0, s1): kBatch rows are
+// loaded while the kBatch before them are worked on; the first ones when the
+// object is made, ahead of the statistics.
+template <typename T, int V, int KIND>
+struct Applier {
+  static constexpr int kBatch = 4;
+  const T* p;
+  T* o;
+  int64_t xs, ys, left;
+  Vec<T, V> u[kBatch];
+
+  __device__ __forceinline__ Applier(const NormArgs& g, int64_t n, int64_t s0, int64_t s1, int c, int cols, bool on) {
+    const int rows = kThreads / cols, depth = threadIdx.x / cols;
+    left = on && depth < rows && s0 + depth < s1 ? (s1 - s0 - depth + rows - 1) / rows : 0;
+    xs = (int64_t)rows * g.x_ss;
+    ys = (int64_t)rows * g.y_ss;
+    p = (const T*)g.x + n * g.x_sn + (s0 + depth) * g.x_ss + c;
+    o = (T*)g.y + n * g.y_sn + (s0 + depth) * g.y_ss + c;
+    load(u);
   }
-  const int64_t xs = (int64_t)rows * g.x_ss, ys = (int64_t)rows * g.y_ss;
-  const T* p = x + (s0 + depth) * g.x_ss + c;
-  T* o = y + (s0 + depth) * g.y_ss + c;
-  int64_t left = (s1 - s0 - depth + rows - 1) / rows;
-  auto one = [&](const Vec<T, V>& u, T* to) {
-    Vec<T, V> r;
+  __device__ __forceinline__ void load(Vec<T, V> (&to)[kBatch]) {   // the kBatch rows at p
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      from_f32(r.v[e], activate_for(T(), __builtin_fmaf(to_f32(u.v[e]) - mu[e], k[e], b[e]), g.act));
-    store_once<T, V>(r, to);
-  };
-  for (; left >= 4; left -= 4, p += 4 * xs, o += 4 * ys) {   // in place: all four are read before any is written
-    Vec<T, V> u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const Vec<T, V>*>(p + i * xs);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) one(u[i], o + i * ys);
+    for (int i = 0; i < kBatch; ++i)
+      if (i < left) to[i] = *reinterpret_cast<const Vec<T, V>*>(p + i * xs);
   }
-  for (; left > 0; --left, p += xs, o += ys) one(*reinterpret_cast<const Vec<T, V>*>(p), o);
-}
+  __device__ __forceinline__ void run(const NormArgs& g, int c, const float (&mu)[V], const float (&rs)[V]) {
+    if (left <= 0) return;
+    float k[V], b[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      k[e] = rs[e] * (g.weight ? g.weight[c + e] : 1.f);
+      b[e] = g.bias ? g.bias[c + e] : 0.f;
+    }
+    while (true) {
+      Vec<T, V> next[kBatch];
+      const int64_t had = left;
+      left -= kBatch;
+      p += kBatch * xs;
+      load(next);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (i < had) {
+          Vec<T, V> r;
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            from_f32(r.v[e], activate_for<T, KIND>(__builtin_fmaf(to_f32(u[i].v[e]) - mu[e], k[e], b[e]), g.act));
+          store_once<T, V>(r, o + i * ys);
+        }
+      o += kBatch * ys;
+      if (left <= 0) return;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) u[i] = next[i];
+    }
+  }
+};
 
 // Moments of (sample, slab, group).
 template <typename T, int V>
@@ -235,12 +261,16 @@ __global__ void __launch_bounds__(kThreads) norm_join_kernel(NormArgs g, int sla
 }
 
 // The output of a slab; stat null: the slabs' moments are joined here.
-template <typename T, int V>
+template <typename T, int V, int KIND>
 __global__ void __launch_bounds__(kThreads) norm_apply_kernel(NormArgs g, Split sp, const Moments* ws, const float2* stat) {
   __shared__ float2 st[kThreads * V];
   const int cg = g.C / g.groups;
   const int g0 = blockIdx.y * sp.gpb, ng = min(sp.gpb, g.groups - g0);
   const int64_t n = blockIdx.z;
+  const int cl = (threadIdx.x % sp.cols) * V;   // channel within the block
+  // slabs last to first: what the moments kernel read last is still cached
+  const int64_t s0 = (sp.slabs - 1 - (int)blockIdx.x) * sp.len, s1 = min(g.S, s0 + sp.len);
+  Applier<T, V, KIND> out(g, n, s0, s1, g0 * cg + cl, sp.cols, cl < ng * cg);
   if (stat) {
     for (int i = threadIdx.x; i < ng; i += kThreads) st[i] = stat[n * g.groups + g0 + i];
   } else {
@@ -252,7 +282,6 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(NormArgs g, Split 
     }
   }
   __syncthreads();
-  const int cl = (threadIdx.x % sp.cols) * V;   // channel within the block
   if (cl >= ng * cg) return;
   float mu[V], rs[V];
 #pragma unroll
@@ -261,14 +290,12 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(NormArgs g, Split 
     mu[e] = v.x;
     rs[e] = v.y;
   }
-  // slabs last to first: what the moments kernel read last is still cached
-  const int64_t s0 = (sp.slabs - 1 - (int)blockIdx.x) * sp.len, s1 = min(g.S, s0 + sp.len);
-  apply<T, V>(g, (const T*)g.x + n * g.x_sn, (T*)g.y + n * g.y_sn, s0, s1, g0 * cg + cl, sp.cols, mu, rs);
+  out.run(g, g0 * cg + cl, mu, rs);
 }
 
 // A run of whole groups of one sample, statistics and output.  A group wider
 // than the workgroup (run == 1 then) is taken in chunks of its channels.
-template <typename T, int V>
+template <typename T, int V, int KIND>
 __global__ void __launch_bounds__(kThreads) norm_whole_kernel(NormArgs g, int gpb, int cols) {
   __shared__ Moments mom[kThreads * V];
   __shared__ float2 st[kThreads * V];
@@ -277,7 +304,6 @@ __global__ void __launch_bounds__(kThreads) norm_whole_kernel(NormArgs g, int gp
   const int g0 = blockIdx.x * gpb, ng = min(gpb, g.groups - g0);
   const int c0 = g0 * cg, cend = c0 + ng * cg, width = cols * V;
   const T* x = (const T*)g.x + n * g.x_sn;
-  T* y = (T*)g.y + n * g.y_sn;
   const int L = lanes_per(ng);
   Moments tot = {0.f, 0.f, 0.f};
   for (int cc = c0; cc < cend; cc += width) {
@@ -304,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) norm_whole_kernel(NormArgs g, int gp
       mu[e] = v.x;
       rs[e] = v.y;
     }
-    apply<T, V>(g, x, y, 0, g.S, c, cols, mu, rs);
+    Applier<T, V, KIND>(g, n, 0, g.S, c, cols, true).run(g, c, mu, rs);
   }
 }
 
@@ -322,8 +348,8 @@ int slabs_for(int64_t N, int64_t S, int64_t C, int64_t groups) {
 
 size_t stat_bytes(int64_t N, int64_t groups) { return (size_t)(N * groups * 8 + 255) / 256 * 256; }
 
-template <typename T, int V>
-hipError_t run(const NormArgs& g, void* workspace, hipStream_t st) {
+template <typename T, int V, int KIND>
+hipError_t run_kind(const NormArgs& g, void* workspace, hipStream_t st) {
   const int cg = g.C / g.groups;
   const int slabs = slabs_for(g.N, g.S, g.C, g.groups);
   // whole groups a workgroup can cover; vectors may straddle groups only
@@ -335,7 +361,7 @@ hipError_t run(const NormArgs& g, void* workspace, hipStream_t st) {
     if (cg % V == 0)
       while (gpb > 1 && gpb * cg > 16 * V) gpb = (gpb + 1) / 2;
     const int w = (gpb * cg + V - 1) / V, cols = w < kThreads ? w : kThreads;
-    norm_whole_kernel<T, V><<<dim3((g.groups + gpb - 1) / gpb, (unsigned)g.N), kThreads, 0, st>>>(g, gpb, cols);
+    norm_whole_kernel<T, V, KIND><<<dim3((g.groups + gpb - 1) / gpb, (unsigned)g.N), kThreads, 0, st>>>(g, gpb, cols);
     return hipGetLastError();
   }
   Split sp;
@@ -350,8 +376,17 @@ hipError_t run(const NormArgs& g, void* workspace, hipStream_t st) {
   norm_moments_kernel<T, V><<<grid, kThreads, 0, st>>>(g, sp, mom);
   const bool inline_join = sp.slabs <= kJoinInline;
   if (!inline_join) norm_join_kernel<<<(unsigned)(g.N * g.groups), kThreads, 0, st>>>(g, sp.slabs, mom, stat);
-  norm_apply_kernel<T, V><<<grid, kThreads, 0, st>>>(g, sp, mom, inline_join ? nullptr : stat);
+  norm_apply_kernel<T, V, KIND><<<grid, kThreads, 0, st>>>(g, sp, mom, inline_join ? nullptr : stat);
   return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t run(const NormArgs& g, void* workspace, hipStream_t st) {
+  switch (act_kind(g.act)) {
+    case ACT_KIND_PLAIN: return run_kind<T, V, ACT_KIND_PLAIN>(g, workspace, st);
+    case ACT_KIND_ERF: return run_kind<T, V, ACT_KIND_ERF>(g, workspace, st);
+    default: return run_kind<T, V, ACT_KIND_SIGMOID>(g, workspace, st);
+  }
 }
 
 }  // namespace
