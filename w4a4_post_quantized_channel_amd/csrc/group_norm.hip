@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxSlabs = 2048;
-constexpr int kJoinInline = 96;    // slabs the output kernel joins by itself
+constexpr int kJoinInline = 64;    // slabs the output kernel joins by itself
 constexpr int64_t kSlabElems = 8192;
 
 struct Moments {
@@ -177,37 +177,42 @@ __device__ __forceinline__ void channel_moments(const NormArgs& g, const T* x, i
 // object is made, ahead of the statistics.
 template <typename T, int V, int KIND>
 struct Applier {
-  static constexpr int kBatch = 4;
+  static constexpr int kBatch = 8;
   const T* p;
   T* o;
-  int64_t xs, ys, left;
+  int64_t xs, ys;
+  int left;
   Vec<T, V> u[kBatch];
+  float w[V], b[V];
 
   __device__ __forceinline__ Applier(const NormArgs& g, int64_t n, int64_t s0, int64_t s1, int c, int cols, bool on) {
     const int rows = kThreads / cols, depth = threadIdx.x / cols;
-    left = on && depth < rows && s0 + depth < s1 ? (s1 - s0 - depth + rows - 1) / rows : 0;
+    // a slab's positions fit 32 bits (the entry point refuses more)
+    left = on && depth < rows && s0 + depth < s1 ? (int)((uint32_t)(s1 - s0 - depth + rows - 1) / (uint32_t)rows) : 0;
     xs = (int64_t)rows * g.x_ss;
     ys = (int64_t)rows * g.y_ss;
     p = (const T*)g.x + n * g.x_sn + (s0 + depth) * g.x_ss + c;
     o = (T*)g.y + n * g.y_sn + (s0 + depth) * g.y_ss + c;
     load(u);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      w[e] = g.weight && on ? g.weight[c + e] : 1.f;
+      b[e] = g.bias && on ? g.bias[c + e] : 0.f;
+    }
   }
   __device__ __forceinline__ void load(Vec<T, V> (&to)[kBatch]) {   // the kBatch rows at p
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
       if (i < left) to[i] = *reinterpret_cast<const Vec<T, V>*>(p + i * xs);
   }
-  __device__ __forceinline__ void run(const NormArgs& g, int c, const float (&mu)[V], const float (&rs)[V]) {
+  __device__ __forceinline__ void run(const NormArgs& g, const float (&mu)[V], const float (&rs)[V]) {
     if (left <= 0) return;
-    float k[V], b[V];
+    float k[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      k[e] = rs[e] * (g.weight ? g.weight[c + e] : 1.f);
-      b[e] = g.bias ? g.bias[c + e] : 0.f;
-    }
+    for (int e = 0; e < V; ++e) k[e] = rs[e] * w[e];
     while (true) {
       Vec<T, V> next[kBatch];
-      const int64_t had = left;
+      const int had = left;
       left -= kBatch;
       p += kBatch * xs;
       load(next);
@@ -290,7 +295,7 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(NormArgs g, Split 
     mu[e] = v.x;
     rs[e] = v.y;
   }
-  out.run(g, g0 * cg + cl, mu, rs);
+  out.run(g, mu, rs);
 }
 
 // A run of whole groups of one sample, statistics and output.  A group wider
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) norm_whole_kernel(NormArgs g, int gp
       mu[e] = v.x;
       rs[e] = v.y;
     }
-    Applier<T, V, KIND>(g, n, 0, g.S, c, cols, true).run(g, c, mu, rs);
+    Applier<T, V, KIND>(g, n, 0, g.S, c, cols, true).run(g, mu, rs);
   }
 }
 
@@ -343,6 +348,8 @@ int slabs_for(int64_t N, int64_t S, int64_t C, int64_t groups) {
   int64_t want = kMaxSlabs / N;
   if (want > elems / kSlabElems) want = elems / kSlabElems;
   if (want > S) want = S;
+  // a third launch and more slabs than that gain less than they cost
+  if (want > kJoinInline && want < 4 * kJoinInline) want = kJoinInline;
   return want < 2 ? 1 : (int)want;
 }
 
