@@ -437,7 +437,7 @@ size_t w4a4_workspace_size(int64_t M, int64_t N, int64_t K, int32_t fmt);
  *            out overlaps no input.
  *  own_len   device int32[B], clamped to [0, S]; NULL: S for every sequence.
  *  prefix_keep  device uint8[P], or NULL: all kept.
- * Shape rules: D is 64, 128 or 256; Hq a multiple of Hkv; P, S >= 0 (their
+ * Shape rules: D is 64, 128 or 256; Hq a multiple of Hkv; 0 <= P <= 2^30, 0 <= S <= 2^24 (their
  * pointers may be NULL when 0).  NaN or Inf among a sequence's own values
  * reaches the rows that see them, as NaN or Inf in part or all of the row,
  * and no other row. */
@@ -479,7 +479,7 @@ size_t w4a4_prefix_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t
  *                (same ldr), otherwise y overlaps no input.
  *  y   M x N, F32 or BF16, row stride ldy.
  * The sum, bias, activation and residual are fp32; one rounding to y_dtype.
- * Shape rules: K % 8 == 0, M, N <= 2^30; ldx, ldw % 8 == 0 and
+ * Shape rules: K % 8 == 0, M, N <= 2^30, M N <= 2^40; ldx, ldw % 8 == 0 and
  * <= 2^21 (so K too); ldy, ldr <= 2^22.  x, w 16-byte aligned; bias, residual and y by
  * their element size. */
 enum { W4A4_ACT_NONE = 0, W4A4_ACT_RELU = 1, W4A4_ACT_GELU = 2, W4A4_ACT_GELU_TANH = 3, W4A4_ACT_SILU = 4,

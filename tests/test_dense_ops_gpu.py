@@ -404,3 +404,73 @@ def test_linear_and_norm_repeat_bit_for_bit(ops):
     ws = ops.make_group_norm_workspace(1, 20000, 96, 32)
     a = [ops.group_norm_act(f, 32, workspace=ws).view(torch.int16).cpu() for _ in range(3)]
     assert torch.equal(a[0], a[1]) and torch.equal(a[0], a[2])
+
+
+# ----------------------------------------------------------------------------
+# Shapes large enough for the large tiles, against 64 bits on the GPU
+# ----------------------------------------------------------------------------
+LARGE_ATTN = [
+    # B, T, Hq, Hkv, D, P, S, causal, keep, workspace
+    (16, 64, 32, 8, 128, 4003, 70, True, 0.7, True),
+    (16, 64, 32, 8, 64, 4003, 70, False, None, True),
+    (33, 64, 32, 8, 128, 300, 64, True, None, False),
+    (64, 64, 32, 8, 128, 100, 64, False, 0.5, False),
+    (64, 64, 32, 8, 64, 30, 10, True, None, False),
+    (20, 50, 40, 5, 128, 1000, 50, False, 0.9, True),
+    (8, 64, 16, 4, 256, 700, 64, True, 0.9, True),
+]
+
+
+@pytest.mark.parametrize("case", LARGE_ATTN, ids=[f"B{c[0]}T{c[1]}H{c[2]}-{c[3]}D{c[4]}P{c[5]}S{c[6]}" for c in LARGE_ATTN])
+def test_attention_large_tiles(ops, case):
+    B, T, Hq, Hkv, D, P, S, causal, keep, workspace = case
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B + P)
+    mk = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+    q, kp, vp, ko, vo = mk(B, T, Hq, D), mk(P, Hkv, D), mk(P, Hkv, D), mk(B, S, Hkv, D), mk(B, S, Hkv, D)
+    lens = torch.randint(0, S + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    mask = None if keep is None else torch.rand(P, generator=g, device="cuda") < keep
+    print(f"[attn large] {case}", flush=True)
+    ws = ops.make_prefix_attention_workspace(B, T, Hq, Hkv, D, P, S) if workspace else None
+    out = ops.prefix_attention(q, kp, vp, ko, vo, own_len=lens, prefix_keep=mask, causal=causal, workspace=ws)
+    G, pos, t = Hq // Hkv, torch.arange(S, device="cuda"), torch.arange(T, device="cuda")
+    for b in range(B):
+        k = torch.cat([kp, ko[b]]).double().repeat_interleave(G, 1).permute(1, 2, 0).contiguous()   # Hq, D, keys
+        v = torch.cat([vp, vo[b]]).double().repeat_interleave(G, 1).permute(1, 0, 2).contiguous()
+        qb = q[b].double().permute(1, 0, 2).contiguous()
+        s = torch.matmul(qb, k) / math.sqrt(D)
+        end = lens[b] - T + 1 + t if causal else lens[b].expand(T)
+        hide = torch.zeros(T, P + S, dtype=torch.bool, device="cuda")
+        if mask is not None:
+            hide[:, :P] = ~mask
+        hide[:, P:] = pos >= end.unsqueeze(1)
+        p = torch.nan_to_num(torch.softmax(s.masked_fill(hide, -math.inf), -1))
+        o, mag = torch.matmul(p, v).permute(1, 0, 2), torch.matmul(p, v.abs()).permute(1, 0, 2)
+        sc = (torch.matmul(qb.abs(), k.abs()).amax(-1) / math.sqrt(D)).t().unsqueeze(-1)
+        tol = BF16 * o.abs() + (1.01 * BF16 + 2 * D * F32 * sc + 1e-5) * mag + 1e-30
+        err = (out[b].double() - o).abs()
+        assert bool((err <= tol).all()), (b, float((err - tol).max()), float(err.max()))
+
+
+LARGE_LINEAR = [
+    # M, N, K, act, bias, residual, y_dtype
+    (4090, 5117, 520, "gelu_tanh", torch.float32, True, torch.bfloat16),
+    (4096, 5120, 328, "gelu", torch.bfloat16, True, torch.float32),
+    (2040, 4090, 520, "swiglu", torch.float32, True, torch.bfloat16),
+    (2048, 4096, 520, "relu", None, False, torch.float32),
+    (1000, 4090, 2056, "swiglu", torch.bfloat16, True, torch.float32),
+    (1000, 8200, 2056, "none", torch.float32, True, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("case", LARGE_LINEAR, ids=[f"{c[0]}x{c[1]}x{c[2]}-{c[3]}" for c in LARGE_LINEAR])
+def test_linear_large_tiles(ops, case):
+    M, N, K, act, bias, residual, y_dtype = case
+    x, w, b, r = _linear_inputs(M, N, K, act, bias, residual, y_dtype, seed=M)
+    dev = [None if t is None else t.cuda() for t in (x, w, b, r)]
+    want, tol = _linear_reference(dev[0], dev[1], dev[2], act, dev[3], BF16 if y_dtype == torch.bfloat16 else F32)
+    print(f"[linear large] {case}", flush=True)
+    y = ops.bf16_linear(dev[0], dev[1], bias=dev[2], act=act, residual=dev[3], y_dtype=y_dtype,
+                        workspace=ops.make_bf16_linear_workspace(M, N, K, act))
+    err = (y.double() - want).abs()
+    assert bool((err <= tol).all()), (float((err - tol).max()), float(err.max()))

@@ -50,7 +50,7 @@ int check_attn_sizes(const char* fn, int64_t B, int64_t T, int64_t Hq, int64_t H
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: head width %lld is not 64, 128 or 256", fn, (long long)D);
   if (Hq % Hkv != 0)
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: %lld query heads over %lld KV heads", fn, (long long)Hq, (long long)Hkv);
-  if (Hq > 65536 || P > (1LL << 30) || S > (1LL << 30) || T > (1LL << 24) || B > (1LL << 24) ||
+  if (Hq > 65536 || P > (1LL << 30) || S > (1LL << 24) || T > (1LL << 24) || B > (1LL << 24) ||
       B * T > (1LL << 30) / Hq)
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: sizes too large", fn);
   return ok();
@@ -109,7 +109,7 @@ size_t w4a4_prefix_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t
 static int check_dense_sizes(const char* fn, int64_t M, int64_t N, int64_t K, int32_t act) {
   if (M < 0 || N < 0 || K <= 0) return fail(W4A4_ERR_INVALID_ARG, "%s: bad sizes", fn);
   if (K % 8 != 0) return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: K=%lld not a multiple of 8", fn, (long long)K);
-  if (K > (1LL << 21) || M > (1LL << 30) || N > (1LL << 30))
+  if (K > (1LL << 21) || M > (1LL << 30) || N > (1LL << 30) || (N > 0 && M > (1LL << 40) / N))
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: sizes too large", fn);
   if (act < W4A4_ACT_NONE || act > W4A4_ACT_SWIGLU)
     return fail(W4A4_ERR_UNSUPPORTED_FORMAT, "%s: unknown activation %d", fn, act);

@@ -22,14 +22,22 @@
 //
 // Work split.  A workgroup holds WQ x WK waves: WQ groups of 32 rows, and WK
 // key groups that take every WK-th block and are joined through LDS at the
-// end.  Blocks are copied global -> LDS (16 bytes a lane, XOR-swizzled on the
-// way so that the fragment reads are free of bank conflicts) into NBUF
-// buffers per key group.  The block list of a row tile, prefix blocks then
-// the own blocks of its sequences, is cut into `parts` for shapes with few
-// rows; partial (m, l, o) go to the workspace and a second kernel joins them.
+// end.  A block's K and V go global -> LDS XOR-swizzled, so that the fragment
+// reads are free of bank conflicts (none counted), into NBUF buffers per key
+// group.  The block list of a row tile, prefix blocks then the own blocks of
+// its sequences, is cut into `parts` for shapes with few rows; partial
+// (m, l, o) go to the workspace and a second kernel joins them.
+//
+// What bounds it (one MI355X).  Many rows (16 x 64 queries, 32 heads over 8,
+// width 128, 16384 + 192 keys, 277 GFLOP): 265-284 us, 0.98-1.05 PFLOP/s, 56%
+// of the matrix cycles at the 1.7 GHz the card holds there; a phase takes
+// about 1750 cycles where its 32 products need 1024, the rest being the
+// softmax's vector work, the issue of copies and the barriers.  Few rows: the
+// load path of a CU (43 bytes a cycle measured, all waves loading) and the
+// chain of dependent memory latencies at the start and end of a workgroup.
 #include "dense.h"
 #include "device_common.h"
-#include "lds_dma.h"
+#include "lds_sync.h"
 
 namespace w4a4 {
 

@@ -15,10 +15,19 @@
 //
 // Few output tiles: K is split over workgroups; fp32 partial sums go to the
 // workspace and a second kernel adds them in order and runs the epilogue.
+//
+// What bounds it (one MI355X).  4096 x 5120 x 5120 with bias and GELU: 256
+// tiles of 256 x 320 are one round of the card, 162-180 us (1.2-1.3 PFLOP/s)
+// against 153 us of matrix time at the rate a large library product reaches.
+// A direct copy takes about 100 cycles to issue; with its 9 copies a stage up
+// front the loop ran 200 us, one to a step 192; the epilogue that read bias
+// and residual per chunk cost 36 us of that, the present one under 10.
+// 64 x 2048 x 8192: 14 us, of which the second launch and the partial sums
+// take 5 and the weights' 33.5 MB 6.6 at the copy rate.
 #include "activation.h"
 #include "dense.h"
 #include "device_common.h"
-#include "lds_dma.h"
+#include "lds_sync.h"
 
 namespace w4a4 {
 
@@ -430,7 +439,6 @@ size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int act) {
 }
 
 hipError_t launch_gemm_bf16(const DenseArgs& g, void* workspace, hipStream_t st) {
-
   const GemmPlan pl = plan_gemm(g.M, g.N, g.K, g.act, workspace != nullptr);
   GemmPlanArgs p{g, pl.tiles_m, pl.tiles_n, pl.splits, (g.K + 63) / 64, (float*)workspace, pl.pn};
   switch (pl.tile) {

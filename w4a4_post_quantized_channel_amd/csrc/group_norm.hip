@@ -2,7 +2,10 @@
 //
 // Memory bound: the features are read once for the statistics and once for
 // the output; the second read comes from the 256 MB last-level cache where
-// the features fit it.
+// the features fit it.  1597440 x 96 bf16 (306 MB): 50 us for the moments, 6
+// to join them, 109-119 for the output, against 120 us for one read and one
+// write at the rate of a device copy (5.1 TB/s).  Small inputs (1560 x 384:
+// 13.7 us) are two launches of dependent memory latencies.
 //
 // Statistics.  A thread keeps V adjacent channels and walks down the
 // positions of its slab, so loads are whole lines and a lane's groups are

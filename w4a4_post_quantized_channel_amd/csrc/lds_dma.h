@@ -52,26 +52,10 @@ __device__ __forceinline__ void dma4_at(const v4u& rs, uint32_t lds, uint32_t of
                : "memory", "m0");
 }
 
-// dma16_at without a scalar offset.
-__device__ __forceinline__ void dma16_v(const v4u& rs, uint32_t lds, uint32_t off) {
-  const uint32_t m = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(m), "v"(off), "s"(rs)
-               : "memory", "m0");
-}
-
 // s_waitcnt with vmcnt <= n and no wait on the other counters.
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
-}
-
-// The same with every LDS read of this wave returned too: what a wave needs
-// before a barrier after which others may overwrite what it has read.
-template <int N>
-__device__ __forceinline__ void wait_vmcnt_lds() {
-  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));
 }
 
 }  // namespace w4a4
