@@ -6,6 +6,7 @@ Tolerances come from the arithmetic: the unit roundoff of the output type
 bf16 probabilities, and the worst-case growth of fp32 sums.
 """
 import math
+import random
 
 import pytest
 
@@ -421,17 +422,15 @@ LARGE_ATTN = [
 ]
 
 
-@pytest.mark.parametrize("case", LARGE_ATTN, ids=[f"B{c[0]}T{c[1]}H{c[2]}-{c[3]}D{c[4]}P{c[5]}S{c[6]}" for c in LARGE_ATTN])
-def test_attention_large_tiles(ops, case):
-    B, T, Hq, Hkv, D, P, S, causal, keep, workspace = case
+def _attention_on_gpu(ops, B, T, Hq, Hkv, D, P, S, causal, keep, workspace, seed):
     g = torch.Generator(device="cuda")
-    g.manual_seed(B + P)
+    g.manual_seed(seed)
     mk = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
     q, kp, vp, ko, vo = mk(B, T, Hq, D), mk(P, Hkv, D), mk(P, Hkv, D), mk(B, S, Hkv, D), mk(B, S, Hkv, D)
     lens = torch.randint(0, S + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
     mask = None if keep is None else torch.rand(P, generator=g, device="cuda") < keep
-    print(f"[attn large] {case}", flush=True)
     ws = ops.make_prefix_attention_workspace(B, T, Hq, Hkv, D, P, S) if workspace else None
+    print(f"[attn] {(B, T, Hq, Hkv, D, P, S, causal, keep, workspace, seed)}", flush=True)
     out = ops.prefix_attention(q, kp, vp, ko, vo, own_len=lens, prefix_keep=mask, causal=causal, workspace=ws)
     G, pos, t = Hq // Hkv, torch.arange(S, device="cuda"), torch.arange(T, device="cuda")
     for b in range(B):
@@ -450,6 +449,27 @@ def test_attention_large_tiles(ops, case):
         tol = BF16 * o.abs() + (1.01 * BF16 + 2 * D * F32 * sc + 1e-5) * mag + 1e-30
         err = (out[b].double() - o).abs()
         assert bool((err <= tol).all()), (b, float((err - tol).max()), float(err.max()))
+
+
+@pytest.mark.parametrize("case", LARGE_ATTN, ids=[f"B{c[0]}T{c[1]}H{c[2]}-{c[3]}D{c[4]}P{c[5]}S{c[6]}" for c in LARGE_ATTN])
+def test_attention_large_tiles(ops, case):
+    _attention_on_gpu(ops, *case, seed=case[0] + case[5])
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_attention_random_shapes(ops, seed):
+    """Sizes over the whole range, so that every tile, with and without parts, is met."""
+    r = random.Random(seed)
+    n = 0
+    while n < 12:
+        Hkv = r.choice([1, 2, 4, 5, 8])
+        B, T = int(2 ** r.uniform(0, 6)), r.choice([1, int(2 ** r.uniform(0, 6.2))])
+        Hq, D, P, S = Hkv * r.choice([1, 2, 3, 4, 7, 8]), r.choice([64, 128, 256]), int(2 ** r.uniform(0, 13)), int(2 ** r.uniform(0, 8.3))
+        if B * T * Hq * (P + S) > 4e7:
+            continue
+        _attention_on_gpu(ops, B, T, Hq, Hkv, D, P, S, r.random() < 0.5, r.choice([None, 0.0, 0.5, 0.95]), r.random() < 0.7,
+                          seed=100 * seed + n)
+        n += 1
 
 
 LARGE_LINEAR = [
@@ -474,3 +494,37 @@ def test_linear_large_tiles(ops, case):
                         workspace=ops.make_bf16_linear_workspace(M, N, K, act))
     err = (y.double() - want).abs()
     assert bool((err <= tol).all()), (float((err - tol).max()), float(err.max()))
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_linear_random_shapes(ops, seed):
+    r = random.Random(seed)
+    for n in range(10):
+        M, N, K = int(2 ** r.uniform(0, 11)), int(2 ** r.uniform(0, 12)), 8 * int(2 ** r.uniform(0, 8.5))
+        act = r.choice(["none", "relu", "gelu", "gelu_tanh", "silu", "swiglu"])
+        y_dtype = r.choice([torch.bfloat16, torch.float32])
+        x, w, b, res = _linear_inputs(M, N, K, act, r.choice([None, torch.float32, torch.bfloat16]), r.random() < 0.5, y_dtype,
+                                      100 * seed + n)
+        dev = [None if t is None else t.cuda() for t in (x, w, b, res)]
+        want, tol = _linear_reference(dev[0], dev[1], dev[2], act, dev[3], BF16 if y_dtype == torch.bfloat16 else F32)
+        ws = ops.make_bf16_linear_workspace(M, N, K, act) if r.random() < 0.7 else None
+        print(f"[linear] {M}x{N}x{K} {act} {y_dtype} ws={ws is not None}", flush=True)
+        y = ops.bf16_linear(dev[0], dev[1], bias=dev[2], act=act, residual=dev[3], y_dtype=y_dtype, workspace=ws)
+        err = (y.double() - want).abs()
+        assert bool((err <= tol).all()), (float((err - tol).max()), float(err.max()))
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_group_norm_random_shapes(ops, seed):
+    r = random.Random(seed)
+    for n in range(8):
+        groups = r.choice([1, 2, 3, 8, 32])
+        N, S, C = r.randint(1, 4), int(2 ** r.uniform(0, 14)), groups * r.choice([1, 2, 3, 5, 8, 12, 16, 40])
+        dtype, act = r.choice([torch.bfloat16, torch.float32]), r.choice(["none", "relu", "gelu", "gelu_tanh", "silu"])
+        g = _gen(100 * seed + n)
+        x = (torch.randn(N, S, C, generator=g) + 2 * torch.randn(C, generator=g)).to(dtype)
+        w, b = torch.randn(C, generator=g), torch.randn(C, generator=g)
+        ws = ops.make_group_norm_workspace(N, S, C, groups) if r.random() < 0.7 else None
+        print(f"[norm] {N}x{S}x{C} groups={groups} {act} {dtype} ws={ws is not None}", flush=True)
+        want, tol = _norm_reference(x, groups, w, b, 1e-5, act, BF16 if dtype == torch.bfloat16 else F32)
+        _check(ops.group_norm_act(x.cuda(), groups, w.cuda(), b.cuda(), act=act, workspace=ws), want, tol)
