@@ -339,6 +339,69 @@ gemm_bf16_kernel(GemmPlanArgs p) {
   }
 }
 
+// At most 16 rows (decoding): one launch, no LDS on the way.  A workgroup
+// takes 16 output columns and its eight waves a share of K each, operands
+// straight from global memory (16 bytes a lane, kRowsAhead steps of 32 K in
+// flight); the waves' sums are added in order through LDS.
+constexpr int kRowsMax = 16, kRowsWaves = 8, kRowsAhead = 8;
+
+template <int KIND, bool GATED>
+__global__ void __launch_bounds__(64 * kRowsWaves) gemm_bf16_rows_kernel(DenseArgs g) {
+  constexpr int F = GATED ? 2 : 1, PITCH = 20;
+  __shared__ __attribute__((aligned(16))) float red[F][kRowsWaves][16][PITCH];
+  const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 16;
+  const int steps = (g.K + 31) / 32, per = (steps + kRowsWaves - 1) / kRowsWaves;
+  const int s1 = min(steps, (wave + 1) * per);
+  const bool row_on = lr < g.M, col_on = n0 + lr < g.N;
+  const uint16_t* x = g.x + (int64_t)(row_on ? lr : 0) * g.ldx + lq * 8;
+  const uint16_t* w = g.w + (int64_t)(col_on ? n0 + lr : 0) * g.ldw + lq * 8;
+  const uint16_t* up = w + (int64_t)g.N * g.ldw;
+  const v4i zero = {0, 0, 0, 0};
+  auto chunk = [&](const uint16_t* p, int s, bool on) {
+    on = on && s < s1 && s * 32 + lq * 8 < g.K;
+    return on ? *reinterpret_cast<const v4i*>(p + (int64_t)s * 32) : zero;
+  };
+  v4f acc[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) acc[f] = v4f{0, 0, 0, 0};
+  for (int s = wave * per; s < s1; s += kRowsAhead) {
+    v4i a[kRowsAhead], b[F][kRowsAhead];
+#pragma unroll
+    for (int k = 0; k < kRowsAhead; ++k) {
+      a[k] = chunk(x, s + k, row_on);
+      b[0][k] = chunk(w, s + k, col_on);
+      if constexpr (GATED) b[F - 1][k] = chunk(up, s + k, col_on);
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsAhead; ++k)
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, b[f][k]), __builtin_bit_cast(v8bf, a[k]),
+                                                         acc[f], 0, 0, 0);
+  }
+#pragma unroll
+  for (int f = 0; f < F; ++f) *reinterpret_cast<v4f*>(&red[f][wave][lr][lq * 4]) = acc[f];
+  __syncthreads();
+  const int m = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
+  if (m >= g.M) return;
+  const bool vec = vec_ok(g);
+  const Bias8 bias = load_bias8<GATED>(g, n0 + c);
+  const Res8 res = load_res8(g, m, n0 + c, vec);
+  float z[8], u[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    z[e] = u[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kRowsWaves; ++k) {
+      z[e] += red[0][k][m][c + e];
+      if constexpr (GATED) u[e] += red[F - 1][k][m][c + e];
+    }
+  }
+  finish8<KIND, GATED>(g, z, u, bias, res, m, n0 + c, vec);
+}
+
 // Adds the K splits in order and runs the epilogue: 8 columns a thread.
 template <int KIND, bool GATED>
 __global__ void __launch_bounds__(64) gemm_bf16_join_kernel(GemmPlanArgs p) {
@@ -374,16 +437,14 @@ using T128x256 = GCfg<4, 4, 2, 4, 3>;
 using T128x128 = GCfg<4, 2, 2, 4, 4>;
 using T64x128 = GCfg<2, 2, 2, 4, 5>;
 using T32x128 = GCfg<2, 2, 1, 4, 6>;
-using T16x128 = GCfg<1, 2, 1, 4, 6>;
 struct TileInfo {
   int bm, bn;
   double us;   // measured time of a K stage, every CU busy with one workgroup
   bool gated;
 };
 constexpr TileInfo kTiles[] = {{256, 320, 1.95, false}, {256, 256, 1.4, true}, {128, 256, 0.82, true},
-                               {128, 128, 0.53, true},  {64, 128, 0.40, true}, {32, 128, 0.30, true},
-                               {16, 128, 0.28, true}};
-constexpr int kNumTiles = 7, kCUs = 256;
+                               {128, 128, 0.53, true},  {64, 128, 0.40, true}, {32, 128, 0.30, true}};
+constexpr int kNumTiles = 6, kCUs = 256;
 
 struct GemmPlan {
   int tile, tiles_m, tiles_n, splits, pn;
@@ -433,12 +494,29 @@ void launch_tile(const GemmPlanArgs& p, hipStream_t st) {
 
 }  // namespace
 
+// At most 16 rows: the one-launch kernel while K is short.  Measured against
+// the split tiles (us in a graph, one launch / split): 1 x 2048 x 2048 5.6 /
+// 8.0, 16 x 2048 x 2048 6.9 / 9.2, 1 x 4096 x 4096 8.3 / 10.6; from there on
+// its workgroups are too few for the weights: 1 x 2048 x 8192 12.4 / 11.4,
+// 16 x 2048 x 8192 17.8 / 12.3.
+static bool rows_kernel(int64_t M, int64_t K, bool split) { return M <= kRowsMax && (K <= 4096 || !split); }
+
 size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int act) {
+  if (rows_kernel(M, K, true)) return 0;
   const GemmPlan pl = plan_gemm(M, N, K, act, true);
   return pl.splits > 1 ? (size_t)pl.splits * M * pl.pn * 4 : 0;
 }
 
 hipError_t launch_gemm_bf16(const DenseArgs& g, void* workspace, hipStream_t st) {
+  if (rows_kernel(g.M, g.K, workspace != nullptr)) {
+    const unsigned grid = (unsigned)((g.N + 15) / 16);
+    const int kind = act_kind(g.act), threads = 64 * kRowsWaves;
+    if (g.act == W4A4_ACT_SWIGLU) gemm_bf16_rows_kernel<ACT_KIND_SIGMOID, true><<<grid, threads, 0, st>>>(g);
+    else if (kind == ACT_KIND_SIGMOID) gemm_bf16_rows_kernel<ACT_KIND_SIGMOID, false><<<grid, threads, 0, st>>>(g);
+    else if (kind == ACT_KIND_ERF) gemm_bf16_rows_kernel<ACT_KIND_ERF, false><<<grid, threads, 0, st>>>(g);
+    else gemm_bf16_rows_kernel<ACT_KIND_PLAIN, false><<<grid, threads, 0, st>>>(g);
+    return hipGetLastError();
+  }
   const GemmPlan pl = plan_gemm(g.M, g.N, g.K, g.act, workspace != nullptr);
   GemmPlanArgs p{g, pl.tiles_m, pl.tiles_n, pl.splits, (g.K + 63) / 64, (float*)workspace, pl.pn};
   switch (pl.tile) {
@@ -447,8 +525,7 @@ hipError_t launch_gemm_bf16(const DenseArgs& g, void* workspace, hipStream_t st)
     case 2: launch_tile<T128x256>(p, st); break;
     case 3: launch_tile<T128x128>(p, st); break;
     case 4: launch_tile<T64x128>(p, st); break;
-    case 5: launch_tile<T32x128>(p, st); break;
-    default: launch_tile<T16x128>(p, st); break;
+    default: launch_tile<T32x128>(p, st); break;
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.splits == 1) return e;
