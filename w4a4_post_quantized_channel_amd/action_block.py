@@ -15,12 +15,23 @@ GPU, captures it in a HIP graph and prints its time.
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
 
 from . import ops
 from .pipeline import QuantizedLinear
+
+
+@functools.lru_cache(maxsize=256)
+def _scratch_bytes(B: int, T: int, P: int, dim: int, F: int, Hq: int, Hkv: int, D: int) -> int:
+    """Bytes that cover every 16-bit call of a step (a host query of five plans)."""
+    M = B * T
+    return max(ops.bf16_linear_workspace_size(M, (Hq + 2 * Hkv) * D, dim),
+               ops.prefix_attention_workspace_size(B, T, Hq, Hkv, D, P, T),
+               ops.bf16_linear_workspace_size(M, dim, Hq * D), ops.bf16_linear_workspace_size(M, F, dim, "swiglu"),
+               ops.bf16_linear_workspace_size(M, dim, F))
 
 
 class FeatureTokens:
@@ -31,11 +42,12 @@ class FeatureTokens:
 
     def __call__(self, features: torch.Tensor, stream=None) -> torch.Tensor:
         S, C = features.shape
-        ws = ops.make_group_norm_workspace(1, S, C, self.groups, device=features.device)
-        h = ops.group_norm_act(features.unsqueeze(0), self.groups, self.norm_w, self.norm_b, act="silu", workspace=ws,
-                               stream=stream)[0]
-        ws = ops.make_bf16_linear_workspace(S, self.w.shape[0], C, device=features.device)
-        return ops.bf16_linear(h, self.w, bias=self.b, workspace=ws, stream=stream)
+        with torch.cuda.stream(stream):
+            ws = ops.make_group_norm_workspace(1, S, C, self.groups, device=features.device)
+            h = ops.group_norm_act(features.unsqueeze(0), self.groups, self.norm_w, self.norm_b, act="silu",
+                                   workspace=ws)[0]
+            ws = ops.make_bf16_linear_workspace(S, self.w.shape[0], C, device=features.device)
+            return ops.bf16_linear(h, self.w, bias=self.b, workspace=ws)
 
 
 class ActionBlock:
@@ -44,6 +56,11 @@ class ActionBlock:
     wqkv   [(Hq + 2 Hkv) D, dim] float, packed once as ``fmt`` codes (None: kept as a 16-bit product);
     wkv    [2 Hkv D, dim] bf16, the observation's keys and values;
     wo     [dim, Hq D], bo [dim];  w_gate_up [2 F, dim];  w_down [dim, F] (bf16, bias fp32).
+
+    Each call takes its intermediates, partial sums and result from the
+    allocator on the stream that it runs on (``stream``, or the current one)
+    and keeps none, so calls on several streams, in several threads or in
+    captured graphs may overlap.
     """
 
     def __init__(self, Hq: int, Hkv: int, D: int, wqkv: torch.Tensor, wkv: torch.Tensor, wo: torch.Tensor,
@@ -51,53 +68,50 @@ class ActionBlock:
         self.Hq, self.Hkv, self.D = Hq, Hkv, D
         self.qkv = QuantizedLinear(wqkv.float(), None, None, fmt) if fmt else wqkv.bfloat16()
         self.wkv, self.wo, self.bo, self.w_gate_up, self.w_down = wkv, wo, bo, w_gate_up, w_down
-        self._ws = {}
 
     def _workspaces(self, B: int, T: int, P: int, device):
-        key = (B, T, P, device)
-        if key not in self._ws:
-            dim, F, M = self.wo.shape[0], self.w_down.shape[1], B * T
-            nq = (self.Hq + 2 * self.Hkv) * self.D
-            self._ws[key] = {
-                "qkv": ops.make_bf16_linear_workspace(M, nq, dim, device=device),
-                "attn": ops.make_prefix_attention_workspace(B, T, self.Hq, self.Hkv, self.D, P, T, device=device),
-                "o": ops.make_bf16_linear_workspace(M, dim, self.Hq * self.D, device=device),
-                "gate_up": ops.make_bf16_linear_workspace(M, F, dim, "swiglu", device=device),
-                "down": ops.make_bf16_linear_workspace(M, dim, F, device=device)}
-        return self._ws[key]
+        """One buffer for the step's calls, which follow each other on a stream."""
+        nbytes = _scratch_bytes(B, T, P, self.wo.shape[0], self.w_down.shape[1], self.Hq, self.Hkv, self.D)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        return dict.fromkeys(("qkv", "attn", "o", "gate_up", "down"), ws)
 
     def observe(self, tokens: torch.Tensor, stream=None):
         """Keys and values [P, Hkv, D] of the observation, shared by every sequence and step."""
-        kv = ops.bf16_linear(tokens, self.wkv, stream=stream,
-                             workspace=ops.make_bf16_linear_workspace(tokens.shape[0], self.wkv.shape[0],
-                                                                      tokens.shape[1], device=tokens.device))
+        with torch.cuda.stream(stream):
+            ws = ops.make_bf16_linear_workspace(tokens.shape[0], self.wkv.shape[0], tokens.shape[1],
+                                                device=tokens.device)
+            kv = ops.bf16_linear(tokens, self.wkv, workspace=ws)
         kv = kv.view(-1, 2, self.Hkv, self.D)
         return kv[:, 0], kv[:, 1]
 
-    def _norm(self, x: torch.Tensor, stream) -> torch.Tensor:
+    def _norm(self, x: torch.Tensor) -> torch.Tensor:
         # layer norm of every token: group norm with one group and one position a sample
         M, dim = x.shape
-        return ops.group_norm_act(x.view(M, 1, dim), 1, act="none", stream=stream).view(M, dim)
+        return ops.group_norm_act(x.view(M, 1, dim), 1, act="none").view(M, dim)
 
     def step(self, x: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, keep: Optional[torch.Tensor] = None,
              stream=None) -> torch.Tensor:
         """The block's output for chunks x [B, T, dim] (bf16) that see the kept
         observation tokens and their own chunk."""
+        with torch.cuda.stream(stream):
+            return self._step(x, k_prefix, v_prefix, keep)
+
+    def _step(self, x, k_prefix, v_prefix, keep):
         B, T, dim = x.shape
         Hq, Hkv, D = self.Hq, self.Hkv, self.D
         ws = self._workspaces(B, T, k_prefix.shape[0], x.device)
         x = x.reshape(B * T, dim)
-        h = self._norm(x, stream)
+        h = self._norm(x)
         if isinstance(self.qkv, QuantizedLinear):
-            qkv = self.qkv.forward(h, stream=stream)
+            qkv = self.qkv.with_own_buffers().forward(h)
         else:
-            qkv = ops.bf16_linear(h, self.qkv, workspace=ws["qkv"], stream=stream)
+            qkv = ops.bf16_linear(h, self.qkv, workspace=ws["qkv"])
         qkv = qkv.view(B, T, Hq + 2 * Hkv, D)
         a = ops.prefix_attention(qkv[:, :, :Hq], k_prefix, v_prefix, qkv[:, :, Hq:Hq + Hkv], qkv[:, :, Hq + Hkv:],
-                                 prefix_keep=keep, workspace=ws["attn"], stream=stream)
-        x = ops.bf16_linear(a.view(B * T, Hq * D), self.wo, bias=self.bo, residual=x, workspace=ws["o"], stream=stream)
-        g = ops.bf16_linear(self._norm(x, stream), self.w_gate_up, act="swiglu", workspace=ws["gate_up"], stream=stream)
-        return ops.bf16_linear(g, self.w_down, residual=x, workspace=ws["down"], stream=stream).view(B, T, dim)
+                                 prefix_keep=keep, workspace=ws["attn"])
+        x = ops.bf16_linear(a.view(B * T, Hq * D), self.wo, bias=self.bo, residual=x, workspace=ws["o"])
+        g = ops.bf16_linear(self._norm(x), self.w_gate_up, act="swiglu", workspace=ws["gate_up"])
+        return ops.bf16_linear(g, self.w_down, residual=x, workspace=ws["down"]).view(B, T, dim)
 
 
 def random_block(dim: int, Hq: int, Hkv: int, D: int, F: int, fmt: Optional[str], seed: int = 0, device="cuda"):

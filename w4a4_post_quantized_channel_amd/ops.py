@@ -458,9 +458,13 @@ def _attn_operand(name: str, t: torch.Tensor, shape):
     return st
 
 
+def prefix_attention_workspace_size(B: int, T: int, Hq: int, Hkv: int, D: int, P: int, S: int) -> int:
+    return int(LIB.w4a4_prefix_attention_workspace(B, T, Hq, Hkv, D, P, S))
+
+
 def make_prefix_attention_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, P: int, S: int,
                                     device="cuda") -> Optional[torch.Tensor]:
-    return _ws(int(LIB.w4a4_prefix_attention_workspace(B, T, Hq, Hkv, D, P, S)), device)
+    return _ws(prefix_attention_workspace_size(B, T, Hq, Hkv, D, P, S), device)
 
 
 def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, k_own: torch.Tensor,
@@ -503,8 +507,12 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     return out
 
 
+def bf16_linear_workspace_size(M: int, N: int, K: int, act: str = "none") -> int:
+    return int(LIB.w4a4_bf16_workspace_size(M, N, K, _act_code(act)))
+
+
 def make_bf16_linear_workspace(M: int, N: int, K: int, act: str = "none", device="cuda") -> Optional[torch.Tensor]:
-    return _ws(int(LIB.w4a4_bf16_workspace_size(M, N, K, _act_code(act))), device)
+    return _ws(bf16_linear_workspace_size(M, N, K, act), device)
 
 
 def bf16_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = None, act: str = "none",

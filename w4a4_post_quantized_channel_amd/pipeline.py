@@ -174,6 +174,14 @@ class QuantizedLinear:
         self.project(x, stream)
         return self.gemm(x.shape[0], x.device, out, stream)
 
+    def with_own_buffers(self) -> "QuantizedLinear":
+        """This layer on the same packed weights, with buffers of its own: for a
+        call beside which others (another stream, thread or graph) may run."""
+        r = object.__new__(type(self))   # copy.copy takes several times as long, beside short kernels
+        r.__dict__.update(self.__dict__)
+        r._bufs = {}
+        return r
+
     def replica(self) -> "QuantizedLinear":
         """A layer with the same configuration and its own device copies of the
         packed weights and branch operands (and its own buffers)."""
