@@ -443,6 +443,17 @@ def _ws(nbytes: int, device) -> Optional[torch.Tensor]:
     return None if nbytes == 0 else torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _together(first: torch.Tensor, **others) -> int:
+    """The address of ``first``, with every other operand on its device.  An
+    operand in host memory would fault the kernel: if ``first`` lies there the
+    address is NULL, which the library refuses after its checks of sizes."""
+    device = first.device
+    for name, t in others.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the first operand on {device}")
+    return first.data_ptr() if first.is_cuda else 0
+
+
 def _ws_args(workspace):
     return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
 
@@ -496,8 +507,10 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     if prefix_keep is not None and (prefix_keep.dtype not in (torch.bool, torch.uint8) or prefix_keep.shape != (P,)
                                     or not prefix_keep.is_contiguous()):
         raise TypeError("prefix_keep must be a contiguous bool or uint8 [P] tensor")
+    qp = _together(q, k_prefix=k_prefix, v_prefix=v_prefix, k_own=k_own, v_own=v_own, own_len=own_len,
+                   prefix_keep=prefix_keep, out=out, workspace=workspace)
     desc = _ATTN.pack(B, T, Hq, Hkv, D, P, S, D ** -0.5 if scale is None else scale, causal,
-                      q.data_ptr(), qb, qt, qh, k_prefix.data_ptr(), kpp, kph, v_prefix.data_ptr(), vpp, vph,
+                      qp, qb, qt, qh, k_prefix.data_ptr(), kpp, kph, v_prefix.data_ptr(), vpp, vph,
                       k_own.data_ptr(), kob, kos, koh, v_own.data_ptr(), vob, vos, voh,
                       0 if own_len is None else own_len.data_ptr(),
                       0 if prefix_keep is None else prefix_keep.data_ptr(), out.data_ptr(), ob, ot, oh)
@@ -547,7 +560,8 @@ def bf16_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor
         if residual.dtype is not y.dtype or Mr != M or Nr != N:
             raise TypeError("residual must have y's shape and dtype")
         rp = residual.data_ptr()
-    st = LIB.bf16_linear(x.data_ptr(), ldx, w.data_ptr(), ldw, M, N, K, _EPILOGUE.pack(code, bdt, bp, rp, ldr),
+    xp = _together(x, w=w, bias=bias, residual=residual, y=y, workspace=workspace)
+    st = LIB.bf16_linear(xp, ldx, w.data_ptr(), ldw, M, N, K, _EPILOGUE.pack(code, bdt, bp, rp, ldr),
                          y.data_ptr(), _dtype_code(y), ldy, *_ws_args(workspace), _stream(stream))
     if st != 0:
         _check("bf16_linear", st)
@@ -573,7 +587,8 @@ def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
     for name, v in (("weight", weight), ("bias", bias)):
         if v is not None and (v.dtype != torch.float32 or v.shape != (C,) or not v.is_contiguous()):
             raise TypeError(f"{name} must be a contiguous fp32[C] tensor")
-    st = LIB.w4a4_group_norm_act(x.data_ptr(), _dtype_code(x), N, S, C, groups, x.stride(0),
+    xp = _together(x, weight=weight, bias=bias, out=out, workspace=workspace)
+    st = LIB.w4a4_group_norm_act(xp, _dtype_code(x), N, S, C, groups, x.stride(0),
                                  x.stride(1) if S > 1 else C, _ptr(weight), _ptr(bias), float(eps), _act_code(act),
                                  out.data_ptr(), out.stride(0), out.stride(1) if S > 1 else C, *_ws_args(workspace),
                                  _stream(stream))
