@@ -10,8 +10,8 @@
 // Statistics.  A thread keeps V adjacent channels and walks down the
 // positions of its slab, so loads are whole lines and a lane's groups are
 // fixed.  It sums d and d^2 of differences d = x - x0 to the channel's first
-// value in the slab (exact to an ulp, so a large mean costs no accuracy).
-// Sums become (count, mean, M2) and are joined by
+// value in the slab (exact to an ulp, so a large mean costs no accuracy), in
+// runs of kRun positions joined in fp64 (channel_moments).  Sums become (count, mean, M2) and are joined by
 //   mean = mean_a + (mean_b - mean_a) n_b / n,
 //   M2 = M2_a + M2_b + (mean_b - mean_a)^2 n_a n_b / n,
 // over the threads of a channel, over the channels of a group, and over the
@@ -32,6 +32,7 @@ namespace w4a4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRun = 64;           // positions a thread sums in fp32 before it joins
 constexpr int kMaxSlabs = 2048;
 constexpr int kJoinInline = 64;    // slabs the output kernel joins by itself
 constexpr int64_t kSlabElems = 8192;
@@ -122,22 +123,41 @@ struct Split {
 
 // Moments of the channels [c, c + V) of each thread over positions [s0, s1),
 // joined over the threads of a channel into mom[0 .. cols * V).
+//
+// A walk of more than kRun positions is summed in runs: fp32 inside a run,
+// the runs joined in fp64, and the next run's differences taken to the mean
+// so far.  One fp32 sum over 10^5 positions is off by up to a few parts in
+// 10^3 where its terms are alike (each is rounded the same way), and a first
+// value far from the rest would cost accuracy all along the walk.
 template <typename T, int V>
 __device__ __forceinline__ void channel_moments(const NormArgs& g, const T* x, int64_t s0, int64_t s1, int c, int cend,
                                                 int cols, Moments* mom) {
   const int rows = kThreads / cols, col = threadIdx.x % cols, depth = threadIdx.x / cols;
   float sh[V], s[V], q[V];
-  float n = 0.f;
+  double mean[V], m2[V];   // of the runs before, `done` positions
+  int64_t done = 0;
+  int cnt = 0;             // positions in s and q
 #pragma unroll
   for (int e = 0; e < V; ++e) sh[e] = s[e] = q[e] = 0.f;
+  auto fold = [&]() {
+    const double nb = cnt, inv = 1.0 / nb, w = nb / (double)(done + cnt);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const double ms = s[e] * inv, mb = sh[e] + ms, m2b = fmax(q[e] - s[e] * ms, 0.0);
+      const double d = done > 0 ? mb - mean[e] : 0.0;
+      m2[e] = done > 0 ? m2[e] + m2b + d * d * (done * w) : m2b;
+      mean[e] = done > 0 ? mean[e] + d * w : mb;
+      sh[e] = (float)mean[e];
+      s[e] = q[e] = 0.f;
+    }
+    done += cnt;
+  };
   if (c < cend && depth < rows && s0 + depth < s1) {
     const T* p = x + (s0 + depth) * g.x_ss + c;
     const int64_t step = (int64_t)rows * g.x_ss;
     const Vec<T, V> f = *reinterpret_cast<const Vec<T, V>*>(p);
 #pragma unroll
     for (int e = 0; e < V; ++e) sh[e] = to_f32(f.v[e]);
-    int64_t left = (s1 - s0 - depth + rows - 1) / rows;
-    n = (float)left;
     auto add = [&](const Vec<T, V>& u) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -146,18 +166,30 @@ __device__ __forceinline__ void channel_moments(const NormArgs& g, const T* x, i
         q[e] = __builtin_fmaf(d, d, q[e]);
       }
     };
-    for (; left >= 4; left -= 4, p += 4 * step) {   // four loads in flight
-      Vec<T, V> u[4];
+    int64_t left = (s1 - s0 - depth + rows - 1) / rows;
+    while (true) {
+      cnt = (int)min(left, (int64_t)kRun);
+      left -= cnt;
+      int k = cnt;
+      for (; k >= 4; k -= 4, p += 4 * step) {   // four loads in flight
+        Vec<T, V> u[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) u[k] = *reinterpret_cast<const Vec<T, V>*>(p + k * step);
+        for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const Vec<T, V>*>(p + i * step);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) add(u[k]);
+        for (int i = 0; i < 4; ++i) add(u[i]);
+      }
+      for (; k > 0; --k, p += step) add(*reinterpret_cast<const Vec<T, V>*>(p));
+      if (left == 0) break;
+      fold();
     }
-    for (; left > 0; --left, p += step) add(*reinterpret_cast<const Vec<T, V>*>(p));
+    if (done > 0) fold();
   }
   const int width = cols * V;
-  const float inv = n > 0.f ? 1.f / n : 0.f;
-  if (depth < rows) {
+  if (depth < rows && done > 0) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) mom[depth * width + col * V + e] = {(float)done, (float)mean[e], (float)m2[e]};
+  } else if (depth < rows) {
+    const float n = (float)cnt, inv = cnt > 0 ? 1.f / n : 0.f;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float ms = s[e] * inv;
