@@ -511,7 +511,7 @@ size_t w4a4_bf16_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act);
  *  weight, bias  fp32[C] or NULL (1 and 0).
  *  act     W4A4_ACT_NONE, RELU, GELU, GELU_TANH or SILU.
  * Shape rules: C a multiple of groups, C <= 65536; S <= 2^30, S * C <= 2^40;
- * eps >= 0.
+ * N <= 2^30, N * groups < 2^31; eps >= 0.
  * N == 0 or S == 0 is a no-op. */
 int w4a4_group_norm_act(const void* x, int32_t dtype, int64_t N, int64_t S, int64_t C, int64_t groups,
                         int64_t x_sn, int64_t x_ss, const float* weight, const float* bias, float eps,

@@ -1,0 +1,36 @@
+"""Sizes that the 16-bit operators accept and refuse, through the binding on
+host tensors: an accepted size goes on to the check of pointers, which finds
+no device memory (status -1); a refused one is status -2.  Nothing launches."""
+import os
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+pytestmark = pytest.mark.skipif(not os.path.exists(os.path.join(ROOT, "w4a4_post_quantized_channel_amd", "libw4a4.so")),
+                                reason="libw4a4.so not built")
+
+
+class _NoStream:
+    cuda_stream = 0
+
+
+def _status(call, *a, **kw):
+    from w4a4_post_quantized_channel_amd import ops
+    with pytest.raises(ops.W4A4Error) as e:
+        getattr(ops, call)(*a, stream=_NoStream(), **kw)
+    return e.value.status, str(e.value)
+
+
+@pytest.mark.parametrize("N", [65535, 65536, 70001, 1 << 20])
+def test_norm_takes_more_samples_than_a_grid_dimension(N):
+    """A layer norm of tokens has a sample per token."""
+    status, msg = _status("group_norm_act", torch.zeros(N, 1, 8), 1, out=torch.zeros(N, 1, 8))
+    assert status == -1 and "NULL" in msg
+
+
+def test_norm_refuses_more_groups_than_it_counts():
+    x = torch.zeros(1, 1, 8).expand(1 << 29, 1, 8)
+    assert _status("group_norm_act", x, 4, out=x)[0] == -2
+    assert _status("group_norm_act", x, 2, out=x)[0] == -1

@@ -174,7 +174,7 @@ static int check_norm_sizes(const char* fn, int64_t N, int64_t S, int64_t C, int
   if (N < 0 || S < 0 || C <= 0 || groups <= 0) return fail(W4A4_ERR_INVALID_ARG, "%s: bad sizes", fn);
   if (C % groups != 0)
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: %lld channels in %lld groups", fn, (long long)C, (long long)groups);
-  if (C > 65536 || N > 65535 || S > (1LL << 30) || S > (1LL << 40) / C || N * groups > INT32_MAX)
+  if (C > 65536 || N > (1LL << 30) || S > (1LL << 30) || S > (1LL << 40) / C || N * groups > INT32_MAX)
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: sizes too large", fn);
   return ok();
 }

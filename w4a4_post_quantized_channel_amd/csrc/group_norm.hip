@@ -334,43 +334,46 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(NormArgs g, Split 
 }
 
 // A run of whole groups of one sample, statistics and output.  A group wider
-// than the workgroup (run == 1 then) is taken in chunks of its channels.
+// than the workgroup (ng == 1 then) is taken in chunks of its channels.  A
+// workgroup goes on to sample n + gridDim.y: a grid's second dimension ends at
+// 65535, and a layer norm has a sample per token.
 template <typename T, int V, int KIND>
 __global__ void __launch_bounds__(kThreads) norm_whole_kernel(NormArgs g, int gpb, int cols) {
   __shared__ Moments mom[kThreads * V];
   __shared__ float2 st[kThreads * V];
   const int cg = g.C / g.groups;
-  const int64_t n = blockIdx.y;
   const int g0 = blockIdx.x * gpb, ng = min(gpb, g.groups - g0);
   const int c0 = g0 * cg, cend = c0 + ng * cg, width = cols * V;
-  const T* x = (const T*)g.x + n * g.x_sn;
   const int L = lanes_per(ng);
-  Moments tot = {0.f, 0.f, 0.f};
-  for (int cc = c0; cc < cend; cc += width) {
-    channel_moments<T, V>(g, x, 0, g.S, cc + (threadIdx.x % cols) * V, cend, cols, mom);
-    for (int i = threadIdx.x / L; i < ng; i += kThreads / L) {
-      Moments m = ng == 1 ? tot : Moments{0.f, 0.f, 0.f};
-      const int cnt = ng == 1 ? min(width, cend - cc) : cg;
-      for (int c = threadIdx.x % L; c < cnt; c += L) m = join(m, mom[i * cg + c]);
-      tot = m;
-      if (cc + width >= cend) {
-        m = join_lanes(m, L);
-        if (threadIdx.x % L == 0) st[i] = mean_rstd(m, g.eps);
+  for (int64_t n = blockIdx.y; n < g.N; n += gridDim.y) {
+    const T* x = (const T*)g.x + n * g.x_sn;
+    Moments tot = {0.f, 0.f, 0.f};
+    for (int cc = c0; cc < cend; cc += width) {
+      channel_moments<T, V>(g, x, 0, g.S, cc + (threadIdx.x % cols) * V, cend, cols, mom);
+      for (int i = threadIdx.x / L; i < ng; i += kThreads / L) {
+        Moments m = ng == 1 ? tot : Moments{0.f, 0.f, 0.f};
+        const int cnt = ng == 1 ? min(width, cend - cc) : cg;
+        for (int c = threadIdx.x % L; c < cnt; c += L) m = join(m, mom[i * cg + c]);
+        tot = m;
+        if (cc + width >= cend) {
+          m = join_lanes(m, L);
+          if (threadIdx.x % L == 0) st[i] = mean_rstd(m, g.eps);
+        }
       }
+      __syncthreads();
     }
-    __syncthreads();
-  }
-  for (int cc = c0; cc < cend; cc += width) {
-    const int c = cc + (threadIdx.x % cols) * V;
-    if (c >= cend) break;
-    float mu[V], rs[V];
+    for (int cc = c0; cc < cend; cc += width) {
+      const int c = cc + (threadIdx.x % cols) * V;
+      if (c >= cend) break;
+      float mu[V], rs[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float2 v = st[(c + e - c0) / cg];
-      mu[e] = v.x;
-      rs[e] = v.y;
+      for (int e = 0; e < V; ++e) {
+        const float2 v = st[(c + e - c0) / cg];
+        mu[e] = v.x;
+        rs[e] = v.y;
+      }
+      Applier<T, V, KIND>(g, n, 0, g.S, c, cols, true).run(g, mu, rs);
     }
-    Applier<T, V, KIND>(g, n, 0, g.S, c, cols, true).run(g, mu, rs);
   }
 }
 
@@ -403,7 +406,8 @@ hipError_t run_kind(const NormArgs& g, void* workspace, hipStream_t st) {
     if (cg % V == 0)
       while (gpb > 1 && gpb * cg > 16 * V) gpb = (gpb + 1) / 2;
     const int w = (gpb * cg + V - 1) / V, cols = w < kThreads ? w : kThreads;
-    norm_whole_kernel<T, V, KIND><<<dim3((g.groups + gpb - 1) / gpb, (unsigned)g.N), kThreads, 0, st>>>(g, gpb, cols);
+    const unsigned samples = (unsigned)(g.N < 65535 ? g.N : 65535);
+    norm_whole_kernel<T, V, KIND><<<dim3((g.groups + gpb - 1) / gpb, samples), kThreads, 0, st>>>(g, gpb, cols);
     return hipGetLastError();
   }
   Split sp;
