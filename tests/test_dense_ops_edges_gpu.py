@@ -8,7 +8,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-BF16, F32 = 2.0 ** -8, 2.0 ** -24
+from test_dense_ops_gpu import BF16, F32, _linear_inputs, _linear_reference
 
 
 @pytest.fixture(scope="module")
@@ -21,6 +21,28 @@ def ops():
 
 def _gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# ----------------------------------------------------------------------------
+# bf16 linear
+# ----------------------------------------------------------------------------
+def _linear(ops, M, N, K, act, bias, residual, y_dtype, workspace, seed):
+    x, w, b, r = [None if t is None else t.cuda() for t in _linear_inputs(M, N, K, act, bias, residual, y_dtype, seed)]
+    want, tol = _linear_reference(x, w, b, act, r, BF16 if y_dtype == torch.bfloat16 else F32)
+    print(f"[linear] {M}x{N}x{K} {act} {y_dtype} ws={workspace}", flush=True)
+    y = ops.bf16_linear(x, w, bias=b, act=act, residual=r, y_dtype=y_dtype,
+                        workspace=ops.make_bf16_linear_workspace(M, N, K, act) if workspace else None)
+    err = (y.double() - want).abs()
+    assert bool((err <= tol).all()), (float((err - tol).max()), float(err.max()))
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("M,N,K,act", [(16, 32773, 4200, "gelu"), (5, 20011, 2056, "none"), (1, 32768, 4104, "silu"),
+                                       (4, 33000, 1032, "none"), (4, 33000, 520, "gelu_tanh"), (9, 16500, 4168, "swiglu"),
+                                       (2, 16500, 1544, "swiglu")])
+def test_few_rows_over_many_columns(ops, M, N, K, act, workspace):
+    """Both kernels for at most 16 rows where the columns alone fill the card."""
+    _linear(ops, M, N, K, act, torch.float32, True, torch.float32 if M % 2 else torch.bfloat16, workspace, seed=M)
 
 
 # ----------------------------------------------------------------------------

@@ -1,0 +1,64 @@
+"""bf16_linear's choice of kernel, tile and K split (host code, built with g++)."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "w4a4_post_quantized_channel_amd", "csrc")
+pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+
+DRIVER = r"""
+#include <cstdio>
+#include "gemm_bf16_plan.h"
+int main() {
+  long long M, N, K;
+  int act, ws;
+  while (std::scanf("%lld %lld %lld %d %d", &M, &N, &K, &act, &ws) == 5) {
+    const w4a4::GemmPlan p = w4a4::plan_gemm(M, N, K, act, ws != 0);
+    std::printf("%d %d %d %d %d %d\n", (int)p.rows, p.tile, p.tiles_m, p.tiles_n, p.splits, p.pn);
+  }
+}
+"""
+NONE, SWIGLU = 0, 5
+
+
+@pytest.fixture(scope="module")
+def plans(tmp_path_factory):
+    d = tmp_path_factory.mktemp("plan")
+    (d / "driver.cpp").write_text(DRIVER)
+    exe = str(d / "driver")
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-I" + CSRC, str(d / "driver.cpp"), "-o", exe], capture_output=True,
+                       text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+    def run(shapes):
+        text = "".join(f"{M} {N} {K} {act} {ws}\n" for M, N, K, act, ws in shapes)
+        out = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=60).stdout.splitlines()
+        assert len(out) == len(shapes)
+        return [dict(zip(("rows", "tile", "tiles_m", "tiles_n", "splits", "pn"), map(int, line.split()))) for line in out]
+    return run
+
+
+def test_few_rows_over_many_columns_take_the_tiles(plans):
+    """Where the tiles need no split, a workspace changes nothing; more than
+    four rows, or at most 1024 of K, are the tiles' there."""
+    for ws in (0, 1):
+        for M, N, K, act in [(16, 32768, 8192, NONE), (16, 65536, 5120, NONE), (8, 24576, 8192, NONE), (16, 20480, 4096, NONE),
+                             (1, 32768, 1024, NONE), (16, 16384, 5120, SWIGLU), (12, 131072, 2048, NONE)]:
+            p, = plans([(M, N, K, act, ws)])
+            assert not p["rows"] and p["splits"] == 1, (M, N, K, act, ws, p)
+        for M, N, K, act in [(1, 32768, 8192, NONE), (4, 32768, 4096, NONE), (1, 65536, 2048, SWIGLU)]:
+            assert plans([(M, N, K, act, ws)])[0]["rows"], (M, N, K, act, ws)
+
+
+def test_few_rows_and_columns(plans):
+    for M, N, K in [(1, 2048, 2048), (16, 4096, 4096), (16, 2048, 1024), (3, 77, 264), (1, 1, 8)]:
+        for ws in (0, 1):
+            assert plans([(M, N, K, NONE, ws)])[0]["rows"]
+    for M, N, K in [(1, 64, 8192), (16, 4096, 8192), (16, 8192, 5120)]:
+        split, alone = plans([(M, N, K, NONE, 1), (M, N, K, NONE, 0)])
+        assert not split["rows"] and split["splits"] > 1      # K over workgroups, where they may be joined
+        assert alone["rows"]
+    assert not plans([(17, 2048, 2048, NONE, 1)])[0]["rows"]

@@ -27,6 +27,7 @@
 #include "activation.h"
 #include "dense.h"
 #include "device_common.h"
+#include "gemm_bf16_plan.h"
 #include "lds_sync.h"
 
 namespace w4a4 {
@@ -343,7 +344,7 @@ gemm_bf16_kernel(GemmPlanArgs p) {
 // takes 16 output columns and its eight waves a share of K each, operands
 // straight from global memory (16 bytes a lane, kRowsAhead steps of 32 K in
 // flight); the waves' sums are added in order through LDS.
-constexpr int kRowsMax = 16, kRowsWaves = 8, kRowsAhead = 8;
+constexpr int kRowsAhead = 8;
 
 template <int KIND, bool GATED>
 __global__ void __launch_bounds__(64 * kRowsWaves) gemm_bf16_rows_kernel(DenseArgs g) {
@@ -430,49 +431,19 @@ __global__ void __launch_bounds__(64) gemm_bf16_join_kernel(GemmPlanArgs p) {
   finish8<KIND, GATED>(g, z, u, load_bias8<GATED>(g, n), load_res8(g, m, n, vec_ok(g)), m, n, vec_ok(g));
 }
 
-// Tiles, largest first.
+// kTiles
 using T256x320 = GCfg<8, 5, 2, 4, 2>;   // not for SwiGLU (odd fragment count)
 using T256x256 = GCfg<8, 4, 2, 4, 2>;
 using T128x256 = GCfg<4, 4, 2, 4, 3>;
 using T128x128 = GCfg<4, 2, 2, 4, 4>;
 using T64x128 = GCfg<2, 2, 2, 4, 5>;
 using T32x128 = GCfg<2, 2, 1, 4, 6>;
-struct TileInfo {
-  int bm, bn;
-  double us;   // measured time of a K stage, every CU busy with one workgroup
-  bool gated;
-};
-constexpr TileInfo kTiles[] = {{256, 320, 1.95, false}, {256, 256, 1.4, true}, {128, 256, 0.82, true},
-                               {128, 128, 0.53, true},  {64, 128, 0.40, true}, {32, 128, 0.30, true}};
-constexpr int kNumTiles = 6, kCUs = 256;
-
-struct GemmPlan {
-  int tile, tiles_m, tiles_n, splits, pn;
-};
-
-GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int act, bool split) {
-  const bool gated = act == W4A4_ACT_SWIGLU;
-  const int64_t stages = (K + 63) / 64;
-  GemmPlan best{};
-  double best_cost = 1e300;
-  for (int i = 0; i < kNumTiles; ++i) {
-    const TileInfo& ti = kTiles[i];
-    if (gated && !ti.gated) continue;
-    const int64_t bn = gated ? ti.bn / 2 : ti.bn;
-    const int64_t tm = (M + ti.bm - 1) / ti.bm, tn = (N + bn - 1) / bn, tiles = tm * tn;
-    for (int64_t sp = 1; sp <= 64; sp *= 2) {
-      if (sp > 1 && (!split || tiles * sp > 2 * kCUs || stages / sp < 2)) break;
-      const int64_t rounds = (tiles * sp + kCUs - 1) / kCUs;
-      double cost = rounds * ((stages + sp - 1) / sp * ti.us + 1.5 + ti.bm * ti.bn * 4e-5);
-      if (sp > 1) cost += 3.0 + 0.1 * sp + 2.0 * sp * M * tn * ti.bn * 4.0 / 4e6;
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = {i, (int)tm, (int)tn, (int)sp, (int)(tn * ti.bn)};
-      }
-    }
-  }
-  return best;
+template <typename C>
+constexpr bool is_tile(int i) {
+  return kTiles[i].bm == C::BM && kTiles[i].bn == C::BN && kTiles[i].threads == 64 * C::NW && (!kTiles[i].gated || C::TJ % 2 == 0);
 }
+static_assert(is_tile<T256x320>(0) && is_tile<T256x256>(1) && is_tile<T128x256>(2) && is_tile<T128x128>(3) &&
+              is_tile<T64x128>(4) && is_tile<T32x128>(5), "kTiles");
 
 template <typename C, bool GATED>
 void launch_kind(const GemmPlanArgs& p, hipStream_t st) {
@@ -494,21 +465,15 @@ void launch_tile(const GemmPlanArgs& p, hipStream_t st) {
 
 }  // namespace
 
-// At most 16 rows: the one-launch kernel while K is short.  Measured against
-// the split tiles (us in a graph, one launch / split): 1 x 2048 x 2048 5.6 /
-// 8.0, 16 x 2048 x 2048 6.9 / 9.2, 1 x 4096 x 4096 8.3 / 10.6; from there on
-// its workgroups are too few for the weights: 1 x 2048 x 8192 12.4 / 11.4,
-// 16 x 2048 x 8192 17.8 / 12.3.
-static bool rows_kernel(int64_t M, int64_t K, bool split) { return M <= kRowsMax && (K <= 4096 || !split); }
-
 size_t gemm_bf16_workspace(int64_t M, int64_t N, int64_t K, int act) {
-  if (rows_kernel(M, K, true)) return 0;
   const GemmPlan pl = plan_gemm(M, N, K, act, true);
-  return pl.splits > 1 ? (size_t)pl.splits * M * pl.pn * 4 : 0;
+  return !pl.rows && pl.splits > 1 ? (size_t)pl.splits * M * pl.pn * 4 : 0;
 }
 
 hipError_t launch_gemm_bf16(const DenseArgs& g, void* workspace, hipStream_t st) {
-  if (rows_kernel(g.M, g.K, workspace != nullptr)) {
+  // a workspace that no split needs is null here: the plan is the same then
+  const GemmPlan pl = plan_gemm(g.M, g.N, g.K, g.act, workspace != nullptr);
+  if (pl.rows) {
     const unsigned grid = (unsigned)((g.N + 15) / 16);
     const int kind = act_kind(g.act), threads = 64 * kRowsWaves;
     if (g.act == W4A4_ACT_SWIGLU) gemm_bf16_rows_kernel<ACT_KIND_SIGMOID, true><<<grid, threads, 0, st>>>(g);
@@ -517,7 +482,6 @@ hipError_t launch_gemm_bf16(const DenseArgs& g, void* workspace, hipStream_t st)
     else gemm_bf16_rows_kernel<ACT_KIND_PLAIN, false><<<grid, threads, 0, st>>>(g);
     return hipGetLastError();
   }
-  const GemmPlan pl = plan_gemm(g.M, g.N, g.K, g.act, workspace != nullptr);
   GemmPlanArgs p{g, pl.tiles_m, pl.tiles_n, pl.splits, (g.K + 63) / 64, (float*)workspace, pl.pn};
   switch (pl.tile) {
     case 0: launch_tile<T256x320>(p, st); break;
