@@ -479,7 +479,7 @@ size_t w4a4_prefix_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t
  *                (same ldr), otherwise y overlaps no input.
  *  y   M x N, F32 or BF16, row stride ldy.
  * The sum, bias, activation and residual are fp32; one rounding to y_dtype.
- * Shape rules: K % 8 == 0, M, N <= 2^30, M N <= 2^40; ldx, ldw % 8 == 0 and
+ * Shape rules: K % 8 == 0, M <= 2^30, N <= 2^22, M N <= 2^37; ldx, ldw % 8 == 0 and
  * <= 2^21 (so K too); ldy, ldr <= 2^22.  x, w 16-byte aligned; bias, residual and y by
  * their element size. */
 enum { W4A4_ACT_NONE = 0, W4A4_ACT_RELU = 1, W4A4_ACT_GELU = 2, W4A4_ACT_GELU_TANH = 3, W4A4_ACT_SILU = 4,

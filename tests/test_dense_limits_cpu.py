@@ -34,3 +34,15 @@ def test_norm_refuses_more_groups_than_it_counts():
     x = torch.zeros(1, 1, 8).expand(1 << 29, 1, 8)
     assert _status("group_norm_act", x, 4, out=x)[0] == -2
     assert _status("group_norm_act", x, 2, out=x)[0] == -1
+
+
+def test_linear_sizes():
+    from w4a4_post_quantized_channel_amd import ops
+
+    def call(M, N, act=0):                                      # NULL operands: status -1 once the sizes are accepted
+        return ops.LIB.bf16_linear(None, 64, None, 64, M, N, 64, ops._EPILOGUE.pack(act, 0, 0, 0, 0), None, ops.DT_BF16, N,
+                                   None, 0, None)
+
+    assert [call(1 << 30, 128), call(1 << 15, 1 << 22), call(1, 1 << 22, 5)] == [-1, -1, -1]
+    # outputs that no memory holds, rows past the stride that y may have
+    assert [call(1 << 30, 129), call((1 << 15) + 1, 1 << 22), call(1, (1 << 22) + 1, 5), call(1 << 31, 1)] == [-2] * 4

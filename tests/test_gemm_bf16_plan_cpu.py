@@ -1,5 +1,6 @@
 """bf16_linear's choice of kernel, tile and K split (host code, built with g++)."""
 import os
+import random
 import shutil
 import subprocess
 
@@ -21,6 +22,7 @@ int main() {
   }
 }
 """
+TILES = [(256, 320, 512), (256, 256, 512), (128, 256, 512), (128, 128, 512), (64, 128, 512), (32, 128, 256)]
 NONE, SWIGLU = 0, 5
 
 
@@ -62,3 +64,29 @@ def test_few_rows_and_columns(plans):
         assert not split["rows"] and split["splits"] > 1      # K over workgroups, where they may be joined
         assert alone["rows"]
     assert not plans([(17, 2048, 2048, NONE, 1)])[0]["rows"]
+
+
+def test_every_accepted_size_has_a_launch(plans):
+    """A grid holds fewer than 2^32 threads, and its tiles cover the output."""
+    r = random.Random(1)
+    shapes = [(1, 1 << 22, 8, NONE, 1), (16, 1 << 22, 8, SWIGLU, 0), (16, 1 << 22, 1 << 21, NONE, 0), (1 << 30, 1, 8, NONE, 1),
+              (1 << 30, 8, 8, NONE, 1), (1 << 30, 128, 8, NONE, 0), (1 << 30, 128, 8, SWIGLU, 0),
+              (1 << 15, 1 << 22, 8, SWIGLU, 1)]
+    for _ in range(3000):
+        M = int(2 ** r.uniform(0, 30))
+        act = r.choice([NONE, SWIGLU])
+        N = int(2 ** r.uniform(0, min(22, 37 - M.bit_length() + 0.9)))
+        if M * N <= 1 << 37:
+            shapes.append((M, N, 8 * int(2 ** r.uniform(0, 18)), act, r.randint(0, 1)))
+    for (M, N, K, act, ws), p in zip(shapes, plans(shapes)):
+        where = (M, N, K, act, ws, p)
+        if p["rows"]:
+            assert M <= 16 and (N + 15) // 16 * 512 < 1 << 32, where
+            continue
+        bm, bn, threads = TILES[p["tile"]]
+        bn = bn // 2 if act == SWIGLU else bn
+        assert p["tiles_m"] * bm >= M and p["tiles_n"] * bn >= N, where
+        assert 0 < p["tiles_m"] * p["tiles_n"] * p["splits"] * threads < 1 << 32, where
+        assert p["splits"] == 1 or (ws and p["tiles_m"] * p["tiles_n"] * p["splits"] <= 512), where
+        if p["splits"] > 1:                                     # the join: a thread takes 8 columns
+            assert (M * ((N + 7) // 8) + 63) // 64 * 64 < 1 << 32, where

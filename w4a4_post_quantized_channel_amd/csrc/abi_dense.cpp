@@ -109,7 +109,8 @@ size_t w4a4_prefix_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t
 static int check_dense_sizes(const char* fn, int64_t M, int64_t N, int64_t K, int32_t act) {
   if (M < 0 || N < 0 || K <= 0) return fail(W4A4_ERR_INVALID_ARG, "%s: bad sizes", fn);
   if (K % 8 != 0) return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: K=%lld not a multiple of 8", fn, (long long)K);
-  if (K > (1LL << 21) || M > (1LL << 30) || N > (1LL << 30) || (N > 0 && M > (1LL << 40) / N))
+  // (N is bounded by y's row stride)
+  if (K > (1LL << 21) || M > (1LL << 30) || N > (1LL << 22) || (N > 0 && M > (1LL << 37) / N))
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: sizes too large", fn);
   if (act < W4A4_ACT_NONE || act > W4A4_ACT_SWIGLU)
     return fail(W4A4_ERR_UNSUPPORTED_FORMAT, "%s: unknown activation %d", fn, act);

@@ -19,6 +19,8 @@ constexpr int kNumTiles = 6, kCUs = 256;
 // The kernel for at most kRowsMax rows: 16 columns a workgroup.
 constexpr int kRowsMax = 16, kRowsWaves = 8;
 
+constexpr int64_t kMaxThreads = 0xFFFFFFFFll;   // of a launch
+
 struct GemmPlan {
   bool rows;   // the kernel for few rows; the rest says what the tiles would do
   int tile, tiles_m, tiles_n, splits, pn;
@@ -34,6 +36,7 @@ inline GemmPlan plan_tiles(int64_t M, int64_t N, int64_t K, int act, bool split)
     if (gated && !ti.gated) continue;
     const int64_t bn = gated ? ti.bn / 2 : ti.bn;
     const int64_t tm = (M + ti.bm - 1) / ti.bm, tn = (N + bn - 1) / bn, tiles = tm * tn;
+    if (tiles > kMaxThreads / ti.threads) continue;
     for (int64_t sp = 1; sp <= 64; sp *= 2) {
       if (sp > 1 && (!split || tiles * sp > 2 * kCUs || stages / sp < 2)) break;
       const int64_t rounds = (tiles * sp + kCUs - 1) / kCUs;
