@@ -35,6 +35,7 @@
 // softmax's vector work, the issue of copies and the barriers.  Few rows: the
 // load path of a CU (43 bytes a cycle measured, all waves loading) and the
 // chain of dependent memory latencies at the start and end of a workgroup.
+#include "attention_plan.h"
 #include "dense.h"
 #include "device_common.h"
 #include "lds_sync.h"
@@ -688,61 +689,6 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs p) {
   int rem, g, b = div_by(row, p.tg, rem), t = div_by(rem, p.g, g);
   uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * (int)p.g.d + g) * a.o_sh + d;
   *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-}
-
-struct AttnPlan {
-  int cfg;     // index of the (WQ, WK) pair
-  int rpt, tiles, parts, np, ns;
-  int per;     // blocks of a part
-};
-
-struct Shape {
-  int wq, wk, bn;
-  double us;   // an iteration of a workgroup, all CUs busy
-};
-// (WQ, WK, BN) per head width; the kernels below are instantiated from it.
-constexpr Shape kShapes[3][4] = {
-    {{1, 8, 64, 2.0}, {2, 4, 64, 1.8}, {4, 2, 64, 2.0}, {8, 1, 64, 1.5}},      // D = 64
-    {{1, 8, 32, 3.05}, {2, 4, 32, 2.3}, {4, 2, 64, 3.0}, {8, 1, 64, 2.0}},     // D = 128
-    {{2, 2, 32, 3.0}, {4, 1, 32, 2.6}, {0, 0, 0, 0.0}, {0, 0, 0, 0.0}}};       // D = 256
-constexpr int kCUs = 256;
-
-AttnPlan plan_attention(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t P, int64_t S, bool split) {
-  const Shape* sh = kShapes[D == 64 ? 0 : D == 128 ? 1 : 2];
-  const int64_t tg = T * (Hq / Hkv), rows = B * tg;
-  AttnPlan best{};
-  double best_cost = 1e300;
-  for (int c = 0; c < 4; ++c) {
-    if (sh[c].wq == 0) break;
-    const int64_t R = 32 * sh[c].wq;
-    const int64_t rpt = tg <= R ? R / tg * tg : R;
-    const int64_t tiles = (rows + rpt - 1) / rpt;
-    const int64_t np = (P + sh[c].bn - 1) / sh[c].bn, ns = (S + sh[c].bn - 1) / sh[c].bn;
-    const int64_t nseq = tg <= R ? rpt / tg : (R + tg - 1) / tg + (R % tg != 0);
-    const int64_t total = np + (nseq < B ? nseq : B) * ns;
-    const int64_t units = Hkv * tiles;
-    // Parts: up to one round of the card's CUs, with at least one block per
-    // key group, halved as long as that is cheaper.
-    const int64_t cap = (total + sh[c].wk - 1) / sh[c].wk;
-    int64_t most = split && units < kCUs ? kCUs / units : 1;
-    if (most > cap) most = cap < 1 ? 1 : cap;
-    for (int64_t want = most; want >= 1; want /= 2) {
-      const int64_t blocks = total < 1 ? 1 : (total + want - 1) / want;
-      const int64_t parts = total < 1 ? 1 : (total + blocks - 1) / blocks;
-      const int64_t iters = (blocks + sh[c].wk - 1) / sh[c].wk, rounds = (units * parts + kCUs - 1) / kCUs;
-      // Microseconds, fitted to measurements (D = 128: a decoding batch of 64
-      // over 8192 keys 40 us as planned, 46 with 32-row tiles; a chunk of 8 x
-      // 50 over 2040 keys 26 as planned, 29 with 64-row tiles): iterations,
-      // start and end of a workgroup, and the join's launch, parts and bytes.
-      double cost = rounds * (iters * sh[c].us + 5.0);
-      if (parts > 1) cost += 3.5 + 0.1 * parts + parts * Hkv * rows * (double)D * 8.0 / 4e6;
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = {c, (int)rpt, (int)tiles, (int)parts, (int)np, (int)ns, (int)blocks};
-      }
-    }
-  }
-  return best;
 }
 
 template <typename C>
