@@ -36,11 +36,23 @@ def plans(tmp_path_factory):
     assert r.returncode == 0, r.stderr[-2000:]
 
     def run(shapes):
-        text = "".join(f"{M} {N} {K} {act} {ws}\n" for M, N, K, act, ws in shapes)
+        text = "".join(f"{M} {N} {K} {act} {int(ws)}\n" for M, N, K, act, ws in shapes)
         out = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=60).stdout.splitlines()
         assert len(out) == len(shapes)
         return [dict(zip(("rows", "tile", "tiles_m", "tiles_n", "splits", "pn"), map(int, line.split()))) for line in out]
     return run
+
+
+def test_the_gpu_tests_meet_every_tile(plans):
+    pytest.importorskip("torch")
+    from test_linear_tiles_gpu import SHAPES
+    for (tile, gated, split), (M, N, K, ws) in SHAPES.items():
+        p, = plans([(M, N, K, SWIGLU if gated else NONE, ws)])
+        got = ("rows", gated, False) if p["rows"] else (p["tile"], gated, p["splits"] > 1)
+        assert got == (tile, gated, split), ((M, N, K, ws), p)
+    # every tile, whole and split; 256 columns of SwiGLU need an even number of fragments, which 320 lack
+    want = {(t, g, s) for t in range(6) for g in (False, True) for s in (False, True) if t or not g}
+    assert set(SHAPES) == want | {("rows", False, False), ("rows", True, False)}
 
 
 def test_few_rows_over_many_columns_take_the_tiles(plans):
