@@ -45,6 +45,27 @@ def test_few_rows_over_many_columns(ops, M, N, K, act, workspace):
     _linear(ops, M, N, K, act, torch.float32, True, torch.float32 if M % 2 else torch.bfloat16, workspace, seed=M)
 
 
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu", "swiglu"])
+@pytest.mark.parametrize("M", [1, 40])
+def test_activations_of_any_finite_argument(ops, act, M):
+    """Both ends of the range: an activation is its argument or zero there, not
+    a large argument times the smallest sigmoid."""
+    mag = torch.tensor([80.0, 86.5, 87.5, 88.0, 88.5, 89.0, 100.0, 104.0, 1e3, 1e6, 1e10, 1e20, 1e30, 1e38, 3e38])
+    z = torch.cat([-mag, mag]).bfloat16().cuda()
+    x = torch.zeros(M, 8, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1.0
+    w = torch.zeros(z.numel(), 8, dtype=torch.bfloat16, device="cuda")
+    w[:, 0] = z
+    if act == "swiglu":
+        w = torch.cat([w, torch.zeros_like(w)])
+        w[z.numel():, 0] = 0.5                                     # the second factor
+    want, tol = _linear_reference(x, w, None, act, None, F32)
+    y = ops.bf16_linear(x, w, act=act, y_dtype=torch.float32).double()
+    # relative accuracy is lost below the smallest normal number
+    err = (y - want).abs()
+    assert bool((err <= tol + 1e-36).all()), (float((err - tol).max()), y[0].tolist())
+
+
 # ----------------------------------------------------------------------------
 # Group norm
 # ----------------------------------------------------------------------------
@@ -64,3 +85,21 @@ def test_norm_of_more_samples_than_a_grid_dimension(ops, N, S, C, groups, dtype)
         tol = 4 * F32 * v.abs().amax(dim=(1, 3), keepdim=True) * rstd + (4e-6 + 5 * F32 + half) * want.abs() + 1e-30
         err = (y[n:n + 8192].double().view(want.shape) - want).abs()
         assert bool((err <= tol).all()), (n, float((err - tol).max()), float(err.max()))
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norm_activations_far_out(ops, act, dtype):
+    """Biases that carry the activation's argument to both ends of the range."""
+    mag = torch.tensor([60.0, 87.5, 88.5, 104.0, 1e4, 1e10, 1e30, 3e38], device="cuda")
+    b = torch.cat([-mag, mag])
+    x = torch.randn(2, 33, 16, generator=_gen(1), device="cuda").to(dtype)
+    y = ops.group_norm_act(x, 4, torch.zeros(16, device="cuda"), b, act=act).double()
+    z = b.double()
+    slope = {"gelu": lambda: 0.5 * torch.special.erfc(-z / math.sqrt(2)),
+             "gelu_tanh": lambda: torch.sigmoid(2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)),
+             "silu": lambda: torch.sigmoid(z)}[act]()
+    want = (z * slope).expand_as(y)
+    half = BF16 if dtype == torch.bfloat16 else F32
+    err = (y - want).abs()
+    assert bool((err <= (half + 32 * F32) * want.abs() + 1e-36).all()), (float(err.max()), y[0, 0].tolist())

@@ -16,7 +16,8 @@ __device__ __forceinline__ float exp_f32(float x) {
   return __builtin_fmaf(y * r, 0.693147181f, y);
 }
 
-// z * sigmoid(u), sigmoid(u) = 1 / (1 + exp(-u)).
+// z * sigmoid(u), sigmoid(u) = 1 / (1 + exp(-u)).  Past u = -87.3 the
+// reciprocal would be subnormal, and the instruction gives zero, the limit.
 __device__ __forceinline__ float times_sigmoid(float z, float u) {
   return z * __builtin_amdgcn_rcpf(1.f + exp_f32(-u));
 }
