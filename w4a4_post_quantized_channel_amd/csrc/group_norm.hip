@@ -124,12 +124,13 @@ struct Split {
 // Moments of the channels [c, c + V) of each thread over positions [s0, s1),
 // joined over the threads of a channel into mom[0 .. cols * V).
 //
-// A walk of more than kRun positions is summed in runs: fp32 inside a run,
-// the runs joined in fp64, and the next run's differences taken to the mean
-// so far.  One fp32 sum over 10^5 positions is off by up to a few parts in
-// 10^3 where its terms are alike (each is rounded the same way), and a first
-// value far from the rest would cost accuracy all along the walk.
-template <typename T, int V>
+// LONG: a walk may have more than kRun positions and is summed in runs, fp32
+// inside a run, the runs joined in fp64, and the next run's differences taken
+// to the mean so far.  One fp32 sum over 10^5 positions is off by up to a few
+// parts in 10^3 where its terms are alike (each is rounded the same way), and
+// a first value far from the rest would cost accuracy all along the walk.
+// Without LONG the kernels save its registers (0.1-0.2 us of 8-14).
+template <typename T, int V, bool LONG>
 __device__ __forceinline__ void channel_moments(const NormArgs& g, const T* x, int64_t s0, int64_t s1, int c, int cend,
                                                 int cols, Moments* mom) {
   const int rows = kThreads / cols, col = threadIdx.x % cols, depth = threadIdx.x / cols;
@@ -166,11 +167,7 @@ __device__ __forceinline__ void channel_moments(const NormArgs& g, const T* x, i
         q[e] = __builtin_fmaf(d, d, q[e]);
       }
     };
-    int64_t left = (s1 - s0 - depth + rows - 1) / rows;
-    while (true) {
-      cnt = (int)min(left, (int64_t)kRun);
-      left -= cnt;
-      int k = cnt;
+    auto walk = [&](int k) {
       for (; k >= 4; k -= 4, p += 4 * step) {   // four loads in flight
         Vec<T, V> u[4];
 #pragma unroll
@@ -179,13 +176,21 @@ __device__ __forceinline__ void channel_moments(const NormArgs& g, const T* x, i
         for (int i = 0; i < 4; ++i) add(u[i]);
       }
       for (; k > 0; --k, p += step) add(*reinterpret_cast<const Vec<T, V>*>(p));
-      if (left == 0) break;
-      fold();
+    };
+    if constexpr (LONG) {
+      for (int64_t left = (s1 - s0 - depth + rows - 1) / rows; left > 0;) {
+        cnt = (int)min(left, (int64_t)kRun);
+        walk(cnt);
+        fold();
+        left -= cnt;
+      }
+    } else {
+      cnt = (int)((uint32_t)(s1 - s0 - depth + rows - 1) / (uint32_t)rows);
+      walk(cnt);
     }
-    if (done > 0) fold();
   }
   const int width = cols * V;
-  if (depth < rows && done > 0) {
+  if (LONG && depth < rows && done > 0) {
 #pragma unroll
     for (int e = 0; e < V; ++e) mom[depth * width + col * V + e] = {(float)done, (float)mean[e], (float)m2[e]};
   } else if (depth < rows) {
@@ -269,14 +274,14 @@ struct Applier {
 };
 
 // Moments of (sample, slab, group).
-template <typename T, int V>
+template <typename T, int V, bool LONG>
 __global__ void __launch_bounds__(kThreads) norm_moments_kernel(NormArgs g, Split sp, Moments* ws) {
   __shared__ Moments mom[kThreads * V];
   const int cg = g.C / g.groups;
   const int g0 = blockIdx.y * sp.gpb, ng = min(sp.gpb, g.groups - g0);
   const int64_t n = blockIdx.z;
   const int64_t s0 = blockIdx.x * sp.len, s1 = min(g.S, s0 + sp.len);
-  channel_moments<T, V>(g, (const T*)g.x + n * g.x_sn, s0, s1, g0 * cg + (threadIdx.x % sp.cols) * V, (g0 + ng) * cg,
+  channel_moments<T, V, LONG>(g, (const T*)g.x + n * g.x_sn, s0, s1, g0 * cg + (threadIdx.x % sp.cols) * V, (g0 + ng) * cg,
                         sp.cols, mom);
   const int L = lanes_per(ng);
   for (int i = threadIdx.x / L; i < ng; i += kThreads / L) {
@@ -334,46 +339,43 @@ __global__ void __launch_bounds__(kThreads) norm_apply_kernel(NormArgs g, Split 
 }
 
 // A run of whole groups of one sample, statistics and output.  A group wider
-// than the workgroup (ng == 1 then) is taken in chunks of its channels.  A
-// workgroup goes on to sample n + gridDim.y: a grid's second dimension ends at
-// 65535, and a layer norm has a sample per token.
-template <typename T, int V, int KIND>
+// than the workgroup (ng == 1 then) is taken in chunks of its channels.
+template <typename T, int V, int KIND, bool LONG>
 __global__ void __launch_bounds__(kThreads) norm_whole_kernel(NormArgs g, int gpb, int cols) {
   __shared__ Moments mom[kThreads * V];
   __shared__ float2 st[kThreads * V];
   const int cg = g.C / g.groups;
+  const int64_t n = blockIdx.y;
   const int g0 = blockIdx.x * gpb, ng = min(gpb, g.groups - g0);
   const int c0 = g0 * cg, cend = c0 + ng * cg, width = cols * V;
+  const T* x = (const T*)g.x + n * g.x_sn;
   const int L = lanes_per(ng);
-  for (int64_t n = blockIdx.y; n < g.N; n += gridDim.y) {
-    const T* x = (const T*)g.x + n * g.x_sn;
-    Moments tot = {0.f, 0.f, 0.f};
-    for (int cc = c0; cc < cend; cc += width) {
-      channel_moments<T, V>(g, x, 0, g.S, cc + (threadIdx.x % cols) * V, cend, cols, mom);
-      for (int i = threadIdx.x / L; i < ng; i += kThreads / L) {
-        Moments m = ng == 1 ? tot : Moments{0.f, 0.f, 0.f};
-        const int cnt = ng == 1 ? min(width, cend - cc) : cg;
-        for (int c = threadIdx.x % L; c < cnt; c += L) m = join(m, mom[i * cg + c]);
-        tot = m;
-        if (cc + width >= cend) {
-          m = join_lanes(m, L);
-          if (threadIdx.x % L == 0) st[i] = mean_rstd(m, g.eps);
-        }
+  Moments tot = {0.f, 0.f, 0.f};
+  for (int cc = c0; cc < cend; cc += width) {
+    channel_moments<T, V, LONG>(g, x, 0, g.S, cc + (threadIdx.x % cols) * V, cend, cols, mom);
+    for (int i = threadIdx.x / L; i < ng; i += kThreads / L) {
+      Moments m = ng == 1 ? tot : Moments{0.f, 0.f, 0.f};
+      const int cnt = ng == 1 ? min(width, cend - cc) : cg;
+      for (int c = threadIdx.x % L; c < cnt; c += L) m = join(m, mom[i * cg + c]);
+      tot = m;
+      if (cc + width >= cend) {
+        m = join_lanes(m, L);
+        if (threadIdx.x % L == 0) st[i] = mean_rstd(m, g.eps);
       }
-      __syncthreads();
     }
-    for (int cc = c0; cc < cend; cc += width) {
-      const int c = cc + (threadIdx.x % cols) * V;
-      if (c >= cend) break;
-      float mu[V], rs[V];
+    __syncthreads();
+  }
+  for (int cc = c0; cc < cend; cc += width) {
+    const int c = cc + (threadIdx.x % cols) * V;
+    if (c >= cend) break;
+    float mu[V], rs[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float2 v = st[(c + e - c0) / cg];
-        mu[e] = v.x;
-        rs[e] = v.y;
-      }
-      Applier<T, V, KIND>(g, n, 0, g.S, c, cols, true).run(g, mu, rs);
+    for (int e = 0; e < V; ++e) {
+      const float2 v = st[(c + e - c0) / cg];
+      mu[e] = v.x;
+      rs[e] = v.y;
     }
+    Applier<T, V, KIND>(g, n, 0, g.S, c, cols, true).run(g, mu, rs);
   }
 }
 
@@ -391,6 +393,9 @@ int slabs_for(int64_t N, int64_t S, int64_t C, int64_t groups) {
   return want < 2 ? 1 : (int)want;
 }
 
+// Whether a thread of `cols` across the channels meets more than kRun of S positions.
+bool walk_is_long(int64_t S, int cols) { return S > (int64_t)kRun * (kThreads / cols); }
+
 size_t stat_bytes(int64_t N, int64_t groups) { return (size_t)(N * groups * 8 + 255) / 256 * 256; }
 
 template <typename T, int V, int KIND>
@@ -406,9 +411,19 @@ hipError_t run_kind(const NormArgs& g, void* workspace, hipStream_t st) {
     if (cg % V == 0)
       while (gpb > 1 && gpb * cg > 16 * V) gpb = (gpb + 1) / 2;
     const int w = (gpb * cg + V - 1) / V, cols = w < kThreads ? w : kThreads;
-    const unsigned samples = (unsigned)(g.N < 65535 ? g.N : 65535);
-    norm_whole_kernel<T, V, KIND><<<dim3((g.groups + gpb - 1) / gpb, samples), kThreads, 0, st>>>(g, gpb, cols);
-    return hipGetLastError();
+    // a grid's second dimension ends at 65535, and a layer norm has a sample per token
+    NormArgs part = g;
+    for (int64_t left = g.N; left > 0; left -= part.N) {
+      part.N = left < 65535 ? left : 65535;
+      const dim3 grid((g.groups + gpb - 1) / gpb, (unsigned)part.N);
+      if (walk_is_long(g.S, cols)) norm_whole_kernel<T, V, KIND, true><<<grid, kThreads, 0, st>>>(part, gpb, cols);
+      else norm_whole_kernel<T, V, KIND, false><<<grid, kThreads, 0, st>>>(part, gpb, cols);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      part.x = (const T*)part.x + part.N * g.x_sn;
+      part.y = (T*)part.y + part.N * g.y_sn;
+    }
+    return hipSuccess;
   }
   Split sp;
   sp.gpb = gpb;
@@ -419,7 +434,8 @@ hipError_t run_kind(const NormArgs& g, void* workspace, hipStream_t st) {
   float2* stat = (float2*)workspace;
   Moments* mom = (Moments*)((char*)workspace + stat_bytes(g.N, g.groups));
   const dim3 grid(sp.slabs, sp.blocks, (unsigned)g.N);
-  norm_moments_kernel<T, V><<<grid, kThreads, 0, st>>>(g, sp, mom);
+  if (walk_is_long(sp.len, sp.cols)) norm_moments_kernel<T, V, true><<<grid, kThreads, 0, st>>>(g, sp, mom);
+  else norm_moments_kernel<T, V, false><<<grid, kThreads, 0, st>>>(g, sp, mom);
   const bool inline_join = sp.slabs <= kJoinInline;
   if (!inline_join) norm_join_kernel<<<(unsigned)(g.N * g.groups), kThreads, 0, st>>>(g, sp.slabs, mom, stat);
   norm_apply_kernel<T, V, KIND><<<grid, kThreads, 0, st>>>(g, sp, mom, inline_join ? nullptr : stat);
