@@ -46,3 +46,9 @@ def test_linear_sizes():
     assert [call(1 << 30, 128), call(1 << 15, 1 << 22), call(1, 1 << 22, 5)] == [-1, -1, -1]
     # outputs that no memory holds, rows past the stride that y may have
     assert [call(1 << 30, 129), call((1 << 15) + 1, 1 << 22), call(1, (1 << 22) + 1, 5), call(1 << 31, 1)] == [-2] * 4
+
+
+@pytest.mark.parametrize("C", [256, 257, 512, 1024, 2048])
+def test_wide_groups_are_cut_over_positions(C):
+    from w4a4_post_quantized_channel_amd import ops
+    assert ops.LIB.w4a4_group_norm_workspace(1, 60000, C, 1) > 0

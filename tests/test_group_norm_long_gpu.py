@@ -56,6 +56,17 @@ def test_wide_groups(ops, C, groups, workspace):
     _compare(ops, x, groups, *_affine(C, g), workspace)
 
 
+@pytest.mark.parametrize("N,S,C,groups,dtype", [
+    (1, 20003, 2048, 1, torch.bfloat16), (1, 9001, 2056, 1, torch.bfloat16), (2, 3001, 1024, 1, torch.float32),
+    (1, 3001, 1028, 1, torch.float32), (3, 777, 1536, 3, torch.bfloat16), (1, 700, 4096, 2, torch.bfloat16),
+    (1, 5003, 514, 2, torch.bfloat16), (1, 5003, 257, 1, torch.bfloat16), (1, 40, 1000, 1, torch.float32)])
+@pytest.mark.parametrize("workspace", [True, False])
+def test_groups_around_a_workgroups_channels(ops, N, S, C, groups, dtype, workspace):
+    g = torch.Generator(device="cuda").manual_seed(S)
+    x = (torch.randn(N, S, C, generator=g, device="cuda") + 2 * torch.randn(C, generator=g, device="cuda")).to(dtype)
+    _compare(ops, x, groups, *_affine(C, g), workspace)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("C,groups", [(512, 1), (8, 1), (96, 32)])
 @pytest.mark.parametrize("workspace", [True, False])

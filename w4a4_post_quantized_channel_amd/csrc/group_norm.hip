@@ -21,8 +21,9 @@
 // With a workspace the positions of a sample are cut into slabs that fill the
 // card; one kernel takes the moments of each (slab, group), one writes the
 // output.  The output kernel joins the slabs itself when they are few;
-// otherwise a third kernel does.  Without a workspace, or when a sample is
-// small, one workgroup does a run of groups of a sample by itself.
+// otherwise a third kernel does.  Without a workspace, when a sample is small
+// or a group too wide, one workgroup does a run of groups of a sample by
+// itself.
 #include "activation.h"
 #include "dense.h"
 #include "device_common.h"
@@ -31,7 +32,7 @@ namespace w4a4 {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kCUs = 256;
 constexpr int kRun = 64;           // positions a thread sums in fp32 before it joins
 constexpr int kMaxSlabs = 2048;
 constexpr int kJoinInline = 64;    // slabs the output kernel joins by itself
@@ -382,9 +383,12 @@ __global__ void __launch_bounds__(kThreads) norm_whole_kernel(NormArgs g, int gp
 // Slabs of a sample: about eight workgroups a CU over all samples, at least
 // kSlabElems elements each.
 int slabs_for(int64_t N, int64_t S, int64_t C, int64_t groups) {
-  // a group wider than any workgroup's channels is not cut
-  if (C / groups > kThreads) return 1;
   const int64_t elems = S * C;
+  // Groups that fill a workgroup by themselves are cut when there are too few
+  // of them for the card and they are long.  us, cut / whole, bf16: 1 x 64 x
+  // 512 11.8 / 14.1, 2 x 4096 x 512 14.9 / 478, 128 x 64 x 1024 20.8 / 22.5,
+  // but 1 x 32 x 512 11.9 / 10.4 and 250 x 64 x 1024 34.6 / 25.0.
+  if (C / groups > kThreads && (N * groups > kCUs / 2 || elems < 4 * kSlabElems)) return 1;
   int64_t want = kMaxSlabs / N;
   if (want > elems / kSlabElems) want = elems / kSlabElems;
   if (want > S) want = S;
@@ -406,7 +410,9 @@ hipError_t run_kind(const NormArgs& g, void* workspace, hipStream_t st) {
   // where the workgroup covers all of them
   int gpb = cg >= kThreads * V ? 1 : kThreads * V / cg;
   if (gpb > g.groups) gpb = g.groups;
-  if (!workspace || slabs == 1) {
+  // A group of more channels than a workgroup covers (2048 in bf16, 1024 in
+  // fp32, fewer where alignment narrows V) is not cut.
+  if (!workspace || slabs == 1 || cg > kThreads * V) {
     // small: few channels a workgroup, so that more of them share the sample
     if (cg % V == 0)
       while (gpb > 1 && gpb * cg > 16 * V) gpb = (gpb + 1) / 2;
