@@ -23,7 +23,10 @@ and, the same two ways, each kernel of the call alone.  HIP events on the
 replay stream bracket each replay; figures are the median and the 10th /
 90th percentile over replays of the per-call average.
 
-Prints one JSON line.  ``--summarize-profiles DIR`` turns rocprofv3 output
+Prints one JSON line: the headline, its roofline, and per configuration the
+median times.  ``--details FILE`` writes the whole record (percentiles, every
+kernel's roofline, CPU baseline per configuration); the line stays short
+enough for a log's tail.  ``--summarize-profiles DIR`` turns rocprofv3 output
 of this script into the summaries under profiles/ (no GPU).
 """
 from __future__ import annotations
@@ -89,6 +92,7 @@ def parse():
     p.add_argument("--no-configs", action="store_true", help="headline step only")
     p.add_argument("--no-next", action="store_true", help="skip the next rows' workloads (W4A8, FP8)")
     p.add_argument("--no-cpu-baseline", action="store_true")
+    p.add_argument("--details", metavar="FILE", help="write the whole record there as JSON")
     p.add_argument("--copy-calibration", action="store_true",
                    help="only run a plain elementwise copy of 256 MiB five times (hardware-counter scale)")
     p.add_argument("--summarize-profiles", metavar="DIR",
@@ -691,7 +695,7 @@ def main():
             case, layer, r = measure_case(torch, f"{a.workload}:{n}" if a.workload in EXTRA else a.workload, n,
                                           a.replays)
             res.append(summarize_case(case, layer, r))
-        finish({"workload": a.workload, "configs": res}, t_start)
+        finish({"workload": a.workload, "configs": res}, t_start, a.details)
         return
 
     built, warm, flops = measure_headline(torch, HEADLINE[1], a.steps, a.replays)
@@ -775,10 +779,21 @@ def main():
                       "with BLAS on all cores of the CPU share",
             "single_thread_value": flops / (step_us["single"] * 1e-6) / 1e12,
             "host_cores": host, "cpu_model": cpu_model(), "configs": cb}
-    finish(out, t_start)
+    finish(out, t_start, a.details)
 
 
-def finish(out, t_start):
+def short_line(out):
+    """The record without what only ``--details`` keeps: under 4 KB."""
+    line = {k: v for k, v in out.items() if k not in ("configs", "next", "profile_phases", "cpu_baseline")}
+    line["ceilings"] = {k: round(v, 1) if isinstance(v, float) else v for k, v in out["ceilings"].items()}
+    line["calls_us"] = {c["id"]: {m: round(c[m]["us_per_call"]["median"], 2) for m in ("warm", "cold") if m in c}
+                        for c in out["configs"] + out["next"]}
+    if "cpu_baseline" in out:
+        line["cpu_baseline"] = {k: v for k, v in out["cpu_baseline"].items() if k not in ("configs", "sample")}
+    return line
+
+
+def finish(out, t_start, details=None):
     out["wall_s"] = time.perf_counter() - t_start
     out["profile_phases"] = PHASE_LOG
     log = os.environ.get("BENCH_PHASE_LOG")
@@ -786,7 +801,11 @@ def finish(out, t_start):
         os.makedirs(os.path.dirname(log) or ".", exist_ok=True)
         with open(log, "w") as fh:
             json.dump(PHASE_LOG, fh)
-    print(json.dumps(out), flush=True)
+    if details:
+        os.makedirs(os.path.dirname(details) or ".", exist_ok=True)
+        with open(details, "w") as fh:
+            json.dump(out, fh)
+    print(json.dumps(short_line(out) if "metric" in out else out), flush=True)
 
 
 if __name__ == "__main__":
