@@ -127,10 +127,10 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -443,13 +443,15 @@ def _ws(nbytes: int, device) -> Optional[torch.Tensor]:
     return None if nbytes == 0 else torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _together(first: torch.Tensor, **others) -> int:
-    """The address of ``first``, with every other operand on its device.  An
-    operand in host memory would fault the kernel: if ``first`` lies there the
-    address is NULL, which the library refuses after its checks of sizes."""
+def _together(names: str, first: torch.Tensor, *others) -> int:
+    """The address of ``first``, with every other operand (``names``) on its
+    device.  An operand in host memory would fault the kernel: if ``first`` lies
+    there the address is NULL, which the library refuses after its checks of
+    sizes."""
     device = first.device
-    for name, t in others.items():
+    for t in others:
         if t is not None and t.device != device:
+            name = next(n for n, o in zip(names.split(), others) if o is t)
             raise ValueError(f"{name} is on {t.device}, the first operand on {device}")
     return first.data_ptr() if first.is_cuda else 0
 
@@ -507,8 +509,8 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     if prefix_keep is not None and (prefix_keep.dtype not in (torch.bool, torch.uint8) or prefix_keep.shape != (P,)
                                     or not prefix_keep.is_contiguous()):
         raise TypeError("prefix_keep must be a contiguous bool or uint8 [P] tensor")
-    qp = _together(q, k_prefix=k_prefix, v_prefix=v_prefix, k_own=k_own, v_own=v_own, own_len=own_len,
-                   prefix_keep=prefix_keep, out=out, workspace=workspace)
+    qp = _together("k_prefix v_prefix k_own v_own own_len prefix_keep out workspace", q, k_prefix, v_prefix, k_own,
+                   v_own, own_len, prefix_keep, out, workspace)
     desc = _ATTN.pack(B, T, Hq, Hkv, D, P, S, D ** -0.5 if scale is None else scale, causal,
                       qp, qb, qt, qh, k_prefix.data_ptr(), kpp, kph, v_prefix.data_ptr(), vpp, vph,
                       k_own.data_ptr(), kob, kos, koh, v_own.data_ptr(), vob, vos, voh,
@@ -560,7 +562,7 @@ def bf16_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor
         if residual.dtype is not y.dtype or Mr != M or Nr != N:
             raise TypeError("residual must have y's shape and dtype")
         rp = residual.data_ptr()
-    xp = _together(x, w=w, bias=bias, residual=residual, y=y, workspace=workspace)
+    xp = _together("w bias residual y workspace", x, w, bias, residual, y, workspace)
     st = LIB.bf16_linear(xp, ldx, w.data_ptr(), ldw, M, N, K, _EPILOGUE.pack(code, bdt, bp, rp, ldr),
                          y.data_ptr(), _dtype_code(y), ldy, *_ws_args(workspace), _stream(stream))
     if st != 0:
@@ -587,7 +589,7 @@ def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
     for name, v in (("weight", weight), ("bias", bias)):
         if v is not None and (v.dtype != torch.float32 or v.shape != (C,) or not v.is_contiguous()):
             raise TypeError(f"{name} must be a contiguous fp32[C] tensor")
-    xp = _together(x, weight=weight, bias=bias, out=out, workspace=workspace)
+    xp = _together("weight bias out workspace", x, weight, bias, out, workspace)
     st = LIB.w4a4_group_norm_act(xp, _dtype_code(x), N, S, C, groups, x.stride(0),
                                  x.stride(1) if S > 1 else C, _ptr(weight), _ptr(bias), float(eps), _act_code(act),
                                  out.data_ptr(), out.stride(0), out.stride(1) if S > 1 else C, *_ws_args(workspace),
