@@ -15,7 +15,11 @@ struct AttnShape {
   int wq, wk, bn;
   double us;   // an iteration of a workgroup, all CUs busy
 };
-// (WQ, WK, BN) per head width; the kernels are instantiated from it.
+// (WQ, WK, BN) per head width; the kernels are instantiated from it.  The
+// times of D = 128 are fitted to measurements (see plan_attention); those of
+// the other widths are estimates that rank the tiles of one width.  An
+// iteration of the first tile of D = 256 has measured 6 us, not 3, where it
+// has half the card to itself.
 constexpr AttnShape kShapes[3][4] = {
     {{1, 8, 64, 2.0}, {2, 4, 64, 1.8}, {4, 2, 64, 2.0}, {8, 1, 64, 1.5}},      // D = 64
     {{1, 8, 32, 3.05}, {2, 4, 32, 2.3}, {4, 2, 64, 3.0}, {8, 1, 64, 2.0}},     // D = 128

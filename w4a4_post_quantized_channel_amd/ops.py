@@ -424,6 +424,12 @@ def lowrank_project(x: torch.Tensor, *, l1t: Optional[torch.Tensor] = None, idx:
 
 # ---------------------------------------------------------------------------
 # 16-bit operators beside the quantized linears
+#
+# Each takes the workspace that its make_*_workspace gives for the same sizes
+# (None where none is needed).  Called without, it computes the same on an
+# unsplit plan: right for small shapes, many times slower for those that the
+# split spreads over the card (prefix_attention over 8192 keys 3 times,
+# group_norm_act of full frames 250 times).
 # ---------------------------------------------------------------------------
 def _matrix(name: str, t: torch.Tensor):
     """(rows, columns, row stride) of a row-major matrix; the stride of a single row is not used."""
@@ -490,7 +496,8 @@ def prefix_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Te
     q [B, T, Hq, D]; k_prefix, v_prefix [P, Hkv, D]; k_own, v_own [B, S, Hkv, D]
     (all bf16, any strides that are multiples of 8, last dimension contiguous);
     own_len int32[B] or None; prefix_keep bool / uint8 [P] or None; scale
-    defaults to 1 / sqrt(D).  See include/w4a4.h for the formula and the masks.
+    defaults to 1 / sqrt(D).  Pass workspace=make_prefix_attention_workspace(...)
+    unless the prefix is short.  See include/w4a4.h for the formula and the masks.
     """
     B, T, Hq, D = q.shape
     P, Hkv, _ = k_prefix.shape
@@ -537,7 +544,8 @@ def bf16_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor
 
     w holds N rows, or 2 N for act="swiglu" (gate rows, then up rows); bias is
     fp32 or bf16 with one entry per row of w; residual has y's shape and type
-    and may be y itself.
+    and may be y itself.  Without workspace=make_bf16_linear_workspace(...) K is
+    not split, which few rows of a long K need.
     """
     M, K, ldx = _matrix("x", x)
     NW, Kw, ldw = _matrix("w", w)
@@ -578,7 +586,9 @@ def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
                    bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5, act: str = "silu",
                    out: Optional[torch.Tensor] = None, workspace=None, stream=None) -> torch.Tensor:
     """Group normalisation with an activation on channels-last features x [N, S, C]
-    (fp32 or bf16, channels contiguous; weight, bias fp32[C] or None; out may be x)."""
+    (fp32 or bf16, channels contiguous; weight, bias fp32[C] or None; out may be x).
+    Without workspace=make_group_norm_workspace(...) one workgroup takes whole
+    groups of a sample, which is for small samples only."""
     if x.dim() != 3 or x.stride(2) != 1 or x.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("x must be an fp32 or bf16 [N, S, C] tensor with contiguous channels")
     N, S, C = x.shape
