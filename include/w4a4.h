@@ -525,6 +525,185 @@ int w4a4_group_norm_act(const void* x, int32_t dtype, int64_t N, int64_t S, int6
 /* Bytes of workspace w4a4_group_norm_act uses for these sizes; 0: none. */
 size_t w4a4_group_norm_workspace(int64_t N, int64_t S, int64_t C, int64_t groups);
 
+/* ---------------------------------------------------------------------------
+ * Operators around a 4-bit key/value cache
+ *
+ * What a block of an autoregressive video or action model runs between its
+ * quantized linears: the norm in front of the projections, rotary positions
+ * on queries and keys, new keys and values written to a cache that holds them
+ * in NVFP4, and attention over that cache.  The conventions at the top of
+ * this file and those of the 16-bit operators hold here too.
+ * ------------------------------------------------------------------------- */
+
+/* A paged cache of keys and values in NVFP4 (host struct of device pointers):
+ * a page holds ``page`` consecutive tokens of one sequence, head by head.
+ *  k_codes, v_codes    uint8 [n_pages, Hkv, page, D / 2]: E2M1 nibbles, the
+ *                      even channel low.
+ *  k_scales, v_scales  uint8 [n_pages, Hkv, page, D / 16]: one OCP E4M3 scale
+ *                      per 16 channels.  w4a4_cache_append writes
+ *                      non-negative finite ones; the readers ignore the sign
+ *                      bit and take 0x7F as 480, so a cache holds no NaN
+ *                      whatever its bytes.
+ *  *_sp                bytes from page to page (multiples of 16, at least
+ *                      Hkv * page * D / 2 or / 16).
+ *  k_scale, v_scale    the static tensor scales g (> 0, finite): a value is
+ *                      E2M1 * E4M3 * g, and g = amax / (6 * 448) covers amax.
+ *                      A power of two makes every value exact in bf16.
+ * Token slot s is token s % page of page s / page.
+ * Shape rules: D is 64, 128 or 256; page is 16, 32, 64, 128 or 256;
+ * n_pages >= 1, n_pages * page < 2^31; 1 <= Hkv <= 65536.  Pointers 16-byte
+ * aligned. */
+typedef struct w4a4_kvcache {
+  int64_t n_pages, page, Hkv, D;
+  float k_scale, v_scale;
+  void* k_codes;
+  int64_t k_codes_sp;
+  void* k_scales;
+  int64_t k_scales_sp;
+  void* v_codes;
+  int64_t v_codes_sp;
+  void* v_scales;
+  int64_t v_scales_sp;
+} w4a4_kvcache;
+
+/* w4a4_cache_append -- quantises keys and values of M tokens into the cache
+ * as they are written (LatentQuant abstract: NVFP4 quantization of
+ * activations).  Codes and scales are those of quantize_act with
+ * W4A4_FMT_NVFP4, no rotation and no smoothing, on the rows of D channels.
+ *  k, v   [M, Hkv, D], dtype F32 or BF16, channels contiguous, token and head
+ *         strides (elements) multiples of 8, pointers 16-byte aligned.
+ *  slots  device int32[M]: the token slot of each row.  A slot outside the
+ *         cache skips its row.  Slots are distinct: one that is given twice
+ *         holds a mixture of its rows afterwards, other slots are right. */
+int w4a4_cache_append(const w4a4_kvcache* c, const void* k, int64_t k_sm, int64_t k_sh, const void* v, int64_t v_sm,
+                      int64_t v_sh, int32_t dtype, int64_t M, const int32_t* slots, void* stream);
+
+/* w4a4_cache_read -- keys and values of M slots as F32 or BF16 (each value
+ * E2M1 * E4M3 * g rounded once to fp32, then to the dtype).  A slot outside
+ * the cache reads as zeros; slots may repeat.  k, v as in w4a4_cache_append,
+ * written. */
+int w4a4_cache_read(const w4a4_kvcache* c, const int32_t* slots, int64_t M, void* k, int64_t k_sm, int64_t k_sh,
+                    void* v, int64_t v_sm, int64_t v_sh, int32_t dtype, void* stream);
+
+/* w4a4_cache_attention -- softmax attention of B sequences of T queries over
+ * their histories in the cache:
+ *   out[b,t,h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q[b,t,h] . k_j)
+ * over the keys j < lens[b] (causal = 0) or j <= lens[b] - T + t (causal = 1:
+ * the T queries are the sequence's last T positions) whose page is present.
+ * Key j of sequence b is token j % page of page table[b][j / page]; an entry
+ * outside [0, n_pages) is an absent page, whose keys nobody sees.  Query head
+ * h reads KV head h / (Hq / Hkv).  A row that sees no key is zero.
+ * Keys and values enter the products exactly as the cache holds them (fp16),
+ * queries as fp16 after a power of two per row, probabilities as fp16; scores,
+ * softmax sums and outputs accumulate in fp32; one rounding to bf16.
+ *  q, out    bf16 [B, T, Hq, D], channels contiguous; the other strides are
+ *            in elements, multiples of 8, at most 2^30 (batch: 2^38); those of
+ *            a dimension of one are not used.  Pointers 16-byte aligned.  out
+ *            overlaps no input.
+ *  table     device int32 [B, table_pages], row stride table_sb.
+ *  lens      device int32[B], clamped to [0, min(max_len, table_pages * page)].
+ *  max_len   an upper bound of lens that the host knows; it sizes the work.
+ * Shape rules: Hq a multiple of Hkv, Hq <= 65536; B, T <= 2^24,
+ * B T Hq <= 2^30; max_len, table_pages * page <= 2^30. */
+typedef struct w4a4_cache_attn {
+  int64_t B, T, Hq, max_len;
+  float scale;
+  int32_t causal;
+  const void* q;
+  int64_t q_sb, q_st, q_sh;
+  const int32_t* table;
+  int64_t table_sb, table_pages;
+  const int32_t* lens;
+  void* out;
+  int64_t o_sb, o_st, o_sh;
+} w4a4_cache_attn;
+int w4a4_cache_attention(const w4a4_kvcache* c, const w4a4_cache_attn* a, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Bytes of workspace w4a4_cache_attention uses for these sizes (0: none). */
+size_t w4a4_cache_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len);
+
+/* w4a4_rotary_axes -- rotary positions with one to four axes (time, height
+ * and width of a video token) on queries and keys in one launch.  Pair i of a
+ * head, of the axis a whose section it falls into, is turned by the angle
+ * pos[m][a] * f_i:
+ *   (u, w) -> (u cos - w sin, u sin + w cos)
+ * Channels behind the pairs, D - 2 * sum(sections) of them, are copied.
+ *  q, k      [M, Hq, D] and [M, Hk, D], dtype F32 or BF16, channels
+ *            contiguous, any token and head strides (elements); k may be
+ *            absent (Hk = 0).  An output may be its own input (same strides),
+ *            otherwise it overlaps no input.
+ *  pos       [M, axes], int32 or fp32 (pos_dtype I32 or F32), row stride pos_sm.
+ *  sections  pairs of each axis, in order (0 allowed; unused axes 0).
+ *  pairs     W4A4_PAIRS_ADJACENT: channels 2 i and 2 i + 1;
+ *            W4A4_PAIRS_HALVES: channels i and i + sum(sections).
+ *  table     device fp32 [sum(sections)][2]: f_i / (2 pi) as the sum of two
+ *            fp32 numbers, so that far positions keep their angle: angles are
+ *            reduced to a turn in twice 24 bits, products are fp32, one
+ *            rounding to the dtype.
+ * Shape rules: D even, 2 <= D <= 1024; M < 2^31; Hq + Hk <= 65536; Hq >= 1. */
+enum { W4A4_PAIRS_ADJACENT = 0, W4A4_PAIRS_HALVES = 1 };
+typedef struct w4a4_rotary {
+  int64_t M, Hq, Hk, D;
+  int32_t dtype, pos_dtype, axes, pairs;
+  int32_t sections[4];
+  const void* pos;
+  int64_t pos_sm;
+  const float* table;
+  const void* q;
+  int64_t q_sm, q_sh;
+  void* q_out;
+  int64_t qo_sm, qo_sh;
+  const void* k;
+  int64_t k_sm, k_sh;
+  void* k_out;
+  int64_t ko_sm, ko_sh;
+} w4a4_rotary;
+int w4a4_rotary_axes(const w4a4_rotary* r, void* stream);
+
+/* w4a4_gated_norm -- the residual step behind a block, fused with the norm of
+ * the block's output and the modulated norm in front of the next block:
+ *   u  = h,  or  h / sqrt(mean(h^2) + eps) * post_weight  if that is given
+ *   x' = alpha * x + gate[r] * u
+ *   y  = (norm(x') * weight + bias) * (1 + scale[r]) + shift[r]
+ * for M rows of C channels; norm is the layer norm (x' - mean) / sqrt(var +
+ * eps) or, for W4A4_NORM_RMS, x' / sqrt(mean(x'^2) + eps).  Row m takes row
+ * r = m / (M / R) of the modulations (R = 1: one for all, R = M: one a token).
+ * y is computed from x' before its rounding to x's dtype.
+ *  x, x_out   x_dtype F32 or BF16, row strides ldx, ldxo; x_out may be x
+ *             (same stride) or NULL (not stored).
+ *  h          h_dtype F32 or BF16, row stride ldh, or NULL: x' = alpha * x.
+ *  y          y_dtype F32 or BF16, row stride ldy, or NULL (x_out alone).
+ *  gate, scale, shift      fp32 [R, C], row strides, or NULL (1, 0, 0).
+ *  post_weight, weight, bias  fp32[C] or NULL (no norm of h; 1; 0).
+ * All arithmetic in fp32, one rounding per output; outputs overlap no input
+ * but x_out = x.  Shape rules: 1 <= C <= 16384; M < 2^31; M a multiple of R;
+ * eps >= 0. */
+enum { W4A4_NORM_LAYER = 0, W4A4_NORM_RMS = 1 };
+typedef struct w4a4_gated {
+  int64_t M, C, R;
+  float alpha, eps;
+  int32_t kind, x_dtype, h_dtype, y_dtype;
+  const void* x;
+  int64_t ldx;
+  const void* h;
+  int64_t ldh;
+  const float* gate;
+  int64_t gate_sr;
+  const float* scale;
+  int64_t scale_sr;
+  const float* shift;
+  int64_t shift_sr;
+  const float* post_weight;
+  const float* weight;
+  const float* bias;
+  void* x_out;
+  int64_t ldxo;
+  void* y;
+  int64_t ldy;
+} w4a4_gated;
+int w4a4_gated_norm(const w4a4_gated* g, void* stream);
+
 const char* w4a4_status_string(int status);
 const char* w4a4_last_error(void);
 int w4a4_abi_version(void);

@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw4a4.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 SOURCES = ["quantize.hip", "gemm_int.hip", "gemm_wide.hip", "branch.hip", "gptq.hip", "attention.hip",
-           "gemm_bf16.hip", "group_norm.hip", "abi.cpp", "abi_dense.cpp"]
+           "gemm_bf16.hip", "group_norm.hip", "kv_cache.hip", "cache_attention.hip", "rotary.hip", "gated_norm.hip",
+           "abi.cpp", "abi_dense.cpp", "abi_cache.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-ffp-contract=off",

@@ -8,6 +8,7 @@ no fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 from typing import Optional
@@ -35,6 +36,8 @@ EXPORTS = ["quantize_act", "quantize_act_gather", "quantize_act_lowrank", "quant
            "w4a4_workspace_size", "w4a4_status_string",
            "w4a4_prefix_attention", "w4a4_prefix_attention_workspace", "bf16_linear", "w4a4_bf16_workspace_size",
            "w4a4_group_norm_act", "w4a4_group_norm_workspace",
+           "w4a4_cache_append", "w4a4_cache_read", "w4a4_cache_attention", "w4a4_cache_attention_workspace",
+           "w4a4_rotary_axes", "w4a4_gated_norm",
            "w4a4_last_error", "w4a4_abi_version"]
 
 
@@ -54,6 +57,10 @@ _ATTN = struct.Struct("7qfi" + "4q" + "3q3q" + "4q4q" + "2q" + "4q")
 
 
 _EPILOGUE = struct.Struct("2i3q")   # w4a4_epilogue
+_KVCACHE = struct.Struct("4q2f8q")   # w4a4_kvcache
+_CACHE_ATTN = struct.Struct("4qfi" + "4q" + "3q" + "q" + "4q")   # w4a4_cache_attn
+_ROTARY = struct.Struct("4q4i4i" + "3q" + "12q")   # w4a4_rotary
+_GATED = struct.Struct("3q2f4i" + "4q" + "6q" + "3q" + "4q")   # w4a4_gated
 
 
 class W4A4Error(RuntimeError):
@@ -94,6 +101,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "w4a4_bf16_workspace_size": [i64, i64, i64, i32],
         "w4a4_group_norm_act": [vp, i32, i64, i64, i64, i64, i64, i64, vp, vp, f32, i32, vp, i64, i64, vp, sz, vp],
         "w4a4_group_norm_workspace": [i64] * 4,
+        "w4a4_cache_append": [ctypes.c_char_p, vp, i64, i64, vp, i64, i64, i32, i64, vp, vp],   # a packed w4a4_kvcache
+        "w4a4_cache_read": [ctypes.c_char_p, vp, i64, vp, i64, i64, vp, i64, i64, i32, vp],
+        "w4a4_cache_attention": [ctypes.c_char_p, ctypes.c_char_p, vp, sz, vp],
+        "w4a4_cache_attention_workspace": [i64] * 6,
+        "w4a4_rotary_axes": [ctypes.c_char_p, vp],   # a packed w4a4_rotary
+        "w4a4_gated_norm": [ctypes.c_char_p, vp],    # a packed w4a4_gated
         "w4a4_status_string": [ctypes.c_int],
         "w4a4_last_error": [],
         "w4a4_abi_version": [],
@@ -107,6 +120,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.w4a4_prefix_attention_workspace.restype = ctypes.c_size_t
     lib.w4a4_bf16_workspace_size.restype = ctypes.c_size_t
     lib.w4a4_group_norm_workspace.restype = ctypes.c_size_t
+    lib.w4a4_cache_attention_workspace.restype = ctypes.c_size_t
     lib.w4a4_lowrank_width.restype = ctypes.c_int64
     lib.w4a4_status_string.restype = ctypes.c_char_p
     lib.w4a4_last_error.restype = ctypes.c_char_p
@@ -607,3 +621,279 @@ def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
     if st != 0:
         _check("w4a4_group_norm_act", st)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Operators around a 4-bit key/value cache
+#
+# These check that their operands lie on the current device, whose stream they
+# take.
+# ---------------------------------------------------------------------------
+def _stream_for(t, stream) -> int:
+    """The stream of a call on ``t``'s device, which has to be the current one."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"the operands are on {t.device}, the current device is cuda:{torch.cuda.current_device()}: "
+                         f"call under torch.cuda.device({t.device.index})")
+    return _stream(stream)
+
+
+class KVCache:
+    """A paged cache of keys and values in NVFP4 (see w4a4_kvcache in include/w4a4.h).
+
+    k_codes, v_codes uint8 [n_pages, Hkv, page, D / 2]; k_scales, v_scales uint8
+    [n_pages, Hkv, page, D / 16]; pages contiguous inside, any stride from page to
+    page that is a multiple of 16 bytes.  k_scale, v_scale: the static tensor scales
+    (nvfp4_scale_from_amax of calibration data; rounded up to a power of two, every
+    value is exact in bf16).  The tensors may be written between calls, not replaced.
+    """
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+                 k_scale: float = 1.0, v_scale: float = 1.0):
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [n_pages, Hkv, page, D / 2]")
+        n, H, page, half = k_codes.shape
+        self.n_pages, self.Hkv, self.page, self.D = n, H, page, 2 * half
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self.device = k_codes.device
+        strides = []
+        for name, width in (("k_codes", half), ("k_scales", half // 8), ("v_codes", half), ("v_scales", half // 8)):
+            t = getattr(self, name)
+            if t.dtype is not torch.uint8:
+                raise TypeError(f"{name} must be uint8")
+            if t.shape != (n, H, page, width):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, H, page, width)}")
+            if not t[:1].is_contiguous():
+                raise ValueError(f"a page of {name} must be contiguous")
+            strides.append(t.stride(0) if n > 1 else H * page * width)
+        _together("k_scales v_codes v_scales", k_codes, k_scales, v_codes, v_scales)
+        at = [t.data_ptr() if t.is_cuda else 0 for t in (k_codes, k_scales, v_codes, v_scales)]
+        self._desc = _KVCACHE.pack(n, page, H, 2 * half, self.k_scale, self.v_scale, at[0], strides[0], at[1], strides[1],
+                                   at[2], strides[2], at[3], strides[3])
+
+
+def make_kv_cache(n_pages: int, page: int, Hkv: int, D: int, k_scale: float = 1.0, v_scale: float = 1.0,
+                  device="cuda") -> KVCache:
+    """An empty cache (its bytes are whatever the allocator gave; only slots that were appended mean anything)."""
+    def new(width):
+        return torch.empty((n_pages, Hkv, page, width), dtype=torch.uint8, device=device)
+
+    return KVCache(new(D // 2), new(D // 16), new(D // 2), new(D // 16), k_scale, v_scale)
+
+
+def _cache_rows(name: str, t: torch.Tensor, shape, dtype):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return st
+
+
+def _check_slots(slots: torch.Tensor) -> int:
+    if slots.dtype is not torch.int32 or slots.dim() != 1 or not slots.is_contiguous():
+        raise TypeError("slots must be a contiguous int32 vector")
+    return slots.shape[0]
+
+
+def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *, stream=None) -> None:
+    """Quantises k, v [M, Hkv, D] (both fp32 or bf16, strides multiples of 8) into the token slots int32[M]
+    of the cache (slot = page * cache.page + token of the page; one outside the cache skips its row; distinct)."""
+    M = _check_slots(slots)
+    shape = (M, cache.Hkv, cache.D)
+    km, kh, _ = _cache_rows("k", k, shape, k.dtype)
+    vm, vh, _ = _cache_rows("v", v, shape, k.dtype)
+    kp = _together("v slots cache", k, v, slots, cache)
+    st = LIB.w4a4_cache_append(cache._desc, kp, km, kh, v.data_ptr(), vm, vh, _dtype_code(k), M, slots.data_ptr(),
+                               _stream_for(k, stream))
+    if st != 0:
+        _check("w4a4_cache_append", st)
+
+
+def cache_read(cache: KVCache, slots: torch.Tensor, *, k: Optional[torch.Tensor] = None,
+               v: Optional[torch.Tensor] = None, dtype=torch.bfloat16, stream=None):
+    """Keys and values [M, Hkv, D] of the slots int32[M] (zeros for a slot outside the cache), as bf16 or fp32."""
+    M = _check_slots(slots)
+    shape = (M, cache.Hkv, cache.D)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=slots.device)
+    if v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=slots.device)
+    km, kh, _ = _cache_rows("k", k, shape, k.dtype)
+    vm, vh, _ = _cache_rows("v", v, shape, k.dtype)
+    kp = _together("v slots cache", k, v, slots, cache)
+    st = LIB.w4a4_cache_read(cache._desc, slots.data_ptr(), M, kp, km, kh, v.data_ptr(), vm, vh, _dtype_code(k),
+                             _stream_for(k, stream))
+    if st != 0:
+        _check("w4a4_cache_read", st)
+    return k, v
+
+
+def cache_attention_workspace_size(B: int, T: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
+    return int(LIB.w4a4_cache_attention_workspace(B, T, Hq, Hkv, D, max_len))
+
+
+def make_cache_attention_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, max_len: int,
+                                   device="cuda") -> Optional[torch.Tensor]:
+    return _ws(cache_attention_workspace_size(B, T, Hq, Hkv, D, max_len), device)
+
+
+def cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor, *, causal: bool = False,
+                    scale: Optional[float] = None, max_len: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                    workspace=None, stream=None) -> torch.Tensor:
+    """Attention of q [B, T, Hq, D] (bf16) over each sequence's history in the cache.
+
+    table int32 [B, pages] lists a sequence's pages (an entry outside the cache is an
+    absent page, whose keys nobody sees), lens int32[B] its keys; causal: the T queries
+    are its last T positions.  max_len (default: the table's reach) is a bound of lens
+    that the host knows; pass workspace=make_cache_attention_workspace(...) for the
+    same max_len.  scale defaults to 1 / sqrt(D).  See include/w4a4.h.
+    """
+    B, T, Hq, D = q.shape
+    if D != cache.D:
+        raise ValueError(f"q has head width {D}, the cache {cache.D}")
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    qb, qt, qh, _ = _attn_operand("q", q, (B, T, Hq, D))
+    ob, ot, oh, _ = _attn_operand("out", out, (B, T, Hq, D))
+    if table.dtype is not torch.int32 or table.dim() != 2 or table.shape[0] != B or (
+            table.shape[1] > 1 and table.stride(1) != 1):
+        raise TypeError("table must be an int32 [B, pages] tensor with contiguous rows")
+    if lens.dtype is not torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
+        raise TypeError("lens must be a contiguous int32[B] tensor")
+    pages = table.shape[1]
+    qp = _together("table lens out workspace cache", q, table, lens, out, workspace, cache)
+    desc = _CACHE_ATTN.pack(B, T, Hq, pages * cache.page if max_len is None else max_len,
+                            D ** -0.5 if scale is None else scale, causal, qp, qb, qt, qh, table.data_ptr(),
+                            table.stride(0), pages, lens.data_ptr(), out.data_ptr(), ob, ot, oh)
+    st = LIB.w4a4_cache_attention(cache._desc, desc, *_ws_args(workspace), _stream_for(q, stream))
+    if st != 0:
+        _check("w4a4_cache_attention", st)
+    return out
+
+
+class RotaryTable:
+    """Frequencies of rotary_axes: ``sections`` pairs of each axis, ``turns`` fp32 [pairs, 2] (see make_rotary_table)."""
+
+    def __init__(self, sections, turns: torch.Tensor):
+        self.sections, self.turns = tuple(int(s) for s in sections), turns
+        if not 1 <= len(self.sections) <= 4:
+            raise ValueError("one to four axes")
+        if turns.dtype is not torch.float32 or turns.shape != (sum(self.sections), 2) or not turns.is_contiguous():
+            raise TypeError("turns must be a contiguous fp32 [sum(sections), 2] tensor")
+        self._packed = self.sections + (0,) * (4 - len(self.sections))
+
+
+def make_rotary_table(sections, theta: float = 10000.0, *, freqs=None, device="cuda") -> RotaryTable:
+    """The table of rotary_axes for ``sections`` pairs of each axis: pair i of an axis with s pairs turns by
+    theta ** (-i / s) a position.  ``freqs`` gives the frequencies of all pairs instead (radians a position)."""
+    sections = [int(s) for s in sections]
+    if freqs is None:
+        freqs = [theta ** (-i / s) for s in sections for i in range(s)]
+    turns = torch.as_tensor(freqs, dtype=torch.float64).cpu() / (2.0 * math.pi)
+    if turns.shape != (sum(sections),):
+        raise ValueError(f"{tuple(turns.shape)} frequencies for {sum(sections)} pairs")
+    hi = turns.float()
+    return RotaryTable(sections, torch.stack([hi, (turns - hi.double()).float()], dim=1).contiguous().to(device))
+
+
+def rotary_axes(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, table: RotaryTable, *,
+                interleaved: bool = True, q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                stream=None):
+    """Rotary positions with one to four axes on q [M, Hq, D] and k [M, Hk, D] (or None), fp32 or bf16.
+
+    pos int32 or fp32 [M, axes]; interleaved: pairs are channels 2 i and 2 i + 1, otherwise i and
+    i + pairs; channels behind the pairs are copied.  q_out / k_out may be q / k themselves.
+    Returns (q_out, k_out).
+    """
+    M, Hq, D = q.shape
+    if q_out is None:
+        q_out = torch.empty((M, Hq, D), dtype=q.dtype, device=q.device)
+    qm, qh, _ = _cache_rows("q", q, (M, Hq, D), q.dtype)
+    qom, qoh, _ = _cache_rows("q_out", q_out, (M, Hq, D), q.dtype)
+    Hk, kp, km, kh, kop, kom, koh = 0, 0, 0, 0, 0, 0, 0
+    if k is not None:
+        Hk = k.shape[1]
+        if k_out is None:
+            k_out = torch.empty((M, Hk, D), dtype=q.dtype, device=q.device)
+        km, kh, _ = _cache_rows("k", k, (M, Hk, D), q.dtype)
+        kom, koh, _ = _cache_rows("k_out", k_out, (M, Hk, D), q.dtype)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    axes = len(table.sections)
+    if pos.dtype not in (torch.int32, torch.float32) or pos.shape != (M, axes) or (axes > 1 and pos.stride(1) != 1):
+        raise TypeError(f"pos must be an int32 or fp32 [{M}, {axes}] tensor with contiguous rows")
+    qp = _together("k pos table q_out k_out", q, k, pos, table.turns, q_out, k_out)
+    st = LIB.w4a4_rotary_axes(
+        _ROTARY.pack(M, Hq, Hk, D, _dtype_code(q), _dtype_code(pos), axes, 0 if interleaved else 1, *table._packed,
+                     pos.data_ptr(), pos.stride(0), table.turns.data_ptr(), qp, qm, qh, q_out.data_ptr(), qom, qoh,
+                     kp, km, kh, kop, kom, koh), _stream_for(q, stream))
+    if st != 0:
+        _check("w4a4_rotary_axes", st)
+    return q_out, k_out
+
+
+NORMS = {"layer": 0, "rms": 1}
+
+
+def gated_norm(x: torch.Tensor, h: Optional[torch.Tensor] = None, *, gate: Optional[torch.Tensor] = None,
+               alpha: float = 1.0, post_weight: Optional[torch.Tensor] = None, kind: str = "layer",
+               weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               scale: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None, eps: float = 1e-6,
+               x_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, y_dtype=torch.bfloat16,
+               norm: bool = True, stream=None):
+    """The residual step behind a block and the norm in front of the next one:
+
+        x' = alpha x + gate * h              (h: rms-normed with post_weight first, if that is given)
+        y  = (norm(x') weight + bias) (1 + scale) + shift
+
+    x, h [M, C] (fp32 or bf16 each); gate, scale, shift fp32 [R, C], M a multiple of R (R = 1: one for
+    all rows, R = M: one a row); post_weight, weight, bias fp32[C]; kind "layer" or "rms".  x_out may be
+    x itself.  norm=False leaves y out, and without h there is no x_out unless it is passed.
+    Returns (x_out, y).
+    """
+    if kind not in NORMS:
+        raise ValueError(f"unknown norm {kind!r}: one of {sorted(NORMS)}")
+    M, C, ldx = _matrix("x", x)
+    if x_out is None and h is not None:
+        x_out = torch.empty((M, C), dtype=x.dtype, device=x.device)
+    if y is None and norm:
+        y = torch.empty((M, C), dtype=y_dtype, device=x.device)
+    at, ld = [0] * 3, [0] * 3
+    for i, (name, t) in enumerate((("h", h), ("x_out", x_out), ("y", y))):
+        if t is None:
+            continue
+        rows, cols, ld[i] = _matrix(name, t)
+        if rows != M or cols != C:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(M, C)}")
+        at[i] = t.data_ptr()
+    if x_out is not None and x_out.dtype is not x.dtype:
+        raise TypeError("x_out must have x's dtype")
+    R, mods = None, []
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is None:
+            mods += [0, 0]
+            continue
+        rows, cols, s = _matrix(name, t)
+        if t.dtype is not torch.float32:
+            raise TypeError(f"{name} must be fp32")
+        if cols != C or (R is not None and rows != R):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows if R is None else R, C)}")
+        R = rows
+        mods += [t.data_ptr(), s]
+    vecs = []
+    for name, t in (("post_weight", post_weight), ("weight", weight), ("bias", bias)):
+        if t is not None and (t.dtype is not torch.float32 or t.shape != (C,) or not t.is_contiguous()):
+            raise TypeError(f"{name} must be a contiguous fp32[C] tensor")
+        vecs.append(0 if t is None else t.data_ptr())
+    xp = _together("h gate scale shift post_weight weight bias x_out y", x, h, gate, scale, shift, post_weight, weight,
+                   bias, x_out, y)
+    xdt = _dtype_code(x)
+    st = LIB.w4a4_gated_norm(
+        _GATED.pack(M, C, 1 if R is None else R, alpha, eps, NORMS[kind], xdt, xdt if h is None else _dtype_code(h),
+                    xdt if y is None else _dtype_code(y), xp, ldx, at[0], ld[0], *mods, *vecs, at[1], ld[1], at[2], ld[2]),
+        _stream_for(x, stream))
+    if st != 0:
+        _check("w4a4_gated_norm", st)
+    return x_out, y
