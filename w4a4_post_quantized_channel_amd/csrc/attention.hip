@@ -45,6 +45,7 @@
 #include "attention_plan.h"
 #include "dense.h"
 #include "device_common.h"
+#include "divisor.h"
 #include "lds_sync.h"
 
 namespace w4a4 {
@@ -58,22 +59,6 @@ typedef const __attribute__((address_space(3))) v4i lds_v4i;
 
 constexpr float kLazy = 8.f;
 constexpr int kNoBad = 1 << 30;
-
-// Division by a number fixed for a launch: m = floor(2^32 / d) + 1 gives the
-// quotient or one more (2^32 - 1 for d = 1: or one less).
-struct Divisor {
-  uint32_t d, m;
-};
-inline Divisor divisor(int64_t d) {
-  return {(uint32_t)d, d == 1 ? 0xFFFFFFFFu : (uint32_t)((1ull << 32) / (uint64_t)d + 1)};
-}
-__device__ __forceinline__ int div_by(int x, const Divisor& v, int& rem) {
-  int q = (int)__umulhi((uint32_t)x, v.m), r = x - q * (int)v.d;
-  if (r < 0) --q, r += (int)v.d;
-  if (r >= (int)v.d) ++q, r -= (int)v.d;
-  rem = r;
-  return q;
-}
 
 struct AttnArgs {
   w4a4_attn a;

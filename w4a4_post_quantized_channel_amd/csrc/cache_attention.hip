@@ -1,99 +1,499 @@
 // Attention over the 4-bit key/value cache.
 //
-// A wave takes one query head of one token: 64 keys at a time, one a lane,
-// their scores, the running maximum and sum of the softmax, then the values
-// channel by channel.
+// Mathematics.  The rows of a sequence and KV head are its queries (row = t G
+// + g, G query heads per KV head).  Keys come in blocks of 64; a row keeps its
+// running maximum m (in units of exp2), its sum l and its output o in fp32:
+//   p = exp2(c s - m),  l += sum p,  o += p V,   c = scale log2 e * k_scale.
+// m only moves when a score exceeds it by more than kLazy: until then p is at
+// most 2^kLazy, which costs no accuracy (p and l scale alike), and o and l
+// need no rescaling.
+//
+// Types.  A cached value code * e (E2M1 times E4M3, at most six significant
+// bits, 2^-10 to 2880) is exact in fp16, so both products run on fp16 matrix
+// instructions with nothing lost on the cache's side; the static scales k_scale
+// and v_scale enter c and the last division.  A query row is multiplied by the
+// power of two that puts its largest channel at 2^13: bf16's eight bits then
+// fit fp16 for every channel down to 2^-27 of the largest.  Probabilities are
+// rounded to fp16 (2^-12 of them, a sixteenth of the output's own rounding).
+//
+// A wave works alone on every kFewWaves-th block of its workgroup's part, for
+// 16 MT rows at once:
+//  - S^T = K Q^T with v_mfma_f32_16x16x32_f16.  The order of channels inside a
+//    product is free, so lane (key r, group g) takes the D / 4 channels from
+//    g D / 4: they lie side by side, and a key's codes go from global memory
+//    straight into the operand (convert, times scale), never through LDS.
+//  - O^T = V^T P^T takes keys as the inner index.  A lane holds of its query
+//    the scores of keys 16 t + 4 g + i, and P^T takes them in that order, so P
+//    never moves between lanes.  V's codes go through LDS as they are, and the
+//    4-bit transposing read (16 rows x 16 channels per 16 lanes) hands each
+//    lane 16 keys of one channel in the same order; their scales lie in LDS as
+//    fp16, one row of 64 keys per 16 channels.
+// The waves' (m, l, o) are joined through LDS, the parts through the workspace
+// by a second kernel.
 #include "cache.h"
+#include "cache_attention_plan.h"
 #include "device_common.h"
+#include "divisor.h"
 
 namespace w4a4 {
 
 namespace {
 
-__device__ __forceinline__ float e2m1(uint32_t c) {
-  const uint32_t n = c & 7u;
-  const float mag = n < 2 ? 0.5f * n : __uint_as_float(((n >> 1) + 126u) << 23 | (n & 1u) << 22);
-  return c & 8u ? -mag : mag;
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) v2i lds_v2i;
+
+constexpr float kLazy = 8.f;
+constexpr int NW = kFewWaves, BN = kCacheBlock;
+
+struct Args {
+  w4a4_kvcache c;
+  w4a4_cache_attn a;
+  int rows;              // T G rows of a sequence and KV head
+  int lp;                // log2 of the page
+  Divisor g, tiles, heads, parts;
+  float c2;              // > 0
+  float qmul;            // 1, -1 (scale < 0) or 0 (scale of zero: c2 is 1)
+  float* po;             // parts > 1: [part][b][head][row][D], else null
+  float* pml;            // [part][b][head][row][2]
+};
+
+// N bytes of a lane's codes or scales, in 32-bit words.
+template <int BYTES>
+struct Words {
+  static constexpr int N = BYTES < 4 ? 1 : BYTES / 4;
+  uint32_t w[N];
+};
+template <int BYTES>
+__device__ __forceinline__ Words<BYTES> load_words(const uint8_t* p) {
+  Words<BYTES> r;
+  if constexpr (BYTES == 1) r.w[0] = *p;
+  else if constexpr (BYTES == 2) r.w[0] = *reinterpret_cast<const uint16_t*>(p);
+  else if constexpr (BYTES == 4) r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  else if constexpr (BYTES == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = v.x, r.w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+    }
+  }
+  return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(64) attn_row_kernel(w4a4_kvcache c, w4a4_cache_attn a) {
-  __shared__ float q[D], ps[64];
-  __shared__ int pages[64];
-  const int lane = threadIdx.x;
-  const int64_t row = blockIdx.x;
-  const int h = (int)(row % a.Hq), t = (int)(row / a.Hq % a.T), b = (int)(row / a.Hq / a.T);
-  const int hk = h / (int)(a.Hq / c.Hkv), page = (int)c.page;
-  for (int d = lane; d < D; d += 64)
-    q[d] = bf16_bits_to_f32(((const uint16_t*)a.q)[b * a.q_sb + t * a.q_st + h * a.q_sh + d]) * a.scale * c.k_scale;
-  int64_t len = a.lens[b];
-  len = len < a.max_len ? len : a.max_len;
-  len = len < a.table_pages * page ? len : a.table_pages * page;
-  if (a.causal) len = len - a.T + t + 1;
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, o[D / 64] = {};
-  for (int64_t j0 = 0; j0 < len; j0 += 64) {
-    const int64_t j = j0 + lane;
-    int pg = -1;
-    if (j < len) pg = a.table[b * a.table_sb + j / page];
-    if (pg < 0 || pg >= c.n_pages) pg = -1;
-    float s = -INFINITY;
-    if (pg >= 0) {
-      const int64_t r = (int64_t)hk * page + j % page;
-      const uint8_t* cd = (const uint8_t*)c.k_codes + pg * c.k_codes_sp + r * (D / 2);
-      const uint8_t* sc = (const uint8_t*)c.k_scales + pg * c.k_scales_sp + r * (D / 16);
-      s = 0.f;
-      for (int k = 0; k < D / 16; ++k) {
-        float x = 0.f;
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t w = cd[k * 8 + i];
-          x += e2m1(w) * q[k * 16 + 2 * i] + e2m1(w >> 4) * q[k * 16 + 2 * i + 1];
-        }
-        s += x * e4m3_to_f32(sc[k] & 0x7Fu);
+// E4M3 magnitude times 2^-8 as fp16: the seven bits are an fp16 number's upper
+// ones with another bias (subnormals included; 0x7F reads as 480).
+__device__ __forceinline__ uint32_t scale_bits(uint32_t byte) { return (byte & 0x7Fu) << 7; }
+__device__ __forceinline__ v2h both(uint32_t bits) { return __builtin_bit_cast(v2h, bits | bits << 16); }
+
+// Eight codes times 2^8 times their scales (as scale_bits gives them, in pairs).
+__device__ __forceinline__ v8h decode8(uint32_t w, v2h s0, v2h s1, v2h s2, v2h s3) {
+  const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.f, 0) * s0;
+  const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.f, 1) * s1;
+  const v2h c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.f, 2) * s2;
+  const v2h d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.f, 3) * s3;
+  return (v8h){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Maximum and sum over the four lane groups that hold a query.
+__device__ __forceinline__ float group_max(float x) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float group_sum(float x) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){a, b}, v2bf));
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){a, b}, v2h));
+}
+
+// The factor 2^(13 - floor(log2 amax)) of a query row, and its inverse.  Rows
+// of infinities keep theirs (factor 2^-114: Inf stays Inf), zeros stay zero.
+__device__ __forceinline__ float row_factor(float amax, float& inverse) {
+  int e = (int)(__float_as_uint(amax) >> 23);
+  e = e < 14 ? 14 : e > 254 ? 254 : e;
+  inverse = __uint_as_float((uint32_t)(e - 13) << 23);
+  return __uint_as_float((uint32_t)(267 - e) << 23);
+}
+
+template <int D_, int MT_>
+struct Few {
+  static constexpr int D = D_, MT = MT_, R = 16 * MT;
+  static constexpr int KS = D / 32;             // steps of the first product
+  static constexpr int DT = D / 16;             // channel tiles, scales of a row
+  static constexpr int CB = D / 8;              // bytes of codes a lane takes of a key
+  static constexpr int VCH = D / 16;            // 8-byte chunks of a value row
+  static constexpr int VCODES = BN * D / 2, VSCALES = DT * BN * 2;
+  static constexpr int WAVE = VCODES + VSCALES;
+  static constexpr int PITCH = D + 4;           // floats of a row in the join
+  static constexpr int JOIN = NW * R * (PITCH + 2) * 4;
+  static constexpr int LDS = NW * WAVE > JOIN ? NW * WAVE : JOIN;
+};
+
+// Keys a query row sees: those below its limit.
+__device__ __forceinline__ int row_limit(const Args& p, int len, int t) {
+  return p.a.causal ? len - (int)p.a.T + t + 1 : len;
+}
+
+template <typename C>
+__global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_kernel(Args p) {
+  constexpr int D = C::D, MT = C::MT, R = C::R, KS = C::KS, DT = C::DT;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // workgroup -> (sequence, head, part, tile): the tiles that read the same
+  // keys follow each other on an XCD
+  const int nwg = gridDim.x, wid = blockIdx.x;
+  const int u = nwg % 8 == 0 ? (wid % 8) * (nwg / 8) + wid / 8 : wid;
+  int tile, part, hk;
+  const int b = div_by(div_by(div_by(u, p.tiles, tile), p.parts, part), p.heads, hk);
+  const w4a4_kvcache& c = p.c;
+  const w4a4_cache_attn& a = p.a;
+  const int G = (int)p.g.d, page = 1 << p.lp;
+
+  const int r0 = tile * R, nrows = min(R, p.rows - r0);
+  int rem;
+  const int64_t reach = min(a.max_len, a.table_pages << p.lp);
+  const int len = (int)max((int64_t)0, min((int64_t)a.lens[b], reach));
+  const int first = row_limit(p, len, div_by(r0, p.g, rem));            // the tile's lowest limit
+  const int last = row_limit(p, len, div_by(r0 + nrows - 1, p.g, rem));   // and highest
+  const int nblk = (max(last, 0) + BN - 1) / BN;
+  const int per = (nblk + (int)p.parts.d - 1) / (int)p.parts.d;
+  const int lo = min(part * per, nblk), hi = min(lo + per, nblk);
+  const int32_t* table = a.table + b * a.table_sb;
+
+  // pages of a block's four groups of 16 keys, one a lane group; -1: absent
+  auto load_pages = [&](int blk) {
+    const int j = blk * BN + 16 * lg;
+    return blk < hi && j < last ? table[j >> p.lp] : -1;
+  };
+  struct Block {
+    Words<C::CB> k[4];
+    Words<C::CB / 8> ks[4];
+    Words<C::CB> v[4];
+    Words<DT> vs;
+    uint32_t bad;   // groups whose page is absent
+  };
+  const uint8_t* kc = (const uint8_t*)c.k_codes + (int64_t)hk * page * (D / 2) + lr * (D / 2) + lg * C::CB;
+  const uint8_t* ks = (const uint8_t*)c.k_scales + (int64_t)hk * page * DT + lr * DT + lg * (DT / 4);
+  const uint8_t* vc = (const uint8_t*)c.v_codes + (int64_t)hk * page * (D / 2) + lane * C::CB;
+  const uint8_t* vs = (const uint8_t*)c.v_scales + (int64_t)hk * page * DT + lr * DT;
+  auto load_block = [&](int blk, int pg) {
+    Block x;
+    const bool absent = pg < 0 || pg >= c.n_pages;
+    if (absent) pg = 0;                          // any page: its keys are excluded
+    const uint64_t m = __ballot(absent);
+    x.bad = (uint32_t)(m & 1) | (uint32_t)(m >> 15 & 2) | (uint32_t)(m >> 30 & 4) | (uint32_t)(m >> 45 & 8);
+    const int j0 = blk * BN;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int64_t pt = __builtin_amdgcn_readlane(pg, 16 * t);
+      const int tok = (j0 + 16 * t) & (page - 1);
+      x.k[t] = load_words<C::CB>(kc + (pt * c.k_codes_sp + tok * (D / 2)));
+      x.ks[t] = load_words<C::CB / 8>(ks + (pt * c.k_scales_sp + tok * DT));
+      x.v[t] = load_words<C::CB>(vc + (pt * c.v_codes_sp + tok * (D / 2)));
+    }
+    x.vs = load_words<DT>(vs + (pg * c.v_scales_sp + ((j0 + 16 * lg) & (page - 1)) * DT));
+    return x;
+  };
+
+  int pg0 = load_pages(lo + wave), pg1 = load_pages(lo + wave + NW);
+
+  // queries, limits
+  v8h qf[MT][KS];
+  float cr[MT], m[MT], l[MT];
+  int lim[MT];
+#pragma unroll
+  for (int x = 0; x < MT; ++x) {
+    const int row = r0 + min(x * 16 + lr, nrows - 1);    // rows past the end repeat the last
+    int g;
+    const int t = div_by(row, p.g, g);
+    lim[x] = row_limit(p, len, t);
+    const uint16_t* q = (const uint16_t*)a.q + b * a.q_sb + t * a.q_st + (int64_t)(hk * G + g) * a.q_sh + lg * (D / 4);
+    float f[KS][8], amax = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint4 v = *reinterpret_cast<const uint4*>(q + 8 * s);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[s][2 * i] = __uint_as_float(w[i] << 16);
+        f[s][2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        amax = fmaxf(amax, fmaxf(__builtin_fabsf(f[s][2 * i]), __builtin_fabsf(f[s][2 * i + 1])));
       }
     }
-    float mx = s;
-    for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-    const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.f : mn;
-    const float p = pg >= 0 ? expf(s - ms) : 0.f, f = expf(m - ms);
-    m = mn;
-    l = l * f + p;
-    ps[lane] = p;
-    pages[lane] = pg;
-    __syncthreads();
-    for (int e = 0; e < D / 64; ++e) {
-      const int d = e * 64 + lane;
-      float acc = 0.f;
-      for (int k = 0; k < 64; ++k) {
-        if (pages[k] < 0) continue;
-        const int64_t r = (int64_t)hk * page + (j0 + k) % page;
-        const uint32_t w = ((const uint8_t*)c.v_codes)[pages[k] * c.v_codes_sp + r * (D / 2) + d / 2];
-        const uint32_t sc = ((const uint8_t*)c.v_scales)[pages[k] * c.v_scales_sp + r * (D / 16) + d / 16];
-        acc += ps[k] * (e2m1(d & 1 ? w >> 4 : w) * e4m3_to_f32(sc & 0x7Fu));
-      }
-      o[e] = o[e] * f + acc;
-    }
-    __syncthreads();
+    float inv;
+    const float fac = row_factor(group_max(amax), inv) * p.qmul;
+    cr[x] = fmaxf(p.c2 * inv, 1.17549435e-38f);          // never zero: -inf (excluded) times it stays -inf
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) qf[x][s][i] = (_Float16)(f[s][i] * fac);
+    m[x] = -INFINITY;
+    l[x] = 0.f;                                          // this lane group's keys only
   }
-  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
-  const float inv = l == 0.f ? 0.f : c.v_scale / l;
-  for (int e = 0; e < D / 64; ++e)
-    ((__bf16*)a.out)[b * a.o_sb + t * a.o_st + h * a.o_sh + e * 64 + lane] = (__bf16)(o[e] * inv);
+  v4f o[MT][DT];
+#pragma unroll
+  for (int x = 0; x < MT; ++x)
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[x][d] = (v4f){0.f, 0.f, 0.f, 0.f};
+
+  // This wave's LDS.  Row r of codes at r D / 2, its 8-byte chunks swizzled so
+  // that the 64 rows of a transposing read spread over the banks.
+  uint8_t* vl = smem + wave * C::WAVE;
+  uint8_t* sl = vl + C::VCODES;
+  auto chunk = [](int row) { return (row >> (D == 64 ? 3 : D == 128 ? 2 : 1)) & (C::VCH - 1); };
+  // the row whose codes this lane hands to the transposing read: key 16 t + 4 lg + i
+  const int trow = 16 * (lr >> 2) + 4 * lg + (lr & 3);
+  const uint32_t tbase = (uint32_t)(trow * (D / 2)), tswz = chunk(trow);
+
+  Block nxt = load_block(lo + wave, pg0);
+  pg0 = pg1;
+  for (int blk = lo + wave; blk < hi; blk += NW) {
+    const Block cur = nxt;
+    const int j0 = blk * BN;
+    pg1 = load_pages(blk + 2 * NW);
+    if (blk + NW < hi) nxt = load_block(blk + NW, pg0);
+    pg0 = pg1;
+
+    // V into LDS: piece t holds keys 16 t .. 16 t + 15, CB bytes a lane
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int row = 16 * t + lane / (D / 2 / C::CB), ch = lane % (D / 2 / C::CB) * (C::CB / 8), z = chunk(row);
+#pragma unroll
+      for (int i = 0; i < C::CB / 8; ++i)
+        *reinterpret_cast<uint2*>(vl + row * (D / 2) + ((ch + i) ^ z) * 8) = make_uint2(cur.v[t].w[2 * i], cur.v[t].w[2 * i + 1]);
+    }
+    // scales of key 16 lg + lr, in the order of the second product: t = lg, (g, i) from lr
+    {
+      const int at = (lr >> 2) * 16 + lg * 4 + (lr & 3);
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        *reinterpret_cast<uint16_t*>(sl + (d * BN + at) * 2) = (uint16_t)scale_bits(cur.vs.w[d / 4] >> (8 * (d & 3)));
+    }
+
+    v4f s[MT][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int x = 0; x < MT; ++x) s[x][t] = (v4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const v2h sc = both(scale_bits(cur.ks[t].w[0] >> (8 * (k / 2))));
+        const v8h kf = decode8(cur.k[t].w[k], sc, sc, sc, sc);
+#pragma unroll
+        for (int x = 0; x < MT; ++x) s[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[x][k], s[x][t], 0, 0, 0);
+      }
+    }
+    if (cur.bad || j0 + BN > first) {
+#pragma unroll
+      for (int x = 0; x < MT; ++x) {
+        const int vis = lim[x] - j0 - 4 * lg;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[x][t][i] = 16 * t + i < vis && !(cur.bad >> t & 1) ? s[x][t][i] : -INFINITY;
+      }
+    }
+    v8h pf[MT][2];
+#pragma unroll
+    for (int x = 0; x < MT; ++x) {
+      float tm = s[x][0][0];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tm = fmaxf(tm, s[x][t][i]);
+      tm = group_max(tm) * cr[x];
+      if (__any(tm > m[x] + kLazy)) {
+        const float mn = fmaxf(m[x], tm);
+        const float f = __builtin_amdgcn_exp2f(m[x] - (mn == -INFINITY ? 0.f : mn));
+        m[x] = mn;
+        l[x] *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[x][d] *= f;
+      }
+      const float nm = m[x] == -INFINITY ? 0.f : -m[x];
+      uint32_t w[8];
+      float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], cr[x], nm));
+          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i + 1], cr[x], nm));
+          l0 += e0;
+          l1 += e1;
+          w[2 * t + i / 2] = pack_f16(e0, e1);   // the second product takes p with 11 significant bits; l keeps 24
+        }
+      l[x] += l0 + l1;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        pf[x][h] = __builtin_bit_cast(v8h, (v4i){(int)w[4 * h], (int)w[4 * h + 1], (int)w[4 * h + 2], (int)w[4 * h + 3]});
+    }
+    // A wave's LDS accesses keep their order; the compiler has to keep it too.
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const v2i w = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i*)(vl + tbase + ((d ^ tswz) * 8)));
+      const uint4* sp = reinterpret_cast<const uint4*>(sl + (d * BN + lg * 16) * 2);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 q4 = sp[h];
+        const v8h vf = decode8((uint32_t)w[h], __builtin_bit_cast(v2h, q4.x), __builtin_bit_cast(v2h, q4.y),
+                               __builtin_bit_cast(v2h, q4.z), __builtin_bit_cast(v2h, q4.w));
+#pragma unroll
+        for (int x = 0; x < MT; ++x) o[x][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[x][h], o[x][d], 0, 0, 0);
+      }
+    }
+    asm volatile("" ::: "memory");
+  }
+
+  // Join the waves: each leaves its (m, l) and its o, scaled to the common
+  // maximum, in LDS, and all threads sum them.
+  float* red = reinterpret_cast<float*>(smem);
+  float* ml = red + NW * R * C::PITCH;
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < MT; ++x) {
+    l[x] = group_sum(l[x]);
+    if (lg == 0) {
+      ml[(wave * R + x * 16 + lr) * 2] = m[x];
+      ml[(wave * R + x * 16 + lr) * 2 + 1] = l[x];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < MT; ++x) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) mx = fmaxf(mx, ml[(k * R + x * 16 + lr) * 2]);
+    const float f = __builtin_amdgcn_exp2f(m[x] - (mx == -INFINITY ? 0.f : mx));
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+      *reinterpret_cast<v4f*>(&red[(wave * R + x * 16 + lr) * C::PITCH + 16 * d + 4 * lg]) = o[x][d] * f;
+  }
+  __syncthreads();
+  for (int e = tid; e < nrows * (D / 4); e += 64 * NW) {
+    const int rr = e / (D / 4), d = e % (D / 4) * 4;
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) M = fmaxf(M, ml[(k * R + rr) * 2]);
+    const float ms = M == -INFINITY ? 0.f : M;
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      L += ml[(k * R + rr) * 2 + 1] * __builtin_amdgcn_exp2f(ml[(k * R + rr) * 2] - ms);
+      acc += *reinterpret_cast<const v4f*>(&red[(k * R + rr) * C::PITCH + d]);
+    }
+    const int row = r0 + rr;
+    if (p.po) {
+      const int64_t x = (((int64_t)part * a.B + b) * c.Hkv + hk) * p.rows + row;
+      *reinterpret_cast<v4f*>(p.po + x * D + d) = acc;
+      if (d == 0) *reinterpret_cast<v2f*>(p.pml + x * 2) = (v2f){M, L};
+    } else {
+      const float inv = L == 0.f ? 0.f : c.v_scale / L;
+      int g;
+      const int t = div_by(row, p.g, g);
+      uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * G + g) * a.o_sh + d;
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+    }
+  }
+}
+
+// Joins the parts of a row: D / 4 lanes a row, 16 bytes of each part a lane.
+template <int D>
+__global__ void __launch_bounds__(256) cache_join_kernel(Args p) {
+  const w4a4_cache_attn& a = p.a;
+  constexpr int LPR = D / 4;
+  const int64_t gr = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  const int d = threadIdx.x % LPR * 4;
+  const int64_t all = a.B * p.c.Hkv * p.rows;
+  if (gr >= all) return;
+  const int parts = (int)p.parts.d;
+  float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) M = fmaxf(M, p.pml[(k * all + gr) * 2]);
+  const float ms = M == -INFINITY ? 0.f : M;
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) {
+    const v2f ml = *reinterpret_cast<const v2f*>(p.pml + (k * all + gr) * 2);
+    const float f = __builtin_amdgcn_exp2f(ml[0] - ms);
+    L += ml[1] * f;
+    acc += *reinterpret_cast<const v4f*>(p.po + (k * all + gr) * D + d) * f;
+  }
+  const float inv = L == 0.f ? 0.f : p.c.v_scale / L;
+  const int row = (int)(gr % p.rows), bh = (int)(gr / p.rows);
+  int hk, g;
+  const int b = div_by(bh, p.heads, hk), t = div_by(row, p.g, g);
+  uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * (int)p.g.d + g) * a.o_sh + d;
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+}
+
+template <typename C>
+void launch_few(const Args& p, hipStream_t st) {
+  const unsigned grid = (unsigned)(p.a.B * p.c.Hkv * p.tiles.d * p.parts.d);
+  attn_few_kernel<C><<<grid, 64 * NW, 0, st>>>(p);
 }
 
 }  // namespace
 
 size_t cache_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len) {
-  (void)B, (void)T, (void)Hq, (void)Hkv, (void)D, (void)max_len;
-  return 0;
+  const CacheAttnPlan pl = plan_cache_attention(B, T, Hq, Hkv, D, max_len, true);
+  return pl.parts > 1 ? (size_t)pl.parts * B * T * Hq * (D + 2) * 4 : 0;
 }
 
 hipError_t launch_cache_attention(const w4a4_kvcache& c, const w4a4_cache_attn& a, void* workspace, hipStream_t st) {
-  (void)workspace;
-  const unsigned grid = (unsigned)(a.B * a.T * a.Hq);
-  if (c.D == 64) attn_row_kernel<64><<<grid, 64, 0, st>>>(c, a);
-  else if (c.D == 128) attn_row_kernel<128><<<grid, 64, 0, st>>>(c, a);
-  else attn_row_kernel<256><<<grid, 64, 0, st>>>(c, a);
+  const CacheAttnPlan pl = plan_cache_attention(a.B, a.T, a.Hq, c.Hkv, c.D, a.max_len, workspace != nullptr);
+  Args p{};
+  p.c = c;
+  p.a = a;
+  const int64_t g = a.Hq / c.Hkv;
+  p.rows = (int)(a.T * g);
+  p.lp = c.page == 16 ? 4 : c.page == 32 ? 5 : c.page == 64 ? 6 : c.page == 128 ? 7 : 8;
+  p.g = divisor(g);
+  p.tiles = divisor(pl.tiles);
+  p.heads = divisor(c.Hkv);
+  p.parts = divisor(pl.parts);
+  const double c2 = (double)a.scale * c.k_scale * 1.4426950408889634;
+  p.qmul = c2 > 0 ? 1.f : c2 < 0 ? -1.f : 0.f;
+  p.c2 = c2 == 0 ? 1.f : (float)(c2 < 0 ? -c2 : c2);
+  if (pl.parts > 1) {
+    p.po = (float*)workspace;
+    p.pml = p.po + (size_t)pl.parts * a.B * a.T * a.Hq * c.D;
+  }
+  if (c.D == 64) {
+    if (pl.rows == 16) launch_few<Few<64, 1>>(p, st);
+    else if (pl.rows == 32) launch_few<Few<64, 2>>(p, st);
+    else launch_few<Few<64, 4>>(p, st);
+  } else if (c.D == 128) {
+    if (pl.rows == 16) launch_few<Few<128, 1>>(p, st);
+    else if (pl.rows == 32) launch_few<Few<128, 2>>(p, st);
+    else launch_few<Few<128, 4>>(p, st);
+  } else {
+    if (pl.rows == 16) launch_few<Few<256, 1>>(p, st);
+    else launch_few<Few<256, 2>>(p, st);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || pl.parts == 1) return e;
+  const int64_t all = a.B * c.Hkv * (int64_t)p.rows;
+  const int per = 256 / ((int)c.D / 4);
+  const unsigned grid = (unsigned)((all + per - 1) / per);
+  if (c.D == 64) cache_join_kernel<64><<<grid, 256, 0, st>>>(p);
+  else if (c.D == 128) cache_join_kernel<128><<<grid, 256, 0, st>>>(p);
+  else cache_join_kernel<256><<<grid, 256, 0, st>>>(p);
   return hipGetLastError();
 }
 
