@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
         for (int i = 0; i < 4; ++i) tm = fmaxf(tm, s[x][t][i]);
       tm = group_max(tm) * cr[x];
       if (__any(tm > m[x] + kLazy)) {
-        const float mn = fmaxf(m[x], tm);
+        const float mn = tm > m[x] + kLazy ? tm : m[x];   // only the rows that need it move
         const float f = __builtin_amdgcn_exp2f(m[x] - (mn == -INFINITY ? 0.f : mn));
         m[x] = mn;
         l[x] *= f;
@@ -412,6 +412,474 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
   }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows: a workgroup of four waves, NS sets of 32 rows each, shares every
+// block of keys, converted to fp16 once and kept in LDS.
+//
+// Products.  S^T = K Q^T and O^T = V^T P^T with v_mfma_f32_32x32x16_f16: a lane
+// has one query (lane % 32) and of 32 keys the scores of keys 8 (i / 4) +
+// 4 (lane / 32) + i % 4.  The second product takes its 16 keys per step in that
+// order, V^T comes from LDS through the transposing read (4 keys x 16 channels
+// per 16 lanes), and P never moves between lanes.  A fragment read from LDS
+// feeds NS products: with 32 rows a wave, reading fragments would take as long
+// as multiplying them.
+//
+// One wave a SIMD, so a wave overlaps its own work.  Keys go by halves of a
+// block: phase 1 of half u multiplies half u + 1 by the queries while it turns
+// the scores of half u into probabilities; phase 2 multiplies those by V while
+// it converts codes of a later block.  A barrier stands between phase 1 and
+// phase 2 of every even half: between two of them the halves 2 i and 2 i + 1 of
+// V and 2 i + 2 and 2 i + 3 of K are read, which are block i of V and block
+// i + 1 of K, and V of block i + 1 and K of block i + 2 are written to the
+// other buffers.  Steps of one fragment, their products and their share of the
+// vector work are pinned.
+//
+// Maximum.  Probabilities are taken with the m at hand.  Only where a lane's
+// sum of a block passes kMost (or there is no m yet) the maximum is looked for
+// and the block's probabilities are taken again; p is at most kMost, l at
+// least 1 then.
+// ---------------------------------------------------------------------------
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+typedef __attribute__((address_space(3))) v4i lds_v4i;
+
+constexpr float kMost = 1024.f;
+
+template <int D_, int W_, int NS_>
+struct Many {
+  static constexpr int D = D_, W = W_, NS = NS_, R = W * 32 * NS;
+  static constexpr int RB = 2 * D, MAT = BN * RB;       // bytes of a row, of a block of K or V
+  static constexpr int KC = D / 16, DB = D / 32;        // steps, channel blocks
+  static constexpr int MATS = 8 / W;                    // W = 8: waves 0-3 convert K, 4-7 V; W = 4: each both
+  static constexpr int CB = D / 8;                      // bytes of codes a thread converts of one of them
+  static constexpr int STRIDE = 2 / MATS;               // conversions of a chunk: every second or fourth step
+  static constexpr int AHEAD = 4;                       // steps a fragment is read ahead
+  static constexpr int LDS = 4 * MAT;
+};
+
+// 16-byte chunk swizzles of an LDS row.  K: the rows of a chunk column, read 32
+// at a time, spread over the banks.  V: so do 4 rows of 4 adjacent chunks, which
+// the transposing read takes, and (the lower bits) the rows written together.
+template <int D>
+__device__ __forceinline__ int swz_k(int row) {
+  return D == 64 ? (row >> 1) & 7 : row & 15;
+}
+template <int D>
+__device__ __forceinline__ int swz_v(int row) {
+  return D == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 1) : (row & 3) << 2 | ((row >> 2) & 3);
+}
+// The row of its group of 16 that a thread converts of V, so that 16 lanes
+// write all banks (four lanes a row; of K the rows in order do that).
+template <int D>
+__device__ __forceinline__ int write_row_v(int i) {
+  return D == 64 ? (i & 9) | (i & 2) << 1 | (i & 4) >> 1 : (i & 3) << 2 | i >> 2;
+}
+__device__ __forceinline__ float half_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+template <typename C>
+__global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) {
+  constexpr int D = C::D, NS = C::NS, R = C::R, MATS = C::MATS, KC = C::KC, DB = C::DB, AHEAD = C::AHEAD;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];   // K of even and odd blocks, V of them
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  const int nwg = gridDim.x, wid = blockIdx.x;
+  const int u = nwg % 8 == 0 ? (wid % 8) * (nwg / 8) + wid / 8 : wid;
+  int tile, part, hk;
+  const int b = div_by(div_by(div_by(u, p.tiles, tile), p.parts, part), p.heads, hk);
+  const w4a4_kvcache& c = p.c;
+  const w4a4_cache_attn& a = p.a;
+  const int G = (int)p.g.d, page = 1 << p.lp;
+
+  const int r0 = tile * R, nrows = min(R, p.rows - r0);
+  int rem;
+  const int64_t reach = min(a.max_len, a.table_pages << p.lp);
+  const int len = (int)max((int64_t)0, min((int64_t)a.lens[b], reach));
+  const int last = row_limit(p, len, div_by(r0 + nrows - 1, p.g, rem));
+  const int first = row_limit(p, len, div_by(r0 + min(wave * 32 * NS, nrows - 1), p.g, rem));   // of this wave
+  const int nblk = (max(last, 0) + BN - 1) / BN;
+  const int per = (nblk + (int)p.parts.d - 1) / (int)p.parts.d;
+  const int lo = min(part * per, nblk), n = min(lo + per, nblk) - lo;
+  // (without keys there may be no table: any integer then)
+  const int32_t* table = n > 0 ? a.table + b * a.table_sb : a.lens;
+
+  // pages of the four groups of 16 keys from key `j` of this part on, one a lane group
+  auto load_pages = [&](int j) {
+    j += 16 * (lane >> 4);
+    const int key = lo * BN + j;
+    const bool in = j < n * BN && key < last;
+    const int pg = table[in ? key >> p.lp : 0];   // no branch: the waits of later loads count this one
+    return in ? pg : -1;
+  };
+  auto absent = [&](int pg) -> uint32_t {
+    const uint64_t x = __ballot(pg < 0 || pg >= c.n_pages);
+    return (uint32_t)(x & 1) | (uint32_t)(x >> 15 & 2) | (uint32_t)(x >> 30 & 4) | (uint32_t)(x >> 45 & 8);
+  };
+  // This thread converts a row of each block of K, or V, or both: row `in` of
+  // the group of 16, chunks of eight channels chunk(0), chunk(1), ...
+  const int grp = wave & 3, cq = lane & 3;
+  auto chunk = [&](int x) { return D == 256 ? (x >> 2) * 16 + cq * 4 + (x & 3) : cq * (D / 32) + x; };
+  constexpr int PIECES = D == 256 ? 2 : 1, PB = C::CB / PIECES;   // adjacent chunks: PB bytes of codes
+  struct Raw {
+    Words<PB> codes[PIECES];
+    Words<PB / 8> scales[PIECES];
+  };
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+  struct Mat {
+    const uint8_t *codes, *scales;   // the head's, page 0
+    int64_t codes_sp, scales_sp;
+    uint32_t coff, soff, at;         // this lane's bytes in a group of 16 rows; its row in LDS, buffer 0
+    int z;                           // the row's swizzle
+  } mat[MATS];
+#pragma unroll
+  for (int x = 0; x < MATS; ++x) {
+    const bool v = MATS == 2 ? x == 1 : wave >= 4;
+    const int in = v ? write_row_v<D>(lane >> 2) : lane >> 2;
+    mat[x].codes = (const uint8_t*)(v ? c.v_codes : c.k_codes) + (int64_t)hk * page * (D / 2);
+    mat[x].scales = (const uint8_t*)(v ? c.v_scales : c.k_scales) + (int64_t)hk * page * (D / 16);
+    mat[x].codes_sp = v ? c.v_codes_sp : c.k_codes_sp;
+    mat[x].scales_sp = v ? c.v_scales_sp : c.k_scales_sp;
+    mat[x].coff = in * (D / 2) + cq * PB;
+    mat[x].soff = in * (D / 16) + cq * (PB / 8);
+    mat[x].at = lds0 + (v ? 2 * C::MAT : 0) + (16 * grp + in) * C::RB;
+    mat[x].z = v ? swz_v<D>(in) : swz_k<D>(in);
+  }
+  const uint32_t n_pages = (uint32_t)c.n_pages;
+  auto load_raw = [&](const Mat& t, int j, int pgs) {     // keys from j (of the part) on, on pages pgs
+    uint32_t pg = (uint32_t)__builtin_amdgcn_readlane(pgs, 16 * grp);
+    pg = pg < n_pages ? pg : 0;                           // any page: its keys are excluded
+    const uint32_t tok = (uint32_t)((lo * BN + j + 16 * grp) & (page - 1));
+    const uint8_t* cp = t.codes + (pg * t.codes_sp + tok * (D / 2));
+    const uint8_t* sp = t.scales + (pg * t.scales_sp + tok * (D / 16));
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      r.codes[i] = load_words<PB>(cp + t.coff + i * 64);
+      r.scales[i] = load_words<PB / 8>(sp + t.soff + i * 8);
+    }
+    return r;
+  };
+  auto store = [&](const Mat& t, const Raw& r, int x, uint32_t buf) {   // the thread's chunk x, converted
+    constexpr int N = PB / 4;
+    const v2h sc = both(scale_bits(r.scales[x / N].w[0] >> (8 * (x % N / 2))));
+    *(lds_v4i*)(t.at + buf + ((chunk(x) ^ t.z) << 4)) =
+        __builtin_bit_cast(v4i, decode8(r.codes[x / N].w[x % N], sc, sc, sc, sc));
+  };
+
+  int pg0 = load_pages(0), pg1 = load_pages(BN), pg2 = load_pages(2 * BN), pg3 = load_pages(3 * BN);
+  Raw raw[MATS], second;                                  // blocks 0, and block 1 of K
+#pragma unroll
+  for (int x = 0; x < MATS; ++x) raw[x] = load_raw(mat[x], 0, pg0);
+  second = load_raw(mat[0], BN, pg1);
+
+  // queries: row tile r0, wave, set, lane
+  v8h qf[NS][KC];
+  float cr[NS], m[NS], l[NS];
+  int lim[NS];
+#pragma unroll
+  for (int x = 0; x < NS; ++x) {
+    const int row = r0 + min((wave * NS + x) * 32 + lr, nrows - 1);   // rows past the end repeat the last
+    int g;
+    const int t = div_by(row, p.g, g);
+    lim[x] = row_limit(p, len, t);
+    const uint16_t* q = (const uint16_t*)a.q + b * a.q_sb + t * a.q_st + (int64_t)(hk * G + g) * a.q_sh + h * 8;
+    uint4 v[KC];
+    float amax = 0.f;
+#pragma unroll
+    for (int s = 0; s < KC; ++s) v[s] = *reinterpret_cast<const uint4*>(q + 16 * s);
+#pragma unroll
+    for (int s = 0; s < KC; ++s) {
+      const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        amax = fmaxf(amax, fmaxf(__uint_as_float(w[i] << 16 & 0x7FFFFFFFu), __uint_as_float(w[i] & 0x7FFF0000u)));
+    }
+    float inv;
+    const float fac = row_factor(half_max(amax), inv) * p.qmul;
+    cr[x] = fmaxf(p.c2 * inv, 1.17549435e-38f);          // never zero: -inf (excluded) times it stays -inf
+#pragma unroll
+    for (int s = 0; s < KC; ++s) {
+      const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
+      v4i f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[i] = (int)pack_f16(__uint_as_float(w[i] << 16) * fac, __uint_as_float(w[i] & 0xFFFF0000u) * fac);
+      qf[x][s] = __builtin_bit_cast(v8h, f);
+      // with one wave a SIMD it stays in accumulation registers, from where the products take it
+      if constexpr (C::W == 4) asm volatile("" : "+a"(qf[x][s]));
+    }
+    m[x] = -INFINITY;
+    l[x] = 0.f;                                          // this half's keys only
+  }
+  v16f o[NS][DB];
+#pragma unroll
+  for (int x = 0; x < NS; ++x)
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[x][d][i] = 0.f;
+
+  // LDS: two stages of K, two blocks of V; addresses of the fragment reads in
+  // the buffers that are read next
+  const uint32_t ka = lds0 + lr * C::RB + ((h ^ swz_k<D>(lr)) << 4);
+  const int vr = 4 * h + ((lane & 15) >> 2);
+  const int vch = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  uint32_t kad[KC], vad[2][DB];                           // V: rows vr and vr + 8 (the swizzle repeats every 16)
+#pragma unroll
+  for (int k = 0; k < KC; ++k) kad[k] = ka ^ (k << 5);    // the swizzle is an exclusive or of the chunk
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      vad[e][d] = lds0 + 2 * C::MAT + (vr + 8 * e) * C::RB + (((4 * d + vch) ^ swz_v<D>(vr + 8 * e)) << 4) + (lane & 1) * 8;
+  v4i frag[AHEAD];
+  // fragment t of K: 32 keys of half `half`, channels 16 t
+  auto fetch_k = [&](int t, int half) { frag[t % AHEAD] = *(lds_v4i*)(kad[t] + half * 32 * C::RB); };
+  // fragment t of V: keys 16 (t / DB) of half `half`, channels 32 (t % DB)
+  auto fetch_v = [&](int t, int half) {
+    const int off = (half * 32 + t / DB * 16) * C::RB;
+    const v4s v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vad[0][t % DB] + off));
+    const v4s v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vad[1][t % DB] + off));
+    frag[t % AHEAD] = __builtin_bit_cast(v4i, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  typedef v16f Scores[NS];     // of 32 keys
+  uint32_t pk[NS][8];
+  float lb[NS];
+  const v2h one = {(_Float16)1.f, (_Float16)1.f};
+  // Probabilities 2 w and 2 w + 1 of a set, in four stages of one instruction's
+  // depth each, which phase 1 spreads over its steps.
+  float arg[NS][8][2];
+  auto prob = [&](const Scores& s, int x, int w, float nm, int stage) {
+    float* e = arg[x][w];
+    if (stage == 0) {
+      e[0] = __builtin_fmaf(s[x][2 * w], cr[x], nm);
+      e[1] = __builtin_fmaf(s[x][2 * w + 1], cr[x], nm);
+    } else if (stage == 1) {
+      e[0] = __builtin_amdgcn_exp2f(e[0]);
+      e[1] = __builtin_amdgcn_exp2f(e[1]);
+    } else if (stage == 2) {
+      pk[x][w] = pack_f16(e[0], e[1]);   // the second product takes p with 11 significant bits, and so does the sum
+    } else {
+      lb[x] = __builtin_amdgcn_fdot2(__builtin_bit_cast(v2h, pk[x][w]), one, lb[x], false);
+    }
+  };
+  // scores of keys from j0 (of the part) on that a row does not see; bad: absent groups of 16
+  auto exclude = [&](Scores& s, int j0, uint32_t bad) {
+    j0 += lo * BN;
+    if ((bad & 3) == 0 && j0 + 32 <= first) return;
+#pragma unroll
+    for (int x = 0; x < NS; ++x) {
+      const int vis = lim[x] - j0 - 4 * h;
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        s[x][e] = 8 * (e >> 2) + (e & 3) < vis && !(bad >> (e >> 3) & 1) ? s[x][e] : -INFINITY;
+    }
+  };
+  auto sync = [&]() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  const v16f zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  auto qk = [&](Scores& s, int x, int t, const v8h& f) {
+    s[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, qf[x][t], t == 0 ? zero : s[x], 0, 0, 0);
+  };
+
+  // Phase 1: scores `s` to probabilities, products of K's half `half` to `next`.
+  auto phase1 = [&](Scores& s, Scores& next, auto half_, auto then_, auto&& extra) {
+    constexpr int half = half_(), then = then_();    // then: the half of V whose fragments come next, or -1
+    float nm[NS];
+#pragma unroll
+    for (int x = 0; x < NS; ++x) {
+      nm[x] = m[x] == -INFINITY ? 0.f : -m[x];
+      lb[x] = 0.f;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < KC; ++t) {
+      const v8h f = __builtin_bit_cast(v8h, frag[t % AHEAD]);
+#pragma unroll
+      for (int x = 0; x < NS; ++x) {
+        qk(next, x, t, f);
+#pragma unroll
+        for (int g = 3; g >= 0; --g)
+#pragma unroll
+          for (int w = max(t - g, 0) * 8 / KC; w < max(t - g + 1, 0) * 8 / KC; ++w) prob(s, x, w, nm[x], g);
+      }
+      extra(t);
+      if (t + AHEAD < KC) fetch_k(t + AHEAD, half);
+      else if constexpr (then >= 0) fetch_v(t + AHEAD - KC, then);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int t = KC; t < KC + 3; ++t)
+#pragma unroll
+      for (int g = 3; g > t - KC; --g)
+#pragma unroll
+        for (int x = 0; x < NS; ++x)
+#pragma unroll
+          for (int w = (t - g) * 8 / KC; w < (t - g + 1) * 8 / KC; ++w) prob(s, x, w, nm[x], g);
+    bool again = false;
+#pragma unroll
+    for (int x = 0; x < NS; ++x) again |= !(lb[x] <= kMost) || m[x] == -INFINITY;
+    if (__any(again)) {
+#pragma unroll
+      for (int x = 0; x < NS; ++x) {
+        float tm = s[x][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) tm = fmaxf(tm, s[x][e]);
+        // only the rows that need it move: no row's result depends on its neighbours
+        const bool moves = half_max(lb[x]) > kMost || m[x] == -INFINITY;
+        const float mn = moves ? fmaxf(m[x], half_max(tm) * cr[x]) : m[x];
+        const float f = __builtin_amdgcn_exp2f(m[x] - (mn == -INFINITY ? 0.f : mn));
+        m[x] = mn;
+        l[x] *= f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[x][d][e] *= f;
+        lb[x] = 0.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int w = 0; w < 8; ++w) prob(s, x, w, mn == -INFINITY ? 0.f : -mn, g);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < NS; ++x) l[x] += lb[x];
+  };
+  // Phase 2: the probabilities by V's half `half`; convert(t) is called in every step.
+  auto phase2 = [&](auto half_, auto then_, auto&& convert) {
+    constexpr int half = half_(), then = then_();    // then: the half of K whose fragments come next
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < KC; ++t) {
+      convert(t);
+      const v8h f = __builtin_bit_cast(v8h, frag[t % AHEAD]);
+#pragma unroll
+      for (int x = 0; x < NS; ++x) {
+        const uint32_t* w = &pk[x][t / DB * 4];
+        const v4i pv = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+        o[x][t % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, __builtin_bit_cast(v8h, pv), o[x][t % DB], 0, 0, 0);
+      }
+      if (t + AHEAD < KC) fetch_v(t + AHEAD, half);
+      else fetch_k(t + AHEAD - KC, then);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  struct None { constexpr int operator()() const { return -1; } };
+  struct First { constexpr int operator()() const { return 0; } };
+  struct Second { constexpr int operator()() const { return 1; } };
+  auto flip = [&](int k, int v) {
+#pragma unroll
+    for (int i = 0; i < KC; ++i) kad[i] += k;
+#pragma unroll
+    for (int d = 0; d < DB; ++d) vad[0][d] += v, vad[1][d] += v;
+  };
+
+  Scores s0, s1;               // of the first and second half of a block
+  if (n > 0) {
+    uint32_t bad = absent(pg0), next_bad = 0;
+    int pg4 = -1;
+#pragma unroll
+    for (int y = 0; y < MATS; ++y)
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) store(mat[y], raw[y], x, 0);
+    sync();
+#pragma unroll
+    for (int t = 0; t < KC; ++t) {
+      fetch_k(t, 0);
+#pragma unroll
+      for (int x = 0; x < NS; ++x) qk(s0, x, t, __builtin_bit_cast(v8h, frag[t % AHEAD]));
+    }
+#pragma unroll
+    for (int t = 0; t < AHEAD; ++t) fetch_k(t, 1);
+    // Block 1 of K; of V it is converted in the first iteration.
+    const bool only_v = MATS == 1 && wave >= 4;
+    if (!only_v)
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) store(mat[0], second, x, C::MAT);
+    // What an iteration converts first: in the order in which it loads them, so
+    // that a wait for the older one leaves the younger in flight.
+    raw[0] = load_raw(mat[0], only_v ? BN : 2 * BN, only_v ? pg1 : pg2);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (MATS == 2) raw[1] = load_raw(mat[1], BN, pg1);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < n; ++i) {
+      const int odd = i & 1;
+      const uint32_t buf0 = odd == (int)only_v ? 0 : C::MAT, buf1 = odd ? 0 : C::MAT;   // K of block i + 2, V of block i + 1
+      exclude(s0, i * BN, bad);
+      phase1(s0, s1, Second(), None(), [&](int t) {
+        if (t == 1) next_bad = absent(pg1);
+      });
+      flip(odd ? -C::MAT : C::MAT, 0);
+      sync();
+#pragma unroll
+      for (int t = 0; t < AHEAD; ++t) fetch_v(t, 0);
+      phase2(First(), First(), [&](int t) {
+        if (t % (2 * C::STRIDE) == 0) store(mat[0], raw[0], t / (2 * C::STRIDE), buf0);
+        if (MATS == 2 && t == KC - 1) raw[0] = load_raw(mat[0], (i + 3) * BN, pg3);
+      });
+      exclude(s1, i * BN + 32, bad >> 2);
+      phase1(s1, s0, First(), Second(), [&](int t) {
+        if (t == 1) pg4 = load_pages((i + 4) * BN);
+      });
+      phase2(Second(), Second(), [&](int t) {
+        if constexpr (MATS == 2) {
+          if (t % 2 == 0) store(mat[1], raw[1], t / 2, buf1);
+          if (t == KC - 1) raw[1] = load_raw(mat[1], (i + 2) * BN, pg2);
+        } else {
+          if (t % 4 == 0) store(mat[0], raw[0], D / 64 + t / 4, buf0);
+          if (t == KC - 1) raw[0] = load_raw(mat[0], (i + (only_v ? 2 : 3)) * BN, only_v ? pg2 : pg3);
+        }
+      });
+      flip(0, odd ? -C::MAT : C::MAT);
+      bad = next_bad;
+      pg1 = pg2;
+      pg2 = pg3;
+      pg3 = pg4;
+    }
+  }
+
+#pragma unroll
+  for (int x = 0; x < NS; ++x) {
+    l[x] = half_sum(l[x]);
+    const int rl = (wave * NS + x) * 32 + lr, row = r0 + rl;
+    if (rl >= nrows) continue;
+    if (p.po) {
+      const int64_t at = (((int64_t)part * a.B + b) * c.Hkv + hk) * p.rows + row;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<v4f*>(p.po + at * D + 32 * d + 8 * i + 4 * h) =
+              (v4f){o[x][d][4 * i], o[x][d][4 * i + 1], o[x][d][4 * i + 2], o[x][d][4 * i + 3]};
+      if (h == 0) *reinterpret_cast<v2f*>(p.pml + at * 2) = (v2f){m[x], l[x]};
+    } else {
+      const float inv = l[x] == 0.f ? 0.f : c.v_scale / l[x];
+      int g;
+      const int t = div_by(row, p.g, g);
+      uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * G + g) * a.o_sh;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint2*>(out + 32 * d + 8 * i + 4 * h) =
+              make_uint2(pack_bf16(o[x][d][4 * i] * inv, o[x][d][4 * i + 1] * inv),
+                         pack_bf16(o[x][d][4 * i + 2] * inv, o[x][d][4 * i + 3] * inv));
+    }
+  }
+}
+
 // Joins the parts of a row: D / 4 lanes a row, 16 bytes of each part a lane.
 template <int D>
 __global__ void __launch_bounds__(256) cache_join_kernel(Args p) {
@@ -448,6 +916,11 @@ void launch_few(const Args& p, hipStream_t st) {
   attn_few_kernel<C><<<grid, 64 * NW, 0, st>>>(p);
 }
 
+template <typename C>
+void launch_many(const Args& p, hipStream_t st) {
+  attn_many_kernel<C><<<(unsigned)(p.a.B * p.c.Hkv * p.tiles.d * p.parts.d), 64 * C::W, 0, st>>>(p);
+}
+
 }  // namespace
 
 size_t cache_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len) {
@@ -477,14 +950,15 @@ hipError_t launch_cache_attention(const w4a4_kvcache& c, const w4a4_cache_attn& 
   if (c.D == 64) {
     if (pl.rows == 16) launch_few<Few<64, 1>>(p, st);
     else if (pl.rows == 32) launch_few<Few<64, 2>>(p, st);
-    else launch_few<Few<64, 4>>(p, st);
+    else launch_many<Many<64, 8, 1>>(p, st);
   } else if (c.D == 128) {
     if (pl.rows == 16) launch_few<Few<128, 1>>(p, st);
     else if (pl.rows == 32) launch_few<Few<128, 2>>(p, st);
-    else launch_few<Few<128, 4>>(p, st);
+    else launch_many<Many<128, 8, 1>>(p, st);
   } else {
     if (pl.rows == 16) launch_few<Few<256, 1>>(p, st);
-    else launch_few<Few<256, 2>>(p, st);
+    else if (pl.rows == 32) launch_few<Few<256, 2>>(p, st);
+    else launch_many<Many<256, 4, 1>>(p, st);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.parts == 1) return e;
