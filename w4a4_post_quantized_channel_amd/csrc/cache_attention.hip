@@ -179,37 +179,40 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
     const int j = blk * BN + 16 * lg;
     return blk < hi && j < last ? table[j >> p.lp] : -1;
   };
-  struct Block {
-    Words<C::CB> k[4];
-    Words<C::CB / 8> ks[4];
-    Words<C::CB> v[4];
-    Words<DT> vs;
-    uint32_t bad;   // groups whose page is absent
-  };
+  Words<C::CB> kw[4], vw[4];        // a block's codes and scales: K by tiles of 16 keys
+  Words<C::CB / 8> ksw[4];
+  Words<DT> vsw;
+  uint32_t bad = 0;                 // groups whose page is absent
   const uint8_t* kc = (const uint8_t*)c.k_codes + (int64_t)hk * page * (D / 2) + lr * (D / 2) + lg * C::CB;
   const uint8_t* ks = (const uint8_t*)c.k_scales + (int64_t)hk * page * DT + lr * DT + lg * (DT / 4);
   const uint8_t* vc = (const uint8_t*)c.v_codes + (int64_t)hk * page * (D / 2) + lane * C::CB;
   const uint8_t* vs = (const uint8_t*)c.v_scales + (int64_t)hk * page * DT + lr * DT;
-  auto load_block = [&](int blk, int pg) {
-    Block x;
-    const bool absent = pg < 0 || pg >= c.n_pages;
-    if (absent) pg = 0;                          // any page: its keys are excluded
-    const uint64_t m = __ballot(absent);
-    x.bad = (uint32_t)(m & 1) | (uint32_t)(m >> 15 & 2) | (uint32_t)(m >> 30 & 4) | (uint32_t)(m >> 45 & 8);
-    const int j0 = blk * BN;
+  auto held = [&](int pg) { return pg >= 0 && pg < c.n_pages ? pg : 0; };   // an absent page: any, its keys are excluded
+  auto load_k = [&](int blk, int pg) {
+    const uint64_t x = __ballot(pg < 0 || pg >= c.n_pages);
+    bad = (uint32_t)(x & 1) | (uint32_t)(x >> 15 & 2) | (uint32_t)(x >> 30 & 4) | (uint32_t)(x >> 45 & 8);
+    pg = held(pg);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int64_t pt = __builtin_amdgcn_readlane(pg, 16 * t);
-      const int tok = (j0 + 16 * t) & (page - 1);
-      x.k[t] = load_words<C::CB>(kc + (pt * c.k_codes_sp + tok * (D / 2)));
-      x.ks[t] = load_words<C::CB / 8>(ks + (pt * c.k_scales_sp + tok * DT));
-      x.v[t] = load_words<C::CB>(vc + (pt * c.v_codes_sp + tok * (D / 2)));
+      const int tok = (blk * BN + 16 * t) & (page - 1);
+      kw[t] = load_words<C::CB>(kc + (pt * c.k_codes_sp + tok * (D / 2)));
+      ksw[t] = load_words<C::CB / 8>(ks + (pt * c.k_scales_sp + tok * DT));
     }
-    x.vs = load_words<DT>(vs + (pg * c.v_scales_sp + ((j0 + 16 * lg) & (page - 1)) * DT));
-    return x;
+  };
+  auto load_v = [&](int blk, int pg) {
+    pg = held(pg);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int64_t pt = __builtin_amdgcn_readlane(pg, 16 * t);
+      vw[t] = load_words<C::CB>(vc + (pt * c.v_codes_sp + ((blk * BN + 16 * t) & (page - 1)) * (D / 2)));
+    }
+    vsw = load_words<DT>(vs + (pg * c.v_scales_sp + ((blk * BN + 16 * lg) & (page - 1)) * DT));
   };
 
-  int pg0 = load_pages(lo + wave), pg1 = load_pages(lo + wave + NW);
+  int pg = load_pages(lo + wave), pg1 = load_pages(lo + wave + NW);
+  load_v(lo + wave, pg);
+  load_k(lo + wave, pg);
 
   // queries, limits
   v8h qf[MT][KS];
@@ -259,14 +262,14 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
   const int trow = 16 * (lr >> 2) + 4 * lg + (lr & 3);
   const uint32_t tbase = (uint32_t)(trow * (D / 2)), tswz = chunk(trow);
 
-  Block nxt = load_block(lo + wave, pg0);
-  pg0 = pg1;
+  // The next block's values are loaded when this one's are in LDS, its keys when
+  // this one's are multiplied: into the registers that those leave.
   for (int blk = lo + wave; blk < hi; blk += NW) {
-    const Block cur = nxt;
     const int j0 = blk * BN;
+    const uint32_t absent = bad;
+    const bool more = blk + NW < hi;
+    pg = pg1;
     pg1 = load_pages(blk + 2 * NW);
-    if (blk + NW < hi) nxt = load_block(blk + NW, pg0);
-    pg0 = pg1;
 
     // V into LDS: piece t holds keys 16 t .. 16 t + 15, CB bytes a lane
 #pragma unroll
@@ -274,15 +277,17 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
       const int row = 16 * t + lane / (D / 2 / C::CB), ch = lane % (D / 2 / C::CB) * (C::CB / 8), z = chunk(row);
 #pragma unroll
       for (int i = 0; i < C::CB / 8; ++i)
-        *reinterpret_cast<uint2*>(vl + row * (D / 2) + ((ch + i) ^ z) * 8) = make_uint2(cur.v[t].w[2 * i], cur.v[t].w[2 * i + 1]);
+        *reinterpret_cast<uint2*>(vl + row * (D / 2) + ((ch + i) ^ z) * 8) = make_uint2(vw[t].w[2 * i], vw[t].w[2 * i + 1]);
     }
     // scales of key 16 lg + lr, in the order of the second product: t = lg, (g, i) from lr
     {
       const int at = (lr >> 2) * 16 + lg * 4 + (lr & 3);
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        *reinterpret_cast<uint16_t*>(sl + (d * BN + at) * 2) = (uint16_t)scale_bits(cur.vs.w[d / 4] >> (8 * (d & 3)));
+        *reinterpret_cast<uint16_t*>(sl + (d * BN + at) * 2) = (uint16_t)scale_bits(vsw.w[d / 4] >> (8 * (d & 3)));
     }
+
+    if (more) load_v(blk + NW, pg);
 
     v4f s[MT][4];
 #pragma unroll
@@ -291,20 +296,21 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
       for (int x = 0; x < MT; ++x) s[x][t] = (v4f){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const v2h sc = both(scale_bits(cur.ks[t].w[0] >> (8 * (k / 2))));
-        const v8h kf = decode8(cur.k[t].w[k], sc, sc, sc, sc);
+        const v2h sc = both(scale_bits(ksw[t].w[0] >> (8 * (k / 2))));
+        const v8h kf = decode8(kw[t].w[k], sc, sc, sc, sc);
 #pragma unroll
         for (int x = 0; x < MT; ++x) s[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[x][k], s[x][t], 0, 0, 0);
       }
     }
-    if (cur.bad || j0 + BN > first) {
+    if (more) load_k(blk + NW, pg);
+    if (absent || j0 + BN > first) {
 #pragma unroll
       for (int x = 0; x < MT; ++x) {
         const int vis = lim[x] - j0 - 4 * lg;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[x][t][i] = 16 * t + i < vis && !(cur.bad >> t & 1) ? s[x][t][i] : -INFINITY;
+          for (int i = 0; i < 4; ++i) s[x][t][i] = 16 * t + i < vis && !(absent >> t & 1) ? s[x][t][i] : -INFINITY;
       }
     }
     v8h pf[MT][2];
@@ -424,15 +430,13 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
 // feeds NS products: with 32 rows a wave, reading fragments would take as long
 // as multiplying them.
 //
-// One wave a SIMD, so a wave overlaps its own work.  Keys go by halves of a
+// A wave overlaps its own work as far as it can.  Keys go by halves of a
 // block: phase 1 of half u multiplies half u + 1 by the queries while it turns
 // the scores of half u into probabilities; phase 2 multiplies those by V while
 // it converts codes of a later block.  A barrier stands between phase 1 and
-// phase 2 of every even half: between two of them the halves 2 i and 2 i + 1 of
-// V and 2 i + 2 and 2 i + 3 of K are read, which are block i of V and block
-// i + 1 of K, and V of block i + 1 and K of block i + 2 are written to the
-// other buffers.  Steps of one fragment, their products and their share of the
-// vector work are pinned.
+// phase 2 of a block's first half: between two of them V of block i and K of
+// block i + 1 are read, and V of block i + 1 and K of block i + 2 written to the
+// other buffers.
 //
 // Maximum.  Probabilities are taken with the m at hand.  Only where a lane's
 // sum of a block passes kMost (or there is no m yet) the maximum is looked for
@@ -454,7 +458,8 @@ struct Many {
   static constexpr int CB = D / 8;                      // bytes of codes a thread converts of one of them
   static constexpr int STRIDE = 2 / MATS;               // conversions of a chunk: every second or fourth step
   static constexpr int AHEAD = 4;                       // steps a fragment is read ahead
-  static constexpr int LDS = 4 * MAT;
+  static constexpr int LDS = 4 * MAT;                   // two blocks of K, two of V
+  static_assert(KC % AHEAD == 0, "a phase's last fragments and the next one's first take the same registers");
 };
 
 // 16-byte chunk swizzles of an LDS row.  K: the rows of a chunk column, read 32
@@ -573,11 +578,15 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
         __builtin_bit_cast(v4i, decode8(r.codes[x / N].w[x % N], sc, sc, sc, sc));
   };
 
-  int pg0 = load_pages(0), pg1 = load_pages(BN), pg2 = load_pages(2 * BN), pg3 = load_pages(3 * BN);
-  Raw raw[MATS], second;                                  // blocks 0, and block 1 of K
+  int pg[4];                                              // of the next blocks
 #pragma unroll
-  for (int x = 0; x < MATS; ++x) raw[x] = load_raw(mat[x], 0, pg0);
-  second = load_raw(mat[0], BN, pg1);
+  for (int x = 0; x < 4; ++x) pg[x] = load_pages(x * BN);
+  // The blocks that are converted before the first product: of K one more than
+  // of V (a wave that converts V alone converts that one in the loop).
+  const bool only_v = MATS == 1 && wave >= 4;
+  Raw raw[MATS], early[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) early[x] = load_raw(mat[0], x * BN, pg[x]);
 
   // queries: row tile r0, wave, set, lane
   v8h qf[NS][KC];
@@ -626,8 +635,7 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[x][d][i] = 0.f;
 
-  // LDS: two stages of K, two blocks of V; addresses of the fragment reads in
-  // the buffers that are read next
+  // addresses of the fragment reads in the buffers that are read next
   const uint32_t ka = lds0 + lr * C::RB + ((h ^ swz_k<D>(lr)) << 4);
   const int vr = 4 * h + ((lane & 15) >> 2);
   const int vch = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
@@ -653,22 +661,11 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
   uint32_t pk[NS][8];
   float lb[NS];
   const v2h one = {(_Float16)1.f, (_Float16)1.f};
-  // Probabilities 2 w and 2 w + 1 of a set, in four stages of one instruction's
-  // depth each, which phase 1 spreads over its steps.
-  float arg[NS][8][2];
-  auto prob = [&](const Scores& s, int x, int w, float nm, int stage) {
-    float* e = arg[x][w];
-    if (stage == 0) {
-      e[0] = __builtin_fmaf(s[x][2 * w], cr[x], nm);
-      e[1] = __builtin_fmaf(s[x][2 * w + 1], cr[x], nm);
-    } else if (stage == 1) {
-      e[0] = __builtin_amdgcn_exp2f(e[0]);
-      e[1] = __builtin_amdgcn_exp2f(e[1]);
-    } else if (stage == 2) {
-      pk[x][w] = pack_f16(e[0], e[1]);   // the second product takes p with 11 significant bits, and so does the sum
-    } else {
-      lb[x] = __builtin_amdgcn_fdot2(__builtin_bit_cast(v2h, pk[x][w]), one, lb[x], false);
-    }
+  auto prob = [&](const Scores& s, int x, int w, float nm) {   // probabilities 2 w and 2 w + 1 of a set
+    const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][2 * w], cr[x], nm));
+    const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][2 * w + 1], cr[x], nm));
+    pk[x][w] = pack_f16(e0, e1);   // the second product takes p with 11 significant bits, and so does the sum
+    lb[x] = __builtin_amdgcn_fdot2(__builtin_bit_cast(v2h, pk[x][w]), one, lb[x], false);
   };
   // scores of keys from j0 (of the part) on that a row does not see; bad: absent groups of 16
   auto exclude = [&](Scores& s, int j0, uint32_t bad) {
@@ -701,7 +698,6 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
       nm[x] = m[x] == -INFINITY ? 0.f : -m[x];
       lb[x] = 0.f;
     }
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int t = 0; t < KC; ++t) {
       const v8h f = __builtin_bit_cast(v8h, frag[t % AHEAD]);
@@ -709,23 +705,12 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
       for (int x = 0; x < NS; ++x) {
         qk(next, x, t, f);
 #pragma unroll
-        for (int g = 3; g >= 0; --g)
-#pragma unroll
-          for (int w = max(t - g, 0) * 8 / KC; w < max(t - g + 1, 0) * 8 / KC; ++w) prob(s, x, w, nm[x], g);
+        for (int w = t * 8 / KC; w < (t + 1) * 8 / KC; ++w) prob(s, x, w, nm[x]);
       }
       extra(t);
       if (t + AHEAD < KC) fetch_k(t + AHEAD, half);
       else if constexpr (then >= 0) fetch_v(t + AHEAD - KC, then);
-      __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int t = KC; t < KC + 3; ++t)
-#pragma unroll
-      for (int g = 3; g > t - KC; --g)
-#pragma unroll
-        for (int x = 0; x < NS; ++x)
-#pragma unroll
-          for (int w = (t - g) * 8 / KC; w < (t - g + 1) * 8 / KC; ++w) prob(s, x, w, nm[x], g);
     bool again = false;
 #pragma unroll
     for (int x = 0; x < NS; ++x) again |= !(lb[x] <= kMost) || m[x] == -INFINITY;
@@ -747,9 +732,7 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
           for (int e = 0; e < 16; ++e) o[x][d][e] *= f;
         lb[x] = 0.f;
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int w = 0; w < 8; ++w) prob(s, x, w, mn == -INFINITY ? 0.f : -mn, g);
+        for (int w = 0; w < 8; ++w) prob(s, x, w, mn == -INFINITY ? 0.f : -mn);
       }
     }
 #pragma unroll
@@ -758,7 +741,6 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
   // Phase 2: the probabilities by V's half `half`; convert(t) is called in every step.
   auto phase2 = [&](auto half_, auto then_, auto&& convert) {
     constexpr int half = half_(), then = then_();    // then: the half of K whose fragments come next
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int t = 0; t < KC; ++t) {
       convert(t);
@@ -771,7 +753,6 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
       }
       if (t + AHEAD < KC) fetch_v(t + AHEAD, half);
       else fetch_k(t + AHEAD - KC, then);
-      __builtin_amdgcn_sched_barrier(0);
     }
   };
   struct None { constexpr int operator()() const { return -1; } };
@@ -786,12 +767,19 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
 
   Scores s0, s1;               // of the first and second half of a block
   if (n > 0) {
-    uint32_t bad = absent(pg0), next_bad = 0;
-    int pg4 = -1;
+    uint32_t bad = absent(pg[0]), next_bad = 0;
+    int next_pg = -1;
 #pragma unroll
-    for (int y = 0; y < MATS; ++y)
+    for (int y = 0; y < 2; ++y) {
+      if (y == 1 && only_v) continue;
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) store(mat[y], raw[y], x, 0);
+      for (int x = 0; x < D / 32; ++x) store(mat[0], early[y], x, y * C::MAT);
+    }
+    if constexpr (MATS == 2) {
+      raw[1] = load_raw(mat[1], 0, pg[0]);
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) store(mat[1], raw[1], x, 0);
+    }
     sync();
 #pragma unroll
     for (int t = 0; t < KC; ++t) {
@@ -801,52 +789,47 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
     }
 #pragma unroll
     for (int t = 0; t < AHEAD; ++t) fetch_k(t, 1);
-    // Block 1 of K; of V it is converted in the first iteration.
-    const bool only_v = MATS == 1 && wave >= 4;
-    if (!only_v)
-#pragma unroll
-      for (int x = 0; x < D / 32; ++x) store(mat[0], second, x, C::MAT);
     // What an iteration converts first: in the order in which it loads them, so
     // that a wait for the older one leaves the younger in flight.
-    raw[0] = load_raw(mat[0], only_v ? BN : 2 * BN, only_v ? pg1 : pg2);
+    raw[0] = load_raw(mat[0], (only_v ? 1 : 2) * BN, only_v ? pg[1] : pg[2]);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (MATS == 2) raw[1] = load_raw(mat[1], BN, pg1);
+    if constexpr (MATS == 2) raw[1] = load_raw(mat[1], BN, pg[1]);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     for (int i = 0; i < n; ++i) {
-      const int odd = i & 1;
-      const uint32_t buf0 = odd == (int)only_v ? 0 : C::MAT, buf1 = odd ? 0 : C::MAT;   // K of block i + 2, V of block i + 1
+      const uint32_t bufk = (i & 1) * C::MAT, bufv = C::MAT - bufk;   // of blocks i + 2 and i + 1
+      const uint32_t buf0 = only_v ? bufv : bufk;
       exclude(s0, i * BN, bad);
       phase1(s0, s1, Second(), None(), [&](int t) {
-        if (t == 1) next_bad = absent(pg1);
+        if (t == 1) next_bad = absent(pg[1]);
       });
-      flip(odd ? -C::MAT : C::MAT, 0);
+      flip(i & 1 ? -C::MAT : C::MAT, 0);
       sync();
 #pragma unroll
       for (int t = 0; t < AHEAD; ++t) fetch_v(t, 0);
       phase2(First(), First(), [&](int t) {
         if (t % (2 * C::STRIDE) == 0) store(mat[0], raw[0], t / (2 * C::STRIDE), buf0);
-        if (MATS == 2 && t == KC - 1) raw[0] = load_raw(mat[0], (i + 3) * BN, pg3);
+        if (MATS == 2 && t == KC - 1) raw[0] = load_raw(mat[0], (i + 3) * BN, pg[3]);
       });
       exclude(s1, i * BN + 32, bad >> 2);
       phase1(s1, s0, First(), Second(), [&](int t) {
-        if (t == 1) pg4 = load_pages((i + 4) * BN);
+        if (t == 1) next_pg = load_pages((i + 4) * BN);
       });
       phase2(Second(), Second(), [&](int t) {
         if constexpr (MATS == 2) {
-          if (t % 2 == 0) store(mat[1], raw[1], t / 2, buf1);
-          if (t == KC - 1) raw[1] = load_raw(mat[1], (i + 2) * BN, pg2);
+          if (t % 2 == 0) store(mat[1], raw[1], t / 2, bufv);
+          if (t == KC - 1) raw[1] = load_raw(mat[1], (i + 2) * BN, pg[2]);
         } else {
           if (t % 4 == 0) store(mat[0], raw[0], D / 64 + t / 4, buf0);
-          if (t == KC - 1) raw[0] = load_raw(mat[0], (i + (only_v ? 2 : 3)) * BN, only_v ? pg2 : pg3);
+          if (t == KC - 1) raw[0] = load_raw(mat[0], (i + (only_v ? 2 : 3)) * BN, only_v ? pg[2] : pg[3]);
         }
       });
-      flip(0, odd ? -C::MAT : C::MAT);
+      flip(0, i & 1 ? -C::MAT : C::MAT);
       bad = next_bad;
-      pg1 = pg2;
-      pg2 = pg3;
-      pg3 = pg4;
+#pragma unroll
+      for (int x = 0; x < 3; ++x) pg[x] = pg[x + 1];
+      pg[3] = next_pg;
     }
   }
 
