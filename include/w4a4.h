@@ -574,7 +574,8 @@ typedef struct w4a4_kvcache {
  *         strides (elements) multiples of 8, pointers 16-byte aligned.
  *  slots  device int32[M]: the token slot of each row.  A slot outside the
  *         cache skips its row.  Slots are distinct: one that is given twice
- *         holds a mixture of its rows afterwards, other slots are right. */
+ *         holds a mixture of its rows afterwards, other slots are right.
+ * M < 2^31, M Hkv D <= 2^34. */
 int w4a4_cache_append(const w4a4_kvcache* c, const void* k, int64_t k_sm, int64_t k_sh, const void* v, int64_t v_sm,
                       int64_t v_sh, int32_t dtype, int64_t M, const int32_t* slots, void* stream);
 
@@ -604,7 +605,8 @@ int w4a4_cache_read(const w4a4_kvcache* c, const int32_t* slots, int64_t M, void
  *  lens      device int32[B], clamped to [0, min(max_len, table_pages * page)].
  *  max_len   an upper bound of lens that the host knows; it sizes the work.
  * Shape rules: Hq a multiple of Hkv, Hq <= 65536; B, T <= 2^24,
- * B T Hq <= 2^30; max_len, table_pages * page <= 2^30. */
+ * B T Hq <= 2^30, B Hkv ceil(T (Hq / Hkv) / 16) <= 2^22; max_len,
+ * table_pages * page <= 2^30. */
 typedef struct w4a4_cache_attn {
   int64_t B, T, Hq, max_len;
   float scale;

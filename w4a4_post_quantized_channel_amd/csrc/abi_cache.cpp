@@ -86,7 +86,8 @@ int check_io(const char* fn, const w4a4_kvcache* c, const void* k, int64_t k_sm,
   if (st != W4A4_OK) return st;
   if ((st = check_float(fn, "k / v", dtype)) != W4A4_OK) return st;
   if (M < 0) return fail(W4A4_ERR_INVALID_ARG, "%s: bad sizes", fn);
-  if (M > INT32_MAX || M > (1LL << 40) / (c->Hkv * c->D))
+  // (the grid counts fewer than 2^32 threads, one per 16 channels of k and v)
+  if (M > INT32_MAX || M > (1LL << 34) / (c->Hkv * c->D))
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: too many tokens", fn);
   if (M == 0) return ok();
   const struct {
@@ -129,7 +130,9 @@ int check_attn_sizes(const char* fn, int64_t B, int64_t T, int64_t Hq, int64_t H
   if (B < 0 || T < 0 || max_len < 0 || Hq <= 0) return fail(W4A4_ERR_INVALID_ARG, "%s: bad sizes", fn);
   if (Hq % Hkv != 0)
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: %lld query heads over %lld KV heads", fn, (long long)Hq, (long long)Hkv);
-  if (Hq > 65536 || max_len > (1LL << 30) || T > (1LL << 24) || B > (1LL << 24) || B * T > (1LL << 30) / Hq)
+  // (the grid counts fewer than 2^32 threads, 512 or fewer per 16 rows of a sequence and KV head)
+  if (Hq > 65536 || max_len > (1LL << 30) || T > (1LL << 24) || B > (1LL << 24) || B * T > (1LL << 30) / Hq ||
+      B * Hkv * ((T * (Hq / Hkv) + 15) / 16) > (1LL << 22))
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: sizes too large", fn);
   return ok();
 }

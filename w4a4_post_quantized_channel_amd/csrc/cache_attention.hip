@@ -16,7 +16,7 @@
 // fit fp16 for every channel down to 2^-27 of the largest.  Probabilities are
 // rounded to fp16 (2^-12 of them, a sixteenth of the output's own rounding).
 //
-// A wave works alone on every kFewWaves-th block of its workgroup's part, for
+// A wave works alone on every NW-th block of its workgroup's part, for
 // 16 MT rows at once:
 //  - S^T = K Q^T with v_mfma_f32_16x16x32_f16.  The order of channels inside a
 //    product is free, so lane (key r, group g) takes the D / 4 channels from
@@ -44,7 +44,7 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) v2i lds_v2i;
 
 constexpr float kLazy = 8.f;
-constexpr int NW = kFewWaves, BN = kCacheBlock;
+constexpr int BN = kCacheBlock;
 
 struct Args {
   w4a4_kvcache c;
@@ -127,9 +127,9 @@ __device__ __forceinline__ float row_factor(float amax, float& inverse) {
   return __uint_as_float((uint32_t)(267 - e) << 23);
 }
 
-template <int D_, int MT_>
+template <int D_, int MT_, int NW_>
 struct Few {
-  static constexpr int D = D_, MT = MT_, R = 16 * MT;
+  static constexpr int D = D_, MT = MT_, NW = NW_, R = 16 * MT;
   static constexpr int KS = D / 32;             // steps of the first product
   static constexpr int DT = D / 16;             // channel tiles, scales of a row
   static constexpr int CB = D / 8;              // bytes of codes a lane takes of a key
@@ -147,8 +147,8 @@ __device__ __forceinline__ int row_limit(const Args& p, int len, int t) {
 }
 
 template <typename C>
-__global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_kernel(Args p) {
-  constexpr int D = C::D, MT = C::MT, R = C::R, KS = C::KS, DT = C::DT;
+__global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 ? 2 : 1) attn_few_kernel(Args p) {
+  constexpr int D = C::D, MT = C::MT, NW = C::NW, R = C::R, KS = C::KS, DT = C::DT;
   __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -172,12 +172,17 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
   const int nblk = (max(last, 0) + BN - 1) / BN;
   const int per = (nblk + (int)p.parts.d - 1) / (int)p.parts.d;
   const int lo = min(part * per, nblk), hi = min(lo + per, nblk);
-  const int32_t* table = a.table + b * a.table_sb;
+  // (without keys there may be no table: any integer then)
+  const int32_t* table = hi > lo ? a.table + b * a.table_sb : a.lens;
 
-  // pages of a block's four groups of 16 keys, one a lane group; -1: absent
+  // pages of a block's four groups of 16 keys, one a lane group; -1: absent.
+  // Neither this load nor those of a block is ever left out, so that waits can
+  // count the younger ones: past the end they read entry 0 and page 0.
   auto load_pages = [&](int blk) {
     const int j = blk * BN + 16 * lg;
-    return blk < hi && j < last ? table[j >> p.lp] : -1;
+    const bool in = blk < hi && j < last;
+    const int pg = table[in ? j >> p.lp : 0];
+    return in ? pg : -1;
   };
   Words<C::CB> kw[4], vw[4];        // a block's codes and scales: K by tiles of 16 keys
   Words<C::CB / 8> ksw[4];
@@ -211,8 +216,16 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
   };
 
   int pg = load_pages(lo + wave), pg1 = load_pages(lo + wave + NW);
+  // loads stay in this order, so that a wait for the older ones leaves the younger in flight
+  auto in_order = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  in_order();
   load_v(lo + wave, pg);
+  in_order();
   load_k(lo + wave, pg);
+  in_order();
 
   // queries, limits
   v8h qf[MT][KS];
@@ -267,7 +280,6 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
   for (int blk = lo + wave; blk < hi; blk += NW) {
     const int j0 = blk * BN;
     const uint32_t absent = bad;
-    const bool more = blk + NW < hi;
     pg = pg1;
     pg1 = load_pages(blk + 2 * NW);
 
@@ -287,7 +299,9 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
         *reinterpret_cast<uint16_t*>(sl + (d * BN + at) * 2) = (uint16_t)scale_bits(vsw.w[d / 4] >> (8 * (d & 3)));
     }
 
-    if (more) load_v(blk + NW, pg);
+    in_order();
+    load_v(blk + NW, pg);
+    in_order();
 
     v4f s[MT][4];
 #pragma unroll
@@ -302,7 +316,9 @@ __global__ void __launch_bounds__(64 * NW, C::LDS > 80 * 1024 ? 1 : 2) attn_few_
         for (int x = 0; x < MT; ++x) s[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[x][k], s[x][t], 0, 0, 0);
       }
     }
-    if (more) load_k(blk + NW, pg);
+    in_order();
+    load_k(blk + NW, pg);
+    in_order();
     if (absent || j0 + BN > first) {
 #pragma unroll
       for (int x = 0; x < MT; ++x) {
@@ -896,7 +912,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(Args p) {
 template <typename C>
 void launch_few(const Args& p, hipStream_t st) {
   const unsigned grid = (unsigned)(p.a.B * p.c.Hkv * p.tiles.d * p.parts.d);
-  attn_few_kernel<C><<<grid, 64 * NW, 0, st>>>(p);
+  attn_few_kernel<C><<<grid, 64 * C::NW, 0, st>>>(p);
 }
 
 template <typename C>
@@ -930,17 +946,18 @@ hipError_t launch_cache_attention(const w4a4_kvcache& c, const w4a4_cache_attn& 
     p.po = (float*)workspace;
     p.pml = p.po + (size_t)pl.parts * a.B * a.T * a.Hq * c.D;
   }
+  const bool four = pl.waves == 4;
   if (c.D == 64) {
-    if (pl.rows == 16) launch_few<Few<64, 1>>(p, st);
-    else if (pl.rows == 32) launch_few<Few<64, 2>>(p, st);
+    if (pl.rows == 16) four ? launch_few<Few<64, 1, 4>>(p, st) : launch_few<Few<64, 1, 8>>(p, st);
+    else if (pl.rows == 32) launch_few<Few<64, 2, 8>>(p, st);
     else launch_many<Many<64, 8, 1>>(p, st);
   } else if (c.D == 128) {
-    if (pl.rows == 16) launch_few<Few<128, 1>>(p, st);
-    else if (pl.rows == 32) launch_few<Few<128, 2>>(p, st);
+    if (pl.rows == 16) four ? launch_few<Few<128, 1, 4>>(p, st) : launch_few<Few<128, 1, 8>>(p, st);
+    else if (pl.rows == 32) launch_few<Few<128, 2, 8>>(p, st);
     else launch_many<Many<128, 8, 1>>(p, st);
   } else {
-    if (pl.rows == 16) launch_few<Few<256, 1>>(p, st);
-    else if (pl.rows == 32) launch_few<Few<256, 2>>(p, st);
+    if (pl.rows == 16) four ? launch_few<Few<256, 1, 4>>(p, st) : launch_few<Few<256, 1, 8>>(p, st);
+    else if (pl.rows == 32) launch_few<Few<256, 2, 4>>(p, st);
     else launch_many<Many<256, 4, 1>>(p, st);
   }
   hipError_t e = hipGetLastError();

@@ -7,28 +7,68 @@ namespace w4a4 {
 
 struct CacheAttnPlan {
   int rows;      // query rows (token, head of the group) of a workgroup
+  int waves;     // of a workgroup
   int tiles;     // row tiles of a sequence and KV head
   int parts;
 };
 
-constexpr int kFewWaves = 4;      // waves of a workgroup, each with key blocks of its own
 constexpr int kCacheBlock = 64;   // keys of a block
 
+// The kernels of a head width.  16 and 32 rows: every wave takes key blocks of
+// its own, so an iteration covers ``waves`` blocks; more rows: the waves share a
+// block.  us: an iteration, all CUs busy (fitted, see below).
+struct CacheAttnShape {
+  int rows, waves;
+  double us;
+};
+constexpr int kCacheShapes = 4;
+constexpr CacheAttnShape kCacheAttnShapes[3][kCacheShapes] = {
+    {{16, 4, 1.6}, {16, 8, 1.3}, {32, 8, 2.2}, {256, 8, 1.1}},      // D = 64 (estimates)
+    {{16, 4, 2.6}, {16, 8, 2.0}, {32, 8, 3.4}, {256, 8, 1.85}},     // D = 128
+    {{16, 4, 5.0}, {16, 8, 4.6}, {32, 4, 4.5}, {128, 4, 2.0}}};     // D = 256
+constexpr int kCacheCUs = 256;
+
+// Microseconds, fitted to measurements of D = 128 and 256 (a chunk of 8 x 50,
+// 16 heads over 4, 2090 keys: 24 with 32 rows a workgroup, 29 with 16, 33 with
+// 256; 200 queries of 8 heads over 8192 keys: 25 with 32 rows, 33 with 256; 500
+// queries of 8 heads over one of width 256, 4096 keys: 79 with 32, 86 with 16,
+// 57 with 128): iterations, start and end of a workgroup, and the join's launch,
+// parts and bytes.  A part of the kernels for few rows is about 32 blocks at
+// most, so that a batch of unequal histories fills the card to its end (64
+// sequences of 4096 to 8192 keys, 32 heads over 8: 104 us in four parts, 116 in
+// one).
 inline CacheAttnPlan plan_cache_attention(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len,
                                           bool split) {
-  const int64_t rows = T * (Hq / Hkv);
-  CacheAttnPlan p;
-  p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : D == 256 ? 128 : 256;
-  p.tiles = (int)((rows + p.rows - 1) / p.rows);
-  const int64_t units = B * Hkv * p.tiles, blocks = (max_len + kCacheBlock - 1) / kCacheBlock;
-  // Parts: up to three workgroups of the few-row kernel a CU with at least a
-  // block a wave, or one of the many-row kernel.
-  const bool few = p.rows <= 32;
-  const int64_t most = few ? (blocks + kFewWaves - 1) / kFewWaves : (blocks + 1) / 2;
-  int64_t parts = split ? (few ? 768 : 256) / units : 1;
-  if (parts > most) parts = most;
-  p.parts = (int)(parts < 1 ? 1 : parts);
-  return p;
+  const CacheAttnShape* shapes = kCacheAttnShapes[D == 64 ? 0 : D == 128 ? 1 : 2];
+  if (B * T * Hq > 1 << 22) split = false;                   // the card is full of rows
+  const int64_t rows = T * (Hq / Hkv), blocks = (max_len + kCacheBlock - 1) / kCacheBlock;
+  CacheAttnPlan best{};
+  double best_cost = 1e300;
+  for (int c = 0; c < kCacheShapes; ++c) {
+    const CacheAttnShape& s = shapes[c];
+    const bool few = s.rows <= 32;
+    const int64_t step = few ? s.waves : 1;                  // blocks of an iteration
+    const int64_t tiles = (rows + s.rows - 1) / s.rows, units = B * Hkv * tiles;
+    const int64_t slots = few && s.waves == 4 && s.rows == 16 ? 2 * kCacheCUs : kCacheCUs;
+    int64_t most = split ? (blocks + step - 1) / step : 1;
+    if (most > 64) most = 64;
+    if (most < 1) most = 1;
+    int64_t parts = split && few ? (blocks + 15) / 32 : 1;
+    if (parts > most) parts = most;
+    if (parts < 1) parts = 1;
+    for (;; parts = parts * 2 < most ? parts * 2 : most) {
+      const int64_t per = blocks < 1 ? 1 : (blocks + parts - 1) / parts;
+      const int64_t iters = (per + step - 1) / step, rounds = (units * parts + slots - 1) / slots;
+      double cost = rounds * (iters * s.us + 6.0);
+      if (parts > 1) cost += 4.0 + 0.1 * parts + (double)parts * B * Hkv * rows * D * 8.0 / 4e6;
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {s.rows, s.waves, (int)tiles, (int)parts};
+      }
+      if (parts == most) break;
+    }
+  }
+  return best;
 }
 
 }  // namespace w4a4
