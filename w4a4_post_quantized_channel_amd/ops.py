@@ -147,14 +147,14 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+_DTYPES = {torch.bfloat16: DT_BF16, torch.float32: DT_F32, torch.int32: DT_I32}
+
+
 def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
-        return DT_BF16
-    if t.dtype == torch.float32:
-        return DT_F32
-    if t.dtype == torch.int32:
-        return DT_I32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _rowmajor(t: torch.Tensor):
@@ -808,18 +808,20 @@ def rotary_axes(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, t
     i + pairs; channels behind the pairs are copied.  q_out / k_out may be q / k themselves.
     Returns (q_out, k_out).
     """
-    M, Hq, D = q.shape
+    shape, dtype = q.shape, q.dtype
+    M, Hq, D = shape
     if q_out is None:
-        q_out = torch.empty((M, Hq, D), dtype=q.dtype, device=q.device)
-    qm, qh, _ = _cache_rows("q", q, (M, Hq, D), q.dtype)
-    qom, qoh, _ = _cache_rows("q_out", q_out, (M, Hq, D), q.dtype)
-    Hk, kp, km, kh, kop, kom, koh = 0, 0, 0, 0, 0, 0, 0
+        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+    qm, qh, _ = _cache_rows("q", q, shape, dtype)
+    qom, qoh, _ = _cache_rows("q_out", q_out, shape, dtype)
+    Hk = kp = km = kh = kop = kom = koh = 0
     if k is not None:
         Hk = k.shape[1]
+        kshape = (M, Hk, D)
         if k_out is None:
-            k_out = torch.empty((M, Hk, D), dtype=q.dtype, device=q.device)
-        km, kh, _ = _cache_rows("k", k, (M, Hk, D), q.dtype)
-        kom, koh, _ = _cache_rows("k_out", k_out, (M, Hk, D), q.dtype)
+            k_out = torch.empty(kshape, dtype=dtype, device=q.device)
+        km, kh, _ = _cache_rows("k", k, kshape, dtype)
+        kom, koh, _ = _cache_rows("k_out", k_out, kshape, dtype)
         kp, kop = k.data_ptr(), k_out.data_ptr()
     axes = len(table.sections)
     if pos.dtype not in (torch.int32, torch.float32) or pos.shape != (M, axes) or (axes > 1 and pos.stride(1) != 1):
@@ -835,6 +837,30 @@ def rotary_axes(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, t
 
 
 NORMS = {"layer": 0, "rms": 1}
+
+
+def _like(name: str, t: torch.Tensor, shape):
+    """(address, row stride) of a row-major matrix of that shape."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must be row-major")
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+
+
+def _fp32(name: str, t: Optional[torch.Tensor], shape):
+    """(address, row stride) of an fp32 matrix or vector of that shape; (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be fp32")
+    if t.shape != shape:
+        raise (ValueError if len(shape) == 2 else TypeError)(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise (ValueError if len(shape) == 2 else TypeError)(f"{name} must have contiguous channels")
+    return t.data_ptr(), st[0]
 
 
 def gated_norm(x: torch.Tensor, h: Optional[torch.Tensor] = None, *, gate: Optional[torch.Tensor] = None,
@@ -853,46 +879,41 @@ def gated_norm(x: torch.Tensor, h: Optional[torch.Tensor] = None, *, gate: Optio
     x itself.  norm=False leaves y out, and without h there is no x_out unless it is passed.
     Returns (x_out, y).
     """
-    if kind not in NORMS:
+    code = NORMS.get(kind)
+    if code is None:
         raise ValueError(f"unknown norm {kind!r}: one of {sorted(NORMS)}")
+    shape = x.shape
     M, C, ldx = _matrix("x", x)
     if x_out is None and h is not None:
         x_out = torch.empty((M, C), dtype=x.dtype, device=x.device)
     if y is None and norm:
         y = torch.empty((M, C), dtype=y_dtype, device=x.device)
-    at, ld = [0] * 3, [0] * 3
-    for i, (name, t) in enumerate((("h", h), ("x_out", x_out), ("y", y))):
-        if t is None:
-            continue
-        rows, cols, ld[i] = _matrix(name, t)
-        if rows != M or cols != C:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(M, C)}")
-        at[i] = t.data_ptr()
-    if x_out is not None and x_out.dtype is not x.dtype:
-        raise TypeError("x_out must have x's dtype")
-    R, mods = None, []
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if t is None:
-            mods += [0, 0]
-            continue
-        rows, cols, s = _matrix(name, t)
-        if t.dtype is not torch.float32:
-            raise TypeError(f"{name} must be fp32")
-        if cols != C or (R is not None and rows != R):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows if R is None else R, C)}")
-        R = rows
-        mods += [t.data_ptr(), s]
-    vecs = []
-    for name, t in (("post_weight", post_weight), ("weight", weight), ("bias", bias)):
-        if t is not None and (t.dtype is not torch.float32 or t.shape != (C,) or not t.is_contiguous()):
-            raise TypeError(f"{name} must be a contiguous fp32[C] tensor")
-        vecs.append(0 if t is None else t.data_ptr())
+    hp = ldh = xop = ldxo = yp = ldy = 0
+    if h is not None:
+        hp, ldh = _like("h", h, shape)
+    if x_out is not None:
+        xop, ldxo = _like("x_out", x_out, shape)
+        if x_out.dtype is not x.dtype:
+            raise TypeError("x_out must have x's dtype")
+    if y is not None:
+        yp, ldy = _like("y", y, shape)
+    first = gate if gate is not None else scale if scale is not None else shift
+    R, mods = 1, (0, 0, 0, 0, 0, 0)
+    if first is not None:
+        if first.dim() != 2 or first.shape[1] != C:
+            raise ValueError(f"modulations must be [R, {C}], got {tuple(first.shape)}")
+        mshape = first.shape
+        R = mshape[0]
+        mods = (*_fp32("gate", gate, mshape), *_fp32("scale", scale, mshape), *_fp32("shift", shift, mshape))
+    vshape = shape[1:]
+    pw, wp, bp = (_fp32("post_weight", post_weight, vshape)[0], _fp32("weight", weight, vshape)[0],
+                  _fp32("bias", bias, vshape)[0])
     xp = _together("h gate scale shift post_weight weight bias x_out y", x, h, gate, scale, shift, post_weight, weight,
                    bias, x_out, y)
     xdt = _dtype_code(x)
     st = LIB.w4a4_gated_norm(
-        _GATED.pack(M, C, 1 if R is None else R, alpha, eps, NORMS[kind], xdt, xdt if h is None else _dtype_code(h),
-                    xdt if y is None else _dtype_code(y), xp, ldx, at[0], ld[0], *mods, *vecs, at[1], ld[1], at[2], ld[2]),
+        _GATED.pack(M, C, R, alpha, eps, code, xdt, xdt if h is None else _dtype_code(h),
+                    xdt if y is None else _dtype_code(y), xp, ldx, hp, ldh, *mods, pw, wp, bp, xop, ldxo, yp, ldy),
         _stream_for(x, stream))
     if st != 0:
         _check("w4a4_gated_norm", st)
