@@ -460,6 +460,16 @@ def _rotary_reference(x, pos, sections, interleaved):
     return y, size
 
 
+def _assert_rotary(got, x, pos, sections, interleaved):
+    """The angle is off by 2^-25 of a turn at most (2^-22.3), sine and cosine by 2^-23, three roundings in 24 bits:
+    under 2^-21 of |u| + |w|; then the output's own rounding.  Channels behind the pairs are copied."""
+    want, size = _rotary_reference(x, pos, sections, interleaved)
+    tol = torch.finfo(x.dtype).eps / 2 * want.abs() + 2.0 ** -21 * size
+    err = (got.double().cpu() - want).abs()
+    assert bool((err <= tol).all()), float((err - tol).max())
+    assert torch.equal(got[..., 2 * sum(sections):], x[..., 2 * sum(sections):])
+
+
 @pytest.mark.parametrize("i", range(len(ROTARY)))
 @pytest.mark.parametrize("how", ["new", "views", "in place"])
 def test_rotary(ops, i, how):
@@ -479,16 +489,8 @@ def test_rotary(ops, i, how):
     kw = dict(q_out=q, k_out=k if Hk else None) if how == "in place" else {}
     qo, ko = ops.rotary_axes(q, k if Hk else None, wide.to(DEV)[:, :len(sections)], table, interleaved=inter, **kw)
     for x, got in ((q0, qo), (k0, ko)):
-        if x.shape[1] == 0:
-            continue
-        want, size = _rotary_reference(x, pos, sections, inter)
-        # the angle is off by 2^-25 of a turn at most (2^-22.3), sine and cosine by 2^-23, three roundings in 24
-        # bits: under 2^-21 of |u| + |w|; then the output's own rounding
-        tol = torch.finfo(dtype).eps / 2 * want.abs() + 2.0 ** -21 * size
-        err = (got.double().cpu() - want).abs()
-        assert bool((err <= tol).all()), float((err - tol).max())
-        rest = got[..., 2 * sum(sections):]
-        assert torch.equal(rest, x[..., 2 * sum(sections):])
+        if x.shape[1]:
+            _assert_rotary(got, x, pos, sections, inter)
     if how == "in place":
         assert torch.equal(big[:, Hq + Hk:], before[:, Hq + Hk:]) and torch.equal(big[..., D:], before[..., D:])
 
@@ -568,6 +570,27 @@ def _gated_reference(x, h, gate, alpha, post, kind, weight, bias, scale, shift, 
     return xn, size, n, rs, y, f, extra
 
 
+def _assert_gated(xo, y, ref, post):
+    """Sums of C values in 24 bits over at most 64 steps a thread and ten joins: 74 2^-24 of the sum of sizes at
+    most, and half of that again for divisions and roots: 2^-17.  x' carries 2^-17 of h's part for the inner norm
+    and four roundings; y the same of |n| (a value's own error through rs, and rs itself), of the mean's size, and
+    of what is added.  Then each output's own rounding."""
+    xn, size, n, rs, want, f, extra = ref
+    e = 2.0 ** -17 if post else 2.0 ** -22
+    tx = e * size
+    if xo is not None:
+        tol = torch.finfo(xo.dtype).eps / 2 * xn.abs() + tx + 1e-30
+        err = (xo.double().cpu() - xn).abs()
+        assert bool((err <= tol).all()), float((err - tol).max())
+    if y is not None:
+        mean_err = (2.0 ** -17 + e) * size.mean(-1, keepdim=True)
+        ty = f * (rs * (tx + mean_err) + n.abs() * (2.0 ** -17 + e) + n.abs() * rs * size.mean(-1, keepdim=True) * e * 2)
+        ty = ty + 2.0 ** -21 * (f * n.abs() + extra)
+        err = (y.double().cpu() - want).abs()
+        tol = torch.finfo(y.dtype).eps / 2 * want.abs() + ty * 1.01
+        assert bool((err <= tol).all()), float((err - tol).max())
+
+
 @pytest.mark.parametrize("i", range(len(GATED)))
 @pytest.mark.parametrize("how", ["new", "views", "in place"])
 def test_gated_norm(ops, i, how):
@@ -589,25 +612,8 @@ def test_gated_norm(ops, i, how):
     before = bx.clone()
     xo, y = ops.gated_norm(x, h, **kw, y_dtype=yd, x_out=x if how == "in place" else None)
     torch.cuda.synchronize()
-    xn, size, n, rs, want, f, extra = ref
-    # Sums of C values in 24 bits over at most 64 steps a thread and ten joins: 74 2^-24 of the sum of sizes at
-    # most, and half of that again for divisions and roots: 2^-17.  x' carries 2^-17 of h's part for the inner
-    # norm and four roundings; y the same of |n| (a value's own error through rs, and rs itself), of the mean's
-    # size, and of what is added.
-    e = 2.0 ** -17 if post else 2.0 ** -22
-    tx = e * size
-    mean_err = (2.0 ** -17 + e) * size.mean(-1, keepdim=True)
-    ty = f * (rs * (tx + mean_err) + n.abs() * (2.0 ** -17 + e) + n.abs() * rs * size.mean(-1, keepdim=True) * e * 2)
-    ty = ty + 2.0 ** -21 * (f * n.abs() + extra)
-    if xo is not None:
-        tol = torch.finfo(xd).eps / 2 * xn.abs() + tx + 1e-30
-        err = (xo.double().cpu() - xn).abs()
-        assert bool((err <= tol).all()), float((err - tol).max())
-    else:
-        assert not has_h
-    err = (y.double().cpu() - want).abs()
-    tol = torch.finfo(yd).eps / 2 * want.abs() + ty * 1.01
-    assert bool((err <= tol).all()), float((err - tol).max())
+    assert (xo is None) == (not has_h and how != "in place")
+    _assert_gated(xo, y, ref, post)
     if how == "in place" and xo is not None:
         assert xo.data_ptr() == x.data_ptr() and torch.equal(bx[:, C:], before[:, C:])
     else:

@@ -629,11 +629,18 @@ def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
 # These check that their operands lie on the current device, whose stream they
 # take.
 # ---------------------------------------------------------------------------
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the handle alone, without a Stream object
+
+
 def _stream_for(t, stream) -> int:
     """The stream of a call on ``t``'s device, which has to be the current one."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"the operands are on {t.device}, the current device is cuda:{torch.cuda.current_device()}: "
-                         f"call under torch.cuda.device({t.device.index})")
+    if t.is_cuda:
+        index = t.device.index
+        if index != torch.cuda.current_device():
+            raise ValueError(f"the operands are on {t.device}, the current device is cuda:{torch.cuda.current_device()}: "
+                             f"call under torch.cuda.device({index})")
+        if stream is None and _raw_stream is not None:
+            return _raw_stream(index)
     return _stream(stream)
 
 
