@@ -1,0 +1,123 @@
+"""Every tile of the attention over the 4-bit cache, with and without parts, at
+the ends of what it covers: ragged histories, absent pages, rows that see
+nothing, strides.  References in 64 bits on the GPU."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import test_cache_ops_gpu as R  # noqa: E402  (values of a cache, tolerance)
+
+DEV = "cuda"
+
+# (D, rows of a workgroup, its waves, in parts): B, T, Hq, Hkv, max_len, with workspace
+SHAPES = {
+    (64, 16, 4, False): (17, 5, 32, 8, 41, True), (64, 16, 4, True): (11, 1, 12, 4, 2707, True),
+    (64, 16, 8, False): (1, 3, 5, 1, 150, False), (64, 16, 8, True): (1, 2, 7, 1, 2056, True),
+    (64, 32, 8, False): (6, 184, 4, 1, 268, False), (64, 32, 8, True): (1, 176, 4, 1, 2747, True),
+    (64, 256, 8, False): (4, 600, 4, 2, 330, False), (64, 256, 8, True): (1, 1062, 8, 4, 675, True),
+    (128, 16, 4, False): (17, 6, 24, 8, 33, True), (128, 16, 4, True): (17, 1, 4, 4, 1655, True),
+    (128, 16, 8, False): (1, 4, 4, 1, 700, False), (128, 16, 8, True): (1, 1, 9, 1, 1562, True),
+    (128, 32, 8, False): (6, 228, 3, 1, 260, False), (128, 32, 8, True): (2, 62, 8, 1, 2068, True),
+    (128, 256, 8, False): (6, 400, 4, 2, 300, False), (128, 256, 8, True): (3, 318, 9, 3, 595, True),
+    (256, 16, 4, False): (52, 1, 10, 5, 60, False), (256, 16, 4, True): (13, 9, 8, 1, 1555, True),
+    (256, 16, 8, False): (1, 2, 3, 1, 200, False), (256, 16, 8, True): (1, 1, 4, 1, 537, True),
+    (256, 32, 4, False): (1, 10, 2, 1, 130, False), (256, 32, 4, True): (5, 63, 5, 1, 1053, True),
+    (256, 128, 4, False): (1, 50, 5, 1, 70, False), (256, 128, 4, True): (1, 7, 5, 1, 555, True),
+}
+
+
+def _reference(q, c, table, lens, causal, scale, max_len):
+    """_attention_reference by products of a sequence and KV head."""
+    B, T, Hq, D = q.shape
+    G, page = Hq // c.Hkv, c.page
+    kv, gk = R._values(c.k_codes, c.k_scales, c.k_scale)
+    vv, gv = R._values(c.v_codes, c.v_scales, c.v_scale)
+    kv, vv = kv.to(DEV) * gk, vv.to(DEV) * gv
+    out = torch.zeros(B, T, Hq, D, dtype=torch.float64, device=DEV)
+    A, smax = torch.zeros_like(out), torch.zeros(B, T, Hq, 1, dtype=torch.float64, device=DEV)
+    for b in range(B):
+        n = max(0, min(int(lens[b]), table.shape[1] * page, max_len))
+        j = torch.arange(n, device=DEV)
+        pg = table[b, j // page] if n else j.int()
+        held = (pg >= 0) & (pg < c.n_pages)
+        j, pg = j[held], pg[held].long()
+        if not len(j):
+            continue
+        end = n - T + torch.arange(T, device=DEV) + 1 if causal else torch.full((T,), n, device=DEV)
+        see = (j < end.unsqueeze(1)).repeat_interleave(G, 0)             # [T G, n]
+        for h in range(c.Hkv):
+            k, v = kv[pg, h, j % page], vv[pg, h, j % page]
+            x = q[b, :, h * G:(h + 1) * G].double().reshape(T * G, D)
+            s = (x @ k.t().contiguous() * scale).masked_fill(~see, -torch.inf)
+            p = torch.nan_to_num(torch.softmax(s, -1), nan=0.0)
+            size = (x.abs() @ k.abs().t().contiguous()).masked_fill(~see, 0).amax(-1) * abs(scale)
+            at = (b, slice(None), slice(h * G, (h + 1) * G))
+            out[at], A[at] = (p @ v).view(T, G, D), (p @ v.abs()).view(T, G, D)
+            smax[at] = size.view(T, G, 1)
+    return out.cpu(), A.cpu(), smax.cpu()
+
+
+def _case(key, page, seed):
+    D, _, _, _ = key
+    B, T, Hq, Hkv, L, ws = SHAPES[key]
+    from w4a4_post_quantized_channel_amd import ops
+    pages = -(-L // page)
+    c = R._cache(ops, seed, B * pages + 1, page, Hkv, D, 2.0 ** -9, 2.0 ** -9)
+    g = torch.Generator().manual_seed(seed)
+    table = torch.randperm(B * pages + 1, generator=g)[:B * pages].view(B, pages).int()
+    lens = torch.randint(0, L + 1, (B,), generator=g).int()
+    lens[0] = L
+    if B > 2:
+        lens[1], lens[2] = 0, 1
+    for b in range(B):                                                   # a few pages that nobody holds
+        for bad in (-1, B * pages + 1, -2 ** 31):
+            if pages > 6:
+                table[b, int(torch.randint(0, pages, (1,), generator=g))] = bad
+    if B > 3:
+        table[3] = -1                                                    # a sequence whose history is gone
+    q = (R._rand(seed + 1, B, T, Hq, D) * 1.3).to(torch.bfloat16).to(DEV)
+    work = ops.make_cache_attention_workspace(B, T, Hq, Hkv, D, L, device=DEV) if ws else None
+    return ops, q, c, table.to(DEV), lens.to(DEV), L, work
+
+
+@pytest.mark.parametrize("key", list(SHAPES), ids=lambda k: "-".join(map(str, k)))
+@pytest.mark.parametrize("causal,page", [(False, 16), (True, 64), (True, 256)])
+def test_tile(key, causal, page):
+    ops, q, c, table, lens, L, ws = _case(key, page, 1000 + 7 * list(SHAPES).index(key) + page)
+    assert (ws is not None) == SHAPES[key][5] or not key[3]
+    out = ops.cache_attention(q, c, table, lens, causal=causal, max_len=L, workspace=ws)
+    ref = _reference(q, c, table, lens, causal, key[0] ** -0.5, L)
+    R._assert_attention(out, ref, L + page, 6 * 2.0 ** 6 * c.v_scale)
+    assert torch.equal(out, ops.cache_attention(q, c, table, lens, causal=causal, max_len=L, workspace=ws))
+
+
+@pytest.mark.parametrize("key", [(128, 16, 4, True), (128, 32, 8, True), (128, 256, 8, True), (256, 128, 4, True)],
+                         ids=lambda k: "-".join(map(str, k)))
+def test_a_later_maximum(key):
+    """Scores that climb by far more than the running maximum may lag, key after key, and fall again."""
+    ops, q, c, table, lens, L, ws = _case(key, 16, 77)
+    n = c.n_pages * 16
+    table.copy_(torch.arange(table.numel(), dtype=torch.int32).view(table.shape))
+    ramp = torch.arange(n, device=DEV)
+    ramp = torch.minimum(ramp % 600, 600 - ramp % 600) // 12             # scale codes 64 .. 89: factors of 1 to 9
+    c.k_scales.copy_((64 + ramp).view(c.n_pages, 1, 16, 1).expand_as(c.k_scales).to(torch.uint8))
+    out = ops.cache_attention(q * 3, c, table, lens, max_len=L, workspace=ws)
+    ref = _reference(q * 3, c, table, lens, False, key[0] ** -0.5, L)
+    R._assert_attention(out, ref, L + 16, 6 * 2.0 ** 6 * c.v_scale)
+
+
+@pytest.mark.parametrize("L,T", [(16383, 1), (16384, 33), (9001, 700)])
+def test_long_histories(L, T):
+    """Thousands of keys of nearly equal weight: what small probabilities add up to."""
+    from w4a4_post_quantized_channel_amd import ops
+    Hq, Hkv, D, page = 2, 1, 128, 128
+    pages = -(-L // page)
+    c = R._cache(ops, 5, pages, page, Hkv, D, 2.0 ** -12, 2.0 ** -9)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).view(1, pages)
+    lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+    q = R._rand(6, 1, T, Hq, D).to(torch.bfloat16).to(DEV)
+    ws = ops.make_cache_attention_workspace(1, T, Hq, Hkv, D, L, device=DEV)
+    for w in (ws, None):
+        out = ops.cache_attention(q, c, table, lens, causal=True, max_len=L, workspace=w)
+        R._assert_attention(out, _reference(q, c, table, lens, True, D ** -0.5, L), L, 6 * 2.0 ** 6 * c.v_scale)

@@ -40,18 +40,20 @@ constexpr int kCacheCUs = 256;
 inline CacheAttnPlan plan_cache_attention(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len,
                                           bool split) {
   const CacheAttnShape* shapes = kCacheAttnShapes[D == 64 ? 0 : D == 128 ? 1 : 2];
-  if (B * T * Hq > 1 << 22) split = false;                   // the card is full of rows
+  if (B * T * Hq > 1 << 22) split = false;                   // (the join, too, has fewer than 2^32 threads)
   const int64_t rows = T * (Hq / Hkv), blocks = (max_len + kCacheBlock - 1) / kCacheBlock;
   CacheAttnPlan best{};
   double best_cost = 1e300;
   for (int c = 0; c < kCacheShapes; ++c) {
     const CacheAttnShape& s = shapes[c];
+    if (c > 0 && s.rows > shapes[c - 1].rows && rows <= shapes[c - 1].rows) break;   // a smaller tile holds them all
     const bool few = s.rows <= 32;
     const int64_t step = few ? s.waves : 1;                  // blocks of an iteration
     const int64_t tiles = (rows + s.rows - 1) / s.rows, units = B * Hkv * tiles;
     const int64_t slots = few && s.waves == 4 && s.rows == 16 ? 2 * kCacheCUs : kCacheCUs;
     int64_t most = split ? (blocks + step - 1) / step : 1;
     if (most > 64) most = 64;
+    if (most > (1 << 20) / units) most = (1 << 20) / units;     // more rows than that fill the card by themselves
     if (most < 1) most = 1;
     int64_t parts = split && few ? (blocks + 15) / 32 : 1;
     if (parts > most) parts = most;
