@@ -49,10 +49,16 @@ def plans(tmp_path_factory):
 
 
 def test_the_gpu_tests_meet_every_tile(plans):
-    for (D, rows, waves, parts), (B, T, Hq, Hkv, L, ws) in SHAPES.items():
+    for (D, rows, waves, parts, several), (B, T, Hq, Hkv, L, ws) in SHAPES.items():
         p, = plans([(B, T, Hq, Hkv, D, L, ws)])
         assert (p["rows"], p["waves"], p["parts"] > 1) == (rows, waves, parts), ((D, rows, waves, parts), p)
-    assert set(SHAPES) == {(D, r, w, p) for D, t in TILES.items() for r, w in t for p in (False, True)}
+        assert several is None or (p["tiles"] > 1) == several, ((D, rows, waves, parts), p)
+    # the kernels for few rows read keys in two ways, by whether a sequence has one row tile
+    for D, tiles in TILES.items():
+        for rows, waves in tiles:
+            for several in (False, True) if rows <= 32 else (None,):
+                assert any(k[:3] == (D, rows, waves) and k[4] == several for k in SHAPES)
+            assert {k[3] for k in SHAPES if k[:3] == (D, rows, waves)} == {False, True}
 
 
 def test_plans_cover_the_rows_and_fit_a_launch(plans):

@@ -10,20 +10,49 @@ import test_cache_ops_gpu as R  # noqa: E402  (values of a cache, tolerance)
 
 DEV = "cuda"
 
-# (D, rows of a workgroup, its waves, in parts): B, T, Hq, Hkv, max_len, with workspace
+# (D, rows of a workgroup, its waves, in parts, several row tiles of a sequence (None: any)):
+# B, T, Hq, Hkv, max_len, with workspace
 SHAPES = {
-    (64, 16, 4, False): (17, 5, 32, 8, 41, True), (64, 16, 4, True): (11, 1, 12, 4, 2707, True),
-    (64, 16, 8, False): (1, 3, 5, 1, 150, False), (64, 16, 8, True): (1, 2, 7, 1, 2056, True),
-    (64, 32, 8, False): (6, 184, 4, 1, 268, False), (64, 32, 8, True): (1, 176, 4, 1, 2747, True),
-    (64, 256, 8, False): (4, 600, 4, 2, 330, False), (64, 256, 8, True): (1, 1062, 8, 4, 675, True),
-    (128, 16, 4, False): (17, 6, 24, 8, 33, True), (128, 16, 4, True): (17, 1, 4, 4, 1655, True),
-    (128, 16, 8, False): (1, 4, 4, 1, 700, False), (128, 16, 8, True): (1, 1, 9, 1, 1562, True),
-    (128, 32, 8, False): (6, 228, 3, 1, 260, False), (128, 32, 8, True): (2, 62, 8, 1, 2068, True),
-    (128, 256, 8, False): (6, 400, 4, 2, 300, False), (128, 256, 8, True): (3, 318, 9, 3, 595, True),
-    (256, 16, 4, False): (52, 1, 10, 5, 60, False), (256, 16, 4, True): (13, 9, 8, 1, 1555, True),
-    (256, 16, 8, False): (1, 2, 3, 1, 200, False), (256, 16, 8, True): (1, 1, 4, 1, 537, True),
-    (256, 32, 4, False): (1, 10, 2, 1, 130, False), (256, 32, 4, True): (5, 63, 5, 1, 1053, True),
-    (256, 128, 4, False): (1, 50, 5, 1, 70, False), (256, 128, 4, True): (1, 7, 5, 1, 555, True),
+    (128, 16, 4, False, False): (257, 1, 1, 1, 33, True),
+    (128, 16, 4, False, True): (1, 523, 8, 1, 66, True),
+    (128, 16, 4, True, False): (13, 1, 10, 5, 1557, True),
+    (128, 16, 8, False, False): (1, 4, 4, 1, 700, False),
+    (128, 16, 8, False, True): (1, 23, 1, 1, 32, True),
+    (128, 16, 8, True, False): (1, 1, 9, 1, 1562, True),
+    (128, 16, 8, True, True): (1, 18, 1, 1, 1639, True),
+    (128, 256, 8, False, None): (6, 400, 4, 2, 300, False),
+    (128, 256, 8, True, None): (5, 404, 4, 4, 577, True),
+    (128, 32, 8, False, False): (44, 6, 12, 3, 257, True),
+    (128, 32, 8, False, True): (1, 1447, 3, 3, 264, False),
+    (128, 32, 8, True, False): (13, 4, 5, 1, 4642, True),
+    (128, 32, 8, True, True): (1, 181, 4, 1, 2603, True),
+    (256, 128, 4, False, None): (1, 50, 5, 1, 70, False),
+    (256, 128, 4, True, None): (1, 7, 5, 1, 555, True),
+    (256, 16, 4, False, False): (129, 1, 6, 2, 32, False),
+    (256, 16, 4, False, True): (10, 162, 5, 1, 141, True),
+    (256, 16, 4, True, False): (22, 1, 4, 4, 1026, True),
+    (256, 16, 4, True, True): (1, 116, 6, 3, 2652, True),
+    (256, 16, 8, False, False): (1, 2, 3, 1, 200, False),
+    (256, 16, 8, False, True): (1, 10, 2, 1, 266, False),
+    (256, 16, 8, True, False): (1, 1, 4, 1, 537, True),
+    (256, 16, 8, True, True): (1, 9, 2, 1, 582, True),
+    (256, 32, 4, False, False): (1, 10, 2, 1, 32, True),
+    (256, 32, 4, False, True): (1, 33, 1, 1, 135, False),
+    (256, 32, 4, True, False): (9, 4, 25, 5, 1038, True),
+    (256, 32, 4, True, True): (1, 183, 8, 1, 1122, True),
+    (64, 16, 4, False, False): (129, 1, 2, 2, 32, True),
+    (64, 16, 4, False, True): (33, 6, 12, 4, 32, True),
+    (64, 16, 4, True, False): (22, 1, 2, 2, 2683, True),
+    (64, 16, 8, False, False): (1, 3, 5, 1, 150, False),
+    (64, 16, 8, False, True): (1, 6, 4, 1, 33, True),
+    (64, 16, 8, True, False): (1, 2, 7, 1, 2056, True),
+    (64, 16, 8, True, True): (1, 5, 4, 1, 2259, True),
+    (64, 256, 8, False, None): (4, 600, 4, 2, 330, False),
+    (64, 256, 8, True, None): (1, 1365, 6, 3, 654, True),
+    (64, 32, 8, False, False): (44, 7, 9, 3, 269, False),
+    (64, 32, 8, False, True): (1, 1029, 4, 1, 269, True),
+    (64, 32, 8, True, False): (4, 4, 15, 3, 5122, True),
+    (64, 32, 8, True, True): (1, 228, 2, 1, 4160, True),
 }
 
 
@@ -59,7 +88,7 @@ def _reference(q, c, table, lens, causal, scale, max_len):
 
 
 def _case(key, page, seed):
-    D, _, _, _ = key
+    D = key[0]
     B, T, Hq, Hkv, L, ws = SHAPES[key]
     from w4a4_post_quantized_channel_amd import ops
     pages = -(-L // page)
@@ -92,7 +121,8 @@ def test_tile(key, causal, page):
     assert torch.equal(out, ops.cache_attention(q, c, table, lens, causal=causal, max_len=L, workspace=ws))
 
 
-@pytest.mark.parametrize("key", [(128, 16, 4, True), (128, 32, 8, True), (128, 256, 8, True), (256, 128, 4, True)],
+@pytest.mark.parametrize("key", [(128, 16, 4, True, False), (128, 16, 8, True, True), (128, 32, 8, True, True), (128, 256, 8, True, None),
+                                 (256, 128, 4, True, None)],
                          ids=lambda k: "-".join(map(str, k)))
 def test_a_later_maximum(key):
     """Scores that climb by far more than the running maximum may lag, key after key, and fall again."""

@@ -64,7 +64,9 @@ struct Words {
   static constexpr int N = BYTES < 4 ? 1 : BYTES / 4;
   uint32_t w[N];
 };
-template <int BYTES>
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+// ONCE: no other workgroup reads them, and they leave the caches first.
+template <int BYTES, bool ONCE = false>
 __device__ __forceinline__ Words<BYTES> load_words(const uint8_t* p) {
   Words<BYTES> r;
   if constexpr (BYTES == 1) r.w[0] = *p;
@@ -76,7 +78,8 @@ __device__ __forceinline__ Words<BYTES> load_words(const uint8_t* p) {
   } else {
 #pragma unroll
     for (int i = 0; i < BYTES / 16; ++i) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      const u4* a = reinterpret_cast<const u4*>(p) + i;
+      const u4 v = ONCE ? __builtin_nontemporal_load(a) : *a;
       r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
     }
   }
@@ -127,9 +130,10 @@ __device__ __forceinline__ float row_factor(float amax, float& inverse) {
   return __uint_as_float((uint32_t)(267 - e) << 23);
 }
 
-template <int D_, int MT_, int NW_>
+template <int D_, int MT_, int NW_, bool ONCE_>
 struct Few {
   static constexpr int D = D_, MT = MT_, NW = NW_, R = 16 * MT;
+  static constexpr bool ONCE = ONCE_;           // one row tile: every key is read by one workgroup
   static constexpr int KS = D / 32;             // steps of the first product
   static constexpr int DT = D / 16;             // channel tiles, scales of a row
   static constexpr int CB = D / 8;              // bytes of codes a lane takes of a key
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
     for (int t = 0; t < 4; ++t) {
       const int64_t pt = __builtin_amdgcn_readlane(pg, 16 * t);
       const int tok = (blk * BN + 16 * t) & (page - 1);
-      kw[t] = load_words<C::CB>(kc + (pt * c.k_codes_sp + tok * (D / 2)));
+      kw[t] = load_words<C::CB, C::ONCE>(kc + (pt * c.k_codes_sp + tok * (D / 2)));
       ksw[t] = load_words<C::CB / 8>(ks + (pt * c.k_scales_sp + tok * DT));
     }
   };
@@ -210,7 +214,7 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int64_t pt = __builtin_amdgcn_readlane(pg, 16 * t);
-      vw[t] = load_words<C::CB>(vc + (pt * c.v_codes_sp + ((blk * BN + 16 * t) & (page - 1)) * (D / 2)));
+      vw[t] = load_words<C::CB, C::ONCE>(vc + (pt * c.v_codes_sp + ((blk * BN + 16 * t) & (page - 1)) * (D / 2)));
     }
     vsw = load_words<DT>(vs + (pg * c.v_scales_sp + ((blk * BN + 16 * lg) & (page - 1)) * DT));
   };
@@ -909,10 +913,11 @@ __global__ void __launch_bounds__(256) cache_join_kernel(Args p) {
   *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
 }
 
-template <typename C>
+template <int D, int MT, int NW>
 void launch_few(const Args& p, hipStream_t st) {
   const unsigned grid = (unsigned)(p.a.B * p.c.Hkv * p.tiles.d * p.parts.d);
-  attn_few_kernel<C><<<grid, 64 * C::NW, 0, st>>>(p);
+  if (p.tiles.d == 1) attn_few_kernel<Few<D, MT, NW, true>><<<grid, 64 * NW, 0, st>>>(p);
+  else attn_few_kernel<Few<D, MT, NW, false>><<<grid, 64 * NW, 0, st>>>(p);
 }
 
 template <typename C>
@@ -948,16 +953,16 @@ hipError_t launch_cache_attention(const w4a4_kvcache& c, const w4a4_cache_attn& 
   }
   const bool four = pl.waves == 4;
   if (c.D == 64) {
-    if (pl.rows == 16) four ? launch_few<Few<64, 1, 4>>(p, st) : launch_few<Few<64, 1, 8>>(p, st);
-    else if (pl.rows == 32) launch_few<Few<64, 2, 8>>(p, st);
+    if (pl.rows == 16) four ? launch_few<64, 1, 4>(p, st) : launch_few<64, 1, 8>(p, st);
+    else if (pl.rows == 32) launch_few<64, 2, 8>(p, st);
     else launch_many<Many<64, 8, 1>>(p, st);
   } else if (c.D == 128) {
-    if (pl.rows == 16) four ? launch_few<Few<128, 1, 4>>(p, st) : launch_few<Few<128, 1, 8>>(p, st);
-    else if (pl.rows == 32) launch_few<Few<128, 2, 8>>(p, st);
+    if (pl.rows == 16) four ? launch_few<128, 1, 4>(p, st) : launch_few<128, 1, 8>(p, st);
+    else if (pl.rows == 32) launch_few<128, 2, 8>(p, st);
     else launch_many<Many<128, 8, 1>>(p, st);
   } else {
-    if (pl.rows == 16) four ? launch_few<Few<256, 1, 4>>(p, st) : launch_few<Few<256, 1, 8>>(p, st);
-    else if (pl.rows == 32) launch_few<Few<256, 2, 4>>(p, st);
+    if (pl.rows == 16) four ? launch_few<256, 1, 4>(p, st) : launch_few<256, 1, 8>(p, st);
+    else if (pl.rows == 32) launch_few<256, 2, 4>(p, st);
     else launch_many<Many<256, 4, 1>>(p, st);
   }
   hipError_t e = hipGetLastError();

@@ -33,15 +33,15 @@ constexpr int kCacheCUs = 256;
 // 256; 200 queries of 8 heads over 8192 keys: 25 with 32 rows, 33 with 256; 500
 // queries of 8 heads over one of width 256, 4096 keys: 79 with 32, 86 with 16,
 // 57 with 128): iterations, start and end of a workgroup, and the join's launch,
-// parts and bytes.  A part of the kernels for few rows is about 32 blocks at
-// most, so that a batch of unequal histories fills the card to its end (64
-// sequences of 4096 to 8192 keys, 32 heads over 8: 104 us in four parts, 116 in
-// one).
+// parts and bytes; never less than reading the caches.  A batch of unequal histories gains nothing from more parts
+// (64 sequences of 4096 to 8192 keys, 32 heads over 8: 85 us in one part, 89 in
+// two, 92 in three, each with its caches cold).
 inline CacheAttnPlan plan_cache_attention(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len,
                                           bool split) {
   const CacheAttnShape* shapes = kCacheAttnShapes[D == 64 ? 0 : D == 128 ? 1 : 2];
   if (B * T * Hq > 1 << 22) split = false;                   // (the join, too, has fewer than 2^32 threads)
   const int64_t rows = T * (Hq / Hkv), blocks = (max_len + kCacheBlock - 1) / kCacheBlock;
+  const double read = (double)B * Hkv * blocks * kCacheBlock * D * 1.125 / 5.3e6;   // the caches' bytes, once
   CacheAttnPlan best{};
   double best_cost = 1e300;
   for (int c = 0; c < kCacheShapes; ++c) {
@@ -55,13 +55,11 @@ inline CacheAttnPlan plan_cache_attention(int64_t B, int64_t T, int64_t Hq, int6
     if (most > 64) most = 64;
     if (most > (1 << 20) / units) most = (1 << 20) / units;     // more rows than that fill the card by themselves
     if (most < 1) most = 1;
-    int64_t parts = split && few ? (blocks + 15) / 32 : 1;
-    if (parts > most) parts = most;
-    if (parts < 1) parts = 1;
-    for (;; parts = parts * 2 < most ? parts * 2 : most) {
+    for (int64_t parts = 1;; parts = parts * 2 < most ? parts * 2 : most) {
       const int64_t per = blocks < 1 ? 1 : (blocks + parts - 1) / parts;
       const int64_t iters = (per + step - 1) / step, rounds = (units * parts + slots - 1) / slots;
-      double cost = rounds * (iters * s.us + 6.0);
+      const double work = rounds * iters * s.us;
+      double cost = (work > read ? work : read) + rounds * 6.0;
       if (parts > 1) cost += 4.0 + 0.1 * parts + (double)parts * B * Hkv * rows * D * 8.0 / 4e6;
       if (cost < best_cost) {
         best_cost = cost;
