@@ -1,6 +1,8 @@
 """Every tile of the attention over the 4-bit cache, with and without parts, at
 the ends of what it covers: ragged histories, absent pages, rows that see
 nothing, strides.  References in 64 bits on the GPU."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -66,9 +68,9 @@ def _reference(q, c, table, lens, causal, scale, max_len):
     out = torch.zeros(B, T, Hq, D, dtype=torch.float64, device=DEV)
     A, smax = torch.zeros_like(out), torch.zeros(B, T, Hq, 1, dtype=torch.float64, device=DEV)
     for b in range(B):
-        n = max(0, min(int(lens[b]), table.shape[1] * page, max_len))
-        j = torch.arange(n, device=DEV)
-        pg = table[b, j // page] if n else j.int()
+        n = max(0, int(lens[b]))
+        j = torch.arange(min(n, table.shape[1] * page, max_len), device=DEV)
+        pg = table[b, j // page] if len(j) else j.int()
         held = (pg >= 0) & (pg < c.n_pages)
         j, pg = j[held], pg[held].long()
         if not len(j):
@@ -151,3 +153,35 @@ def test_long_histories(L, T):
     for w in (ws, None):
         out = ops.cache_attention(q, c, table, lens, causal=True, max_len=L, workspace=w)
         R._assert_attention(out, _reference(q, c, table, lens, True, D ** -0.5, L), L, 6 * 2.0 ** 6 * c.v_scale)
+
+
+@pytest.mark.parametrize("T", [1, 17, 150])
+def test_a_peak_leaves_the_rest_its_weight(T):
+    """One key ahead of 2^19 - 1 of 2^-22.7 of its weight, which together make 8 percent: two and a half of fp16's
+    smallest steps each, were the peak's probability 1."""
+    from w4a4_post_quantized_channel_amd import ops
+    L, D, page = 2 ** 19, 128, 256
+    c = R._cache(ops, 7, L // page, page, 1, D, 1.0, 1.0)
+    for t, byte in ((c.k_codes, 0), (c.k_scales, 0x38), (c.v_codes, 0x22), (c.v_scales, 0x38)):
+        t.fill_(byte)
+    c.k_codes[0, 0, 0], c.v_codes[0, 0, 0] = 0x22, 0                     # key 0: ones, its value zeros; the others: the reverse
+    table = torch.arange(L // page, dtype=torch.int32, device=DEV).view(1, -1)
+    lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+    q = torch.ones(1, T, 2, D, dtype=torch.bfloat16, device=DEV)
+    scale = (24.0 - math.log2(2.5)) * math.log(2.0) / D
+    ref = _reference(q, c, table, lens, False, scale, L)
+    for w in (ops.make_cache_attention_workspace(1, T, 2, 1, D, L, device=DEV), None):
+        R._assert_attention(ops.cache_attention(q, c, table, lens, scale=scale, workspace=w), ref, L, 1.0)
+
+
+@pytest.mark.parametrize("T,D", [(4, 128), (40, 128), (300, 128), (150, 256)])
+def test_sequences_longer_than_their_cache(T, D):
+    """lens beyond max_len or the table: causal rows keep their positions, keys that do not exist are not seen."""
+    from w4a4_post_quantized_channel_amd import ops
+    c = R._cache(ops, 8, 60, 16, 2, D, 2.0 ** -9, 2.0 ** -9)
+    table = torch.randperm(60, generator=torch.Generator().manual_seed(1)).view(3, 20).int().to(DEV)
+    lens = torch.tensor([320 + T // 2, 2 ** 31 - 1, 301 + T // 3], dtype=torch.int32, device=DEV)
+    q = R._rand(9, 3, T, 4, D).to(torch.bfloat16).to(DEV)
+    for L in (320, 300, 4000):
+        out = ops.cache_attention(q, c, table, lens, causal=True, max_len=L)
+        R._assert_attention(out, _reference(q, c, table, lens, True, D ** -0.5, L), 320, 6 * 2.0 ** 6 * c.v_scale)

@@ -3,10 +3,12 @@
 // Mathematics.  The rows of a sequence and KV head are its queries (row = t G
 // + g, G query heads per KV head).  Keys come in blocks of 64; a row keeps its
 // running maximum m (in units of exp2), its sum l and its output o in fp32:
-//   p = exp2(c s - m),  l += sum p,  o += p V,   c = scale log2 e * k_scale.
+//   p = 2^b exp2(c s - m),  l += sum p,  o += p V,   c = scale log2 e * k_scale.
 // m only moves when a score exceeds it by more than kLazy: until then p is at
-// most 2^kLazy, which costs no accuracy (p and l scale alike), and o and l
-// need no rescaling.
+// most 2^(b + kLazy), which costs no accuracy (p and l scale alike), and o and l
+// need no rescaling.  b (kFewUp, kManyUp) puts p into the upper part of fp16's
+// range, so that what a long history's small probabilities lose below 2^-14 is
+// 2^-25 against a sum of at least 2^b.
 //
 // Types.  A cached value code * e (E2M1 times E4M3, at most six significant
 // bits, 2^-10 to 2880) is exact in fp16, so both products run on fp16 matrix
@@ -14,7 +16,7 @@
 // and v_scale enter c and the last division.  A query row is multiplied by the
 // power of two that puts its largest channel at 2^13: bf16's eight bits then
 // fit fp16 for every channel down to 2^-27 of the largest.  Probabilities are
-// rounded to fp16 (2^-12 of them, a sixteenth of the output's own rounding).
+// rounded to fp16 (off by 2^-11 of them, an eighth of the output's own rounding).
 //
 // A wave works alone on every NW-th block of its workgroup's part, for
 // 16 MT rows at once:
@@ -43,7 +45,7 @@ typedef int v2i __attribute__((ext_vector_type(2)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) v2i lds_v2i;
 
-constexpr float kLazy = 8.f;
+constexpr float kLazy = 8.f, kFewUp = 7.f;   // p < 2^15
 constexpr int BN = kCacheBlock;
 
 struct Args {
@@ -146,9 +148,15 @@ struct Few {
 };
 
 // Keys a query row sees: those below its limit.
-__device__ __forceinline__ int row_limit(const Args& p, int len, int t) {
-  return p.a.causal ? len - (int)p.a.T + t + 1 : len;
-}
+struct Limit {
+  int len, reach, back;      // keys of the sequence; keys there can be; T if causal
+  __device__ __forceinline__ Limit(const Args& p, int b) {
+    len = max(p.a.lens[b], 0);
+    reach = (int)min(p.a.max_len, p.a.table_pages << p.lp);
+    back = p.a.causal ? (int)p.a.T : 0;
+  }
+  __device__ __forceinline__ int operator()(int t) const { return min(back ? len - back + t + 1 : len, reach); }
+};
 
 template <typename C>
 __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 ? 2 : 1) attn_few_kernel(Args p) {
@@ -169,10 +177,9 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
 
   const int r0 = tile * R, nrows = min(R, p.rows - r0);
   int rem;
-  const int64_t reach = min(a.max_len, a.table_pages << p.lp);
-  const int len = (int)max((int64_t)0, min((int64_t)a.lens[b], reach));
-  const int first = row_limit(p, len, div_by(r0, p.g, rem));            // the tile's lowest limit
-  const int last = row_limit(p, len, div_by(r0 + nrows - 1, p.g, rem));   // and highest
+  const Limit limit(p, b);
+  const int first = limit(div_by(r0, p.g, rem));            // the tile's lowest limit
+  const int last = limit(div_by(r0 + nrows - 1, p.g, rem));   // and highest
   const int nblk = (max(last, 0) + BN - 1) / BN;
   const int per = (nblk + (int)p.parts.d - 1) / (int)p.parts.d;
   const int lo = min(part * per, nblk), hi = min(lo + per, nblk);
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
     const int row = r0 + min(x * 16 + lr, nrows - 1);    // rows past the end repeat the last
     int g;
     const int t = div_by(row, p.g, g);
-    lim[x] = row_limit(p, len, t);
+    lim[x] = limit(t);
     const uint16_t* q = (const uint16_t*)a.q + b * a.q_sb + t * a.q_st + (int64_t)(hk * G + g) * a.q_sh + lg * (D / 4);
     float f[KS][8], amax = 0.f;
 #pragma unroll
@@ -350,7 +357,7 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[x][d] *= f;
       }
-      const float nm = m[x] == -INFINITY ? 0.f : -m[x];
+      const float nm = m[x] == -INFINITY ? 0.f : kFewUp - m[x];
       uint32_t w[8];
       float l0 = 0.f, l1 = 0.f;
 #pragma unroll
@@ -459,15 +466,15 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
 // other buffers.
 //
 // Maximum.  Probabilities are taken with the m at hand.  Only where a lane's
-// sum of a block passes kMost (or there is no m yet) the maximum is looked for
-// and the block's probabilities are taken again; p is at most kMost, l at
-// least 1 then.
+// sum of half a block passes kMost (or there is no m yet) the maximum is looked
+// for and the probabilities are taken again; p is at most kMost, l at least
+// 2^kManyUp then.
 // ---------------------------------------------------------------------------
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef __attribute__((address_space(3))) v4i lds_v4i;
 
-constexpr float kMost = 1024.f;
+constexpr float kMost = 32768.f, kManyUp = 5.f;
 
 template <int D_, int W_, int NS_>
 struct Many {
@@ -525,10 +532,9 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
 
   const int r0 = tile * R, nrows = min(R, p.rows - r0);
   int rem;
-  const int64_t reach = min(a.max_len, a.table_pages << p.lp);
-  const int len = (int)max((int64_t)0, min((int64_t)a.lens[b], reach));
-  const int last = row_limit(p, len, div_by(r0 + nrows - 1, p.g, rem));
-  const int first = row_limit(p, len, div_by(r0 + min(wave * 32 * NS, nrows - 1), p.g, rem));   // of this wave
+  const Limit limit(p, b);
+  const int last = limit(div_by(r0 + nrows - 1, p.g, rem));
+  const int first = limit(div_by(r0 + min(wave * 32 * NS, nrows - 1), p.g, rem));   // of this wave
   const int nblk = (max(last, 0) + BN - 1) / BN;
   const int per = (nblk + (int)p.parts.d - 1) / (int)p.parts.d;
   const int lo = min(part * per, nblk), n = min(lo + per, nblk) - lo;
@@ -617,7 +623,7 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
     const int row = r0 + min((wave * NS + x) * 32 + lr, nrows - 1);   // rows past the end repeat the last
     int g;
     const int t = div_by(row, p.g, g);
-    lim[x] = row_limit(p, len, t);
+    lim[x] = limit(t);
     const uint16_t* q = (const uint16_t*)a.q + b * a.q_sb + t * a.q_st + (int64_t)(hk * G + g) * a.q_sh + h * 8;
     uint4 v[KC];
     float amax = 0.f;
@@ -715,7 +721,7 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
     float nm[NS];
 #pragma unroll
     for (int x = 0; x < NS; ++x) {
-      nm[x] = m[x] == -INFINITY ? 0.f : -m[x];
+      nm[x] = m[x] == -INFINITY ? 0.f : kManyUp - m[x];
       lb[x] = 0.f;
     }
 #pragma unroll
@@ -752,7 +758,7 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
           for (int e = 0; e < 16; ++e) o[x][d][e] *= f;
         lb[x] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) prob(s, x, w, mn == -INFINITY ? 0.f : -mn);
+        for (int w = 0; w < 8; ++w) prob(s, x, w, mn == -INFINITY ? 0.f : kManyUp - mn);
       }
     }
 #pragma unroll
