@@ -602,8 +602,9 @@ int w4a4_cache_read(const w4a4_kvcache* c, const int32_t* slots, int64_t M, void
  *            a dimension of one are not used.  Pointers 16-byte aligned.  out
  *            overlaps no input.
  *  table     device int32 [B, table_pages], row stride table_sb.
- *  lens      device int32[B], clamped to [0, min(max_len, table_pages * page)].
+ *  lens      device int32[B], a negative one counts as 0.
  *  max_len   an upper bound of lens that the host knows; it sizes the work.
+ *            Keys from min(max_len, table_pages * page) on do not exist.
  * Shape rules: Hq a multiple of Hkv, Hq <= 65536; B, T <= 2^24,
  * B T Hq <= 2^30, B Hkv ceil(T (Hq / Hkv) / 16) <= 2^22; max_len,
  * table_pages * page <= 2^30. */
@@ -641,8 +642,9 @@ size_t w4a4_cache_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t 
  *            W4A4_PAIRS_HALVES: channels i and i + sum(sections).
  *  table     device fp32 [sum(sections)][2]: f_i / (2 pi) as the sum of two
  *            fp32 numbers, so that far positions keep their angle: angles are
- *            reduced to a turn in twice 24 bits, products are fp32, one
- *            rounding to the dtype.
+ *            reduced to a turn in twice 24 bits (off by 2^-25 of a turn up to
+ *            positions of 2^24, by 2^-23 up to int32 ones of 2^26), products
+ *            are fp32, one rounding to the dtype.
  * Shape rules: D even, 2 <= D <= 1024; M < 2^31; Hq + Hk <= 65536; Hq >= 1. */
 enum { W4A4_PAIRS_ADJACENT = 0, W4A4_PAIRS_HALVES = 1 };
 typedef struct w4a4_rotary {
@@ -679,8 +681,8 @@ int w4a4_rotary_axes(const w4a4_rotary* r, void* stream);
  *  gate, scale, shift      fp32 [R, C], row strides, or NULL (1, 0, 0).
  *  post_weight, weight, bias  fp32[C] or NULL (no norm of h; 1; 0).
  * All arithmetic in fp32, one rounding per output; outputs overlap no input
- * but x_out = x.  Shape rules: 1 <= C <= 16384; M < 2^31; M a multiple of R;
- * eps >= 0. */
+ * but x_out = x.  Shape rules: 1 <= C <= 16384; M < 2^31; M a multiple of R
+ * (R may be 0 where M is); eps >= 0. */
 enum { W4A4_NORM_LAYER = 0, W4A4_NORM_RMS = 1 };
 typedef struct w4a4_gated {
   int64_t M, C, R;

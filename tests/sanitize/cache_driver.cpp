@@ -291,6 +291,8 @@ int main() {
     g.M = 0;
     g.x = nullptr;
     if (w4a4_gated_norm(&g, nullptr) != 0 || g_launches != before) ++failures;
+    g.R = 0;
+    if (w4a4_gated_norm(&g, nullptr) != 0 || g_launches != before) ++failures;
     expect("gated: NULL", w4a4_gated_norm(nullptr, nullptr), -1, before);
   }
   std::printf("ok: %d failures\n", failures);

@@ -180,3 +180,13 @@ def test_rotary_table_keeps_48_bits(ops):
         ops.make_rotary_table([2, 2], freqs=freqs, device="cpu")
     with pytest.raises(ValueError):
         ops.make_rotary_table([1] * 5, device="cpu")
+
+
+@needs_library
+def test_what_a_call_was_packed_from_is_fixed(ops):
+    c = _calls(ops)["cache_append"]["cache"]
+    t = ops.make_rotary_table([3, 2], device="cpu")
+    for x, names in ((c, "k_codes v_scales k_scale D page n_pages"), (t, "sections turns")):
+        for name in names.split():
+            with pytest.raises(AttributeError, match=name):
+                setattr(x, name, getattr(x, name))

@@ -199,9 +199,9 @@ def _attention_reference(q, c, table, lens, causal, scale, max_len=None):
     out = torch.zeros(B, T, Hq, D, dtype=torch.float64)
     A, smax = torch.zeros_like(out), torch.zeros(B, T, Hq, 1, dtype=torch.float64)
     for b in range(B):
-        n = max(0, min(int(lens[b]), reach if max_len is None else min(reach, max_len)))
-        j = torch.arange(n)
-        pg = table[b, j // page] if n else torch.zeros(0, dtype=torch.int32)
+        n = max(0, int(lens[b]))
+        j = torch.arange(min(n, reach if max_len is None else min(reach, max_len)))
+        pg = table[b, j // page] if len(j) else torch.zeros(0, dtype=torch.int32)
         held = (pg >= 0) & (pg < c.n_pages)
         j, pg = j[held], pg[held].long()
         k, v = kv[pg, :, j % page] * gk, vv[pg, :, j % page] * gv          # [n, Hkv, D]
@@ -220,14 +220,13 @@ def _attention_reference(q, c, table, lens, causal, scale, max_len=None):
 
 def _assert_attention(got, ref, n, vmax):
     """The output's rounding to bf16 is 2^-8 of it.  A probability enters the second product as fp16, off by
-    2^-11 of it (below 2^-14, by 2^-25, against a sum of at least 1; it is at most 2^8 where the running maximum
-    lags); a score is a sum of D products in 24 bits, D / 2 * 2^-24 of sum |q k| at most in any order of
+    2^-11 of it (below 2^-14, by 2^-25, against a sum of at least 2^5); a score is a sum of D products in 24 bits, D / 2 * 2^-24 of sum |q k| at most in any order of
     pairs of partial sums, plus exp2's argument and result (2^-22 of smax, 2^-22).  An error d of a score moves
     the output by 2 d A.  Sums of n probabilities and products in 24 bits: n 2^-24 A, twice."""
     out, A, smax = ref
     D = out.shape[-1]
     d = (D / 2 * 2.0 ** -24 + 2.0 ** -22) * smax + 2.0 ** -22
-    tol = 2.0 ** -8 * out.abs() + (2.0 ** -11 + 2 * d + n * 2.0 ** -23) * A * 1.01 + n * 2.0 ** -25 * vmax
+    tol = 2.0 ** -8 * out.abs() + (2.0 ** -11 + 2 * d + n * 2.0 ** -23) * A * 1.01 + n * 2.0 ** -30 * vmax
     err = (got.double().cpu() - out).abs()
     worst = (err - tol).max()
     assert bool((err <= tol).all()), f"over by {float(worst):.3g} at {int((err - tol).argmax())}"
@@ -420,6 +419,22 @@ def test_attention_of_nothing(ops):
     ops.cache_append(c, torch.ones(0, 2, 64, device=DEV), torch.ones(0, 2, 64, device=DEV), empty)
 
 
+def test_norms_and_positions_of_nothing(ops):
+    x = torch.ones(0, 40, dtype=BF, device=DEV)
+    mod = torch.ones(0, 40, device=DEV)                # a modulation a row
+    for m in (mod, torch.ones(3, 40, device=DEV), None):
+        xo, y = ops.gated_norm(x, x, gate=m, scale=m, shift=m)
+        assert xo.shape == y.shape == (0, 40)
+    q = torch.ones(0, 2, 64, dtype=BF, device=DEV)
+    out = ops.rotary_axes(q, q, torch.ones(0, 1, dtype=torch.int32, device=DEV), ops.make_rotary_table([32], device=DEV))
+    assert out[0].shape == out[1].shape == (0, 2, 64)
+    q = torch.ones(3, 2, 64, dtype=BF, device=DEV)
+    none = torch.ones(3, 0, 64, dtype=BF, device=DEV)  # no key heads
+    pos = torch.ones(3, 1, dtype=torch.int32, device=DEV)
+    assert torch.equal(ops.rotary_axes(q, none, pos, ops.make_rotary_table([32], device=DEV))[0],
+                       ops.rotary_axes(q, None, pos, ops.make_rotary_table([32], device=DEV))[0])
+
+
 # ----------------------------------------------------------------------------
 # Rotary positions
 # ----------------------------------------------------------------------------
@@ -440,6 +455,9 @@ ROTARY = [  # M, Hq, Hk, D, sections, interleaved, dtype, far
     (1500, 2, 2, 256, [44, 42, 42], True, BF, 0),
     (5, 1, 1, 1024, [512], True, BF, 0),
     (1, 32, 8, 128, [64], True, BF, 12345),
+    (31, 3, 1, 128, [64], False, F32, 2 ** 25 + 1),
+    (31, 3, 1, 128, [20, 20, 24], True, F32, -2 ** 26),
+    (31, 3, 1, 50, [25], True, F32, 2 ** 26 - 61),
 ]
 
 
@@ -462,9 +480,12 @@ def _rotary_reference(x, pos, sections, interleaved):
 
 def _assert_rotary(got, x, pos, sections, interleaved):
     """The angle is off by 2^-25 of a turn at most (2^-22.3), sine and cosine by 2^-23, three roundings in 24 bits:
-    under 2^-21 of |u| + |w|; then the output's own rounding.  Channels behind the pairs are copied."""
+    under 2^-21 of |u| + |w|; then the output's own rounding.  Channels behind the pairs are copied.
+    int32 positions from 2^24 to 2^26: the table's 2^-52 of a turn times 2^26, and roundings of angles up to 1 and
+    up to 1.5 turns, 2^-25 and 2^-24, are 7 2^-26 of a turn, with the rest under 2^-20."""
     want, size = _rotary_reference(x, pos, sections, interleaved)
-    tol = torch.finfo(x.dtype).eps / 2 * want.abs() + 2.0 ** -21 * size
+    far = pos.numel() and pos.double().abs().max() > 2 ** 24
+    tol = torch.finfo(x.dtype).eps / 2 * want.abs() + (2.0 ** -20 if far else 2.0 ** -21) * size
     err = (got.double().cpu() - want).abs()
     assert bool((err <= tol).all()), float((err - tol).max())
     assert torch.equal(got[..., 2 * sum(sections):], x[..., 2 * sum(sections):])
@@ -476,7 +497,7 @@ def test_rotary(ops, i, how):
     M, Hq, Hk, D, sections, inter, dtype, far = ROTARY[i]
     g = torch.Generator().manual_seed(i)
     pos = torch.randint(0, 60, (M, len(sections)), generator=g) + far
-    pos = pos.int() if i % 2 == 0 else pos.float() + 0.25 * (abs(far) < 1000)
+    pos = pos.int() if i % 2 == 0 or abs(far) > 2 ** 24 else pos.float() + 0.25 * (abs(far) < 1000)
     odd = 8 if how != "views" else 3                   # views: strides that are no multiple of anything
     big = _rand(400 + i, M, Hq + Hk + 1, D + odd).to(dtype).to(DEV)
     q, k = big[:, :Hq, :D], big[:, Hq:Hq + Hk, :D]

@@ -273,9 +273,9 @@ int w4a4_gated_norm(const w4a4_gated* desc, void* stream) {
   const char* fn = "w4a4_gated_norm";
   if (!desc) return fail(W4A4_ERR_INVALID_ARG, "%s: NULL descriptor", fn);
   w4a4_gated g = *desc;
-  if (g.M < 0 || g.C <= 0 || g.R <= 0) return fail(W4A4_ERR_INVALID_ARG, "%s: bad sizes", fn);
+  if (g.M < 0 || g.C <= 0 || g.R < (g.M > 0)) return fail(W4A4_ERR_INVALID_ARG, "%s: bad sizes", fn);
   if (g.C > 16384 || g.M > INT32_MAX) return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: sizes too large", fn);
-  if (g.M % g.R != 0)
+  if (g.R > 0 && g.M % g.R != 0)
     return fail(W4A4_ERR_UNSUPPORTED_SHAPE, "%s: %lld rows over %lld rows of modulations", fn, (long long)g.M,
                 (long long)g.R);
   int st = check_float(fn, "x", g.x_dtype);

@@ -4,7 +4,8 @@
 // f / (2 pi) as hi + lo, so the angle in turns is pos * hi + pos * lo; the
 // rounding error of the first product is recovered by an fma, whole turns are
 // dropped exactly, and what remains is below half a turn in 24 bits: the sine
-// of position 10^6 is as good as that of position 1.
+// of position 10^6 is as good as that of position 1.  An int32 position enters
+// as fp32 and what that rounds off.
 //
 // A thread takes eight channels (16 bytes of bf16) of one token, or eight pairs
 // where the halves of a head pair up, computes their sines once and applies them
@@ -22,10 +23,14 @@ namespace {
 
 typedef float v8f __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ void sincos_of(float pos, float hi, float lo, float& c, float& s) {
-  const float p = pos * hi;
-  const float e = __builtin_fmaf(pos, hi, -p);              // exact
-  const float turn = (p - __builtin_rintf(p)) + __builtin_fmaf(pos, lo, e);
+// A position: what fp32 holds of it, and the rest of an int32.
+struct Pos {
+  float x, rest;
+};
+__device__ __forceinline__ void sincos_of(const Pos& pos, float hi, float lo, float& c, float& s) {
+  const float p = pos.x * hi;
+  const float e = __builtin_fmaf(pos.x, hi, -p);            // exact
+  const float turn = (p - __builtin_rintf(p)) + __builtin_fmaf(pos.rest, hi, __builtin_fmaf(pos.x, lo, e));
   sincospif(2.f * turn, &s, &c);
 }
 
@@ -64,9 +69,12 @@ struct RotaryArgs {
   Divisor by;         // items
 };
 
-__device__ __forceinline__ float position(const w4a4_rotary& a, int64_t m, int axis) {
+__device__ __forceinline__ Pos position(const w4a4_rotary& a, int64_t m, int axis) {
   const int64_t i = m * a.pos_sm + axis;
-  return a.pos_dtype == W4A4_DT_I32 ? (float)((const int32_t*)a.pos)[i] : ((const float*)a.pos)[i];
+  if (a.pos_dtype != W4A4_DT_I32) return {((const float*)a.pos)[i], 0.f};
+  const int n = ((const int32_t*)a.pos)[i];
+  const float x = fminf((float)n, 2147483520.f);             // (the largest fp32 number that is an int32)
+  return {x, (float)(n - (int)x)};
 }
 // Token and item of element i.
 __device__ __forceinline__ int64_t token_of(const RotaryArgs& p, int64_t i, bool small, int& it) {

@@ -644,7 +644,17 @@ def _stream_for(t, stream) -> int:
     return _stream(stream)
 
 
-class KVCache:
+class _Fixed:
+    """Attributes that a call's arguments were packed from are set once: a change would not reach the calls."""
+    _packed = None
+
+    def __setattr__(self, name, value):
+        if self._packed is not None:
+            raise AttributeError(f"a {type(self).__name__} is fixed: make a new one to change {name}")
+        object.__setattr__(self, name, value)
+
+
+class KVCache(_Fixed):
     """A paged cache of keys and values in NVFP4 (see w4a4_kvcache in include/w4a4.h).
 
     k_codes, v_codes uint8 [n_pages, Hkv, page, D / 2]; k_scales, v_scales uint8
@@ -675,7 +685,7 @@ class KVCache:
             strides.append(t.stride(0) if n > 1 else H * page * width)
         _together("k_scales v_codes v_scales", k_codes, k_scales, v_codes, v_scales)
         at = [t.data_ptr() if t.is_cuda else 0 for t in (k_codes, k_scales, v_codes, v_scales)]
-        self._desc = _KVCACHE.pack(n, page, H, 2 * half, self.k_scale, self.v_scale, at[0], strides[0], at[1], strides[1],
+        self._packed = _KVCACHE.pack(n, page, H, 2 * half, self.k_scale, self.v_scale, at[0], strides[0], at[1], strides[1],
                                    at[2], strides[2], at[3], strides[3])
 
 
@@ -713,7 +723,7 @@ def cache_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.
     km, kh, _ = _cache_rows("k", k, shape, k.dtype)
     vm, vh, _ = _cache_rows("v", v, shape, k.dtype)
     kp = _together("v slots cache", k, v, slots, cache)
-    st = LIB.w4a4_cache_append(cache._desc, kp, km, kh, v.data_ptr(), vm, vh, _dtype_code(k), M, slots.data_ptr(),
+    st = LIB.w4a4_cache_append(cache._packed, kp, km, kh, v.data_ptr(), vm, vh, _dtype_code(k), M, slots.data_ptr(),
                                _stream_for(k, stream))
     if st != 0:
         _check("w4a4_cache_append", st)
@@ -731,7 +741,7 @@ def cache_read(cache: KVCache, slots: torch.Tensor, *, k: Optional[torch.Tensor]
     km, kh, _ = _cache_rows("k", k, shape, k.dtype)
     vm, vh, _ = _cache_rows("v", v, shape, k.dtype)
     kp = _together("v slots cache", k, v, slots, cache)
-    st = LIB.w4a4_cache_read(cache._desc, slots.data_ptr(), M, kp, km, kh, v.data_ptr(), vm, vh, _dtype_code(k),
+    st = LIB.w4a4_cache_read(cache._packed, slots.data_ptr(), M, kp, km, kh, v.data_ptr(), vm, vh, _dtype_code(k),
                              _stream_for(k, stream))
     if st != 0:
         _check("w4a4_cache_read", st)
@@ -775,13 +785,13 @@ def cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     desc = _CACHE_ATTN.pack(B, T, Hq, pages * cache.page if max_len is None else max_len,
                             D ** -0.5 if scale is None else scale, causal, qp, qb, qt, qh, table.data_ptr(),
                             table.stride(0), pages, lens.data_ptr(), out.data_ptr(), ob, ot, oh)
-    st = LIB.w4a4_cache_attention(cache._desc, desc, *_ws_args(workspace), _stream_for(q, stream))
+    st = LIB.w4a4_cache_attention(cache._packed, desc, *_ws_args(workspace), _stream_for(q, stream))
     if st != 0:
         _check("w4a4_cache_attention", st)
     return out
 
 
-class RotaryTable:
+class RotaryTable(_Fixed):
     """Frequencies of rotary_axes: ``sections`` pairs of each axis, ``turns`` fp32 [pairs, 2] (see make_rotary_table)."""
 
     def __init__(self, sections, turns: torch.Tensor):
