@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
 
   // pages of a block's four groups of 16 keys, one a lane group; -1: absent.
   // Neither this load nor those of a block is ever left out, so that waits can
-  // count the younger ones: past the end they read entry 0 and page 0.
+  // count the younger ones: past the end they read entry 0, and all lanes the
+  // first bytes of page 0 (one request instead of one a line).
   auto load_pages = [&](int blk) {
     const int j = blk * BN + 16 * lg;
     const bool in = blk < hi && j < last;
@@ -199,31 +200,36 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
   Words<C::CB / 8> ksw[4];
   Words<DT> vsw;
   uint32_t bad = 0;                 // groups whose page is absent
-  const uint8_t* kc = (const uint8_t*)c.k_codes + (int64_t)hk * page * (D / 2) + lr * (D / 2) + lg * C::CB;
-  const uint8_t* ks = (const uint8_t*)c.k_scales + (int64_t)hk * page * DT + lr * DT + lg * (DT / 4);
-  const uint8_t* vc = (const uint8_t*)c.v_codes + (int64_t)hk * page * (D / 2) + lane * C::CB;
-  const uint8_t* vs = (const uint8_t*)c.v_scales + (int64_t)hk * page * DT + lr * DT;
+  const uint8_t* kc = (const uint8_t*)c.k_codes + (int64_t)hk * page * (D / 2);
+  const uint8_t* ks = (const uint8_t*)c.k_scales + (int64_t)hk * page * DT;
+  const uint8_t* vc = (const uint8_t*)c.v_codes + (int64_t)hk * page * (D / 2);
+  const uint8_t* vs = (const uint8_t*)c.v_scales + (int64_t)hk * page * DT;
+  const uint32_t kco = lr * (D / 2) + lg * C::CB, kso = lr * DT + lg * (DT / 4), vco = lane * C::CB;
   auto held = [&](int pg) { return pg >= 0 && pg < c.n_pages ? pg : 0; };   // an absent page: any, its keys are excluded
   auto load_k = [&](int blk, int pg) {
     const uint64_t x = __ballot(pg < 0 || pg >= c.n_pages);
     bad = (uint32_t)(x & 1) | (uint32_t)(x >> 15 & 2) | (uint32_t)(x >> 30 & 4) | (uint32_t)(x >> 45 & 8);
     pg = held(pg);
+    const bool in = blk < hi;
+    const uint32_t ko = in ? kco : 0, so = in ? kso : 0;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int64_t pt = __builtin_amdgcn_readlane(pg, 16 * t);
       const int tok = (blk * BN + 16 * t) & (page - 1);
-      kw[t] = load_words<C::CB, C::ONCE>(kc + (pt * c.k_codes_sp + tok * (D / 2)));
-      ksw[t] = load_words<C::CB / 8>(ks + (pt * c.k_scales_sp + tok * DT));
+      kw[t] = load_words<C::CB, C::ONCE>(kc + (pt * c.k_codes_sp + tok * (D / 2)) + ko);
+      ksw[t] = load_words<C::CB / 8>(ks + (pt * c.k_scales_sp + tok * DT) + so);
     }
   };
   auto load_v = [&](int blk, int pg) {
     pg = held(pg);
+    const bool in = blk < hi;
+    const uint32_t vo = in ? vco : 0, so = in ? (((blk * BN + 16 * lg) & (page - 1)) + lr) * DT : 0;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int64_t pt = __builtin_amdgcn_readlane(pg, 16 * t);
-      vw[t] = load_words<C::CB, C::ONCE>(vc + (pt * c.v_codes_sp + ((blk * BN + 16 * t) & (page - 1)) * (D / 2)));
+      vw[t] = load_words<C::CB, C::ONCE>(vc + (pt * c.v_codes_sp + ((blk * BN + 16 * t) & (page - 1)) * (D / 2)) + vo);
     }
-    vsw = load_words<DT>(vs + (pg * c.v_scales_sp + ((blk * BN + 16 * lg) & (page - 1)) * DT));
+    vsw = load_words<DT>(vs + (pg * c.v_scales_sp) + so);
   };
 
   int pg = load_pages(lo + wave), pg1 = load_pages(lo + wave + NW);
@@ -889,33 +895,68 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
   }
 }
 
-// Joins the parts of a row: D / 4 lanes a row, 16 bytes of each part a lane.
+// Joins the parts of a row: kJoin groups of D / 4 lanes a row take every kJoin-th
+// part, four in flight, 16 bytes of each a lane, and meet in LDS.
+constexpr int kJoin = 4;
 template <int D>
 __global__ void __launch_bounds__(256) cache_join_kernel(Args p) {
   const w4a4_cache_attn& a = p.a;
-  constexpr int LPR = D / 4;
-  const int64_t gr = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
-  const int d = threadIdx.x % LPR * 4;
-  const int64_t all = a.B * p.c.Hkv * p.rows;
-  if (gr >= all) return;
+  constexpr int LPR = D / 4, GROUPS = 256 / LPR, ROWS = GROUPS / kJoin;
+  __shared__ v4f accs[GROUPS][LPR];
+  __shared__ v2f mls[GROUPS];
+  const int group = threadIdx.x / LPR, x = threadIdx.x % LPR, first = group % kJoin;
+  const int64_t gr = (int64_t)blockIdx.x * ROWS + group / kJoin;
+  const int64_t all = a.B * p.c.Hkv * p.rows, at = min(gr, all - 1);
   const int parts = (int)p.parts.d;
   float M = -INFINITY, L = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < parts; ++k) M = fmaxf(M, p.pml[(k * all + gr) * 2]);
-  const float ms = M == -INFINITY ? 0.f : M;
   v4f acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int k = 0; k < parts; ++k) {
-    const v2f ml = *reinterpret_cast<const v2f*>(p.pml + (k * all + gr) * 2);
-    const float f = __builtin_amdgcn_exp2f(ml[0] - ms);
-    L += ml[1] * f;
-    acc += *reinterpret_cast<const v4f*>(p.po + (k * all + gr) * D + d) * f;
+  for (int k0 = first; k0 < parts; k0 += 4 * kJoin) {
+    v2f ml[4];
+    v4f o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t k = min(k0 + i * kJoin, parts - 1);
+      ml[i] = *reinterpret_cast<const v2f*>(p.pml + (k * all + at) * 2);
+      o[i] = *reinterpret_cast<const v4f*>(p.po + (k * all + at) * D + 4 * x);
+    }
+    float mn = M;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (k0 + i * kJoin >= parts) ml[i][0] = -INFINITY;      // (one that another group takes)
+      mn = fmaxf(mn, ml[i][0]);
+    }
+    const float ms = mn == -INFINITY ? 0.f : mn, f = __builtin_amdgcn_exp2f(M - ms);
+    M = mn;
+    L *= f;
+    acc *= f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (k0 + i * kJoin >= parts) break;
+      const float e = __builtin_amdgcn_exp2f(ml[i][0] - ms);
+      L += ml[i][1] * e;
+      acc += o[i] * e;
+    }
+  }
+  accs[group][x] = acc;
+  if (x == 0) mls[group] = (v2f){M, L};
+  __syncthreads();
+  if (first != 0 || gr >= all) return;
+#pragma unroll
+  for (int i = 1; i < kJoin; ++i) M = fmaxf(M, mls[group + i][0]);
+  const float ms = M == -INFINITY ? 0.f : M;
+  L = 0.f;
+  acc = (v4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kJoin; ++i) {
+    const float e = __builtin_amdgcn_exp2f(mls[group + i][0] - ms);
+    L += mls[group + i][1] * e;
+    acc += accs[group + i][x] * e;
   }
   const float inv = L == 0.f ? 0.f : p.c.v_scale / L;
   const int row = (int)(gr % p.rows), bh = (int)(gr / p.rows);
   int hk, g;
   const int b = div_by(bh, p.heads, hk), t = div_by(row, p.g, g);
-  uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * (int)p.g.d + g) * a.o_sh + d;
+  uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * (int)p.g.d + g) * a.o_sh + 4 * x;
   *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
 }
 
@@ -974,7 +1015,7 @@ hipError_t launch_cache_attention(const w4a4_kvcache& c, const w4a4_cache_attn& 
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.parts == 1) return e;
   const int64_t all = a.B * c.Hkv * (int64_t)p.rows;
-  const int per = 256 / ((int)c.D / 4);
+  const int per = 256 / ((int)c.D / 4) / kJoin;
   const unsigned grid = (unsigned)((all + per - 1) / per);
   if (c.D == 64) cache_join_kernel<64><<<grid, 256, 0, st>>>(p);
   else if (c.D == 128) cache_join_kernel<128><<<grid, 256, 0, st>>>(p);
