@@ -458,6 +458,8 @@ ROTARY = [  # M, Hq, Hk, D, sections, interleaved, dtype, far
     (31, 3, 1, 128, [64], False, F32, 2 ** 25 + 1),
     (31, 3, 1, 128, [20, 20, 24], True, F32, -2 ** 26),
     (31, 3, 1, 50, [25], True, F32, 2 ** 26 - 61),
+    (200, 9, 2, 64, [8, 8, 8], False, BF, 0),
+    (200, 9, 2, 64, [12, 9, 9], True, F32, 0),
 ]
 
 
@@ -557,6 +559,13 @@ GATED = [  # M, C, R, kind, h, post, gate, mod, affine, x, h dtype, y
     (9, 4104, 1, "layer", True, False, False, False, False, BF, BF, BF),
     (300, 127, 300, "rms", True, True, True, True, False, F32, BF, BF),
     (2100, 256, 3, "layer", True, False, True, True, False, BF, BF, BF),
+    # a row's last channels alone: at a wave's and a workgroup's end
+    (13, 505, 13, "layer", True, True, True, True, True, BF, F32, BF),
+    (13, 511, 1, "rms", True, True, True, True, True, F32, BF, F32),
+    (3000, 513, 5, "layer", True, True, True, True, True, BF, BF, BF),
+    (2, 8191, 1, "layer", True, True, True, True, True, BF, BF, BF),
+    (3, 8185, 3, "rms", True, False, True, True, True, F32, BF, BF),
+    (2, 16377, 2, "layer", True, True, True, True, True, BF, BF, BF),
 ]
 
 
