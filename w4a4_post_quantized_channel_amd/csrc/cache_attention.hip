@@ -32,6 +32,20 @@
 //    fp16, one row of 64 keys per 16 channels.
 // The waves' (m, l, o) are joined through LDS, the parts through the workspace
 // by a second kernel.
+//
+// What bounds it.  One token each of 64 sequences, 32 heads over 8 of 128, 4096
+// to 8192 keys: the caches' 463 MB at 5.4 TB/s, 85 us (a device copy reaches
+// 5.1).  There each key is read by one workgroup only, past the caches: 92 us
+// against 102 with ordinary loads (7% slower where the history fits the 256 MB
+// cache and is read again at once), and in one part: 85 against 89 in two and 92
+// in three.  A chunk of 8 x 50 queries, 16 heads over 4, 2090 keys (22 us): turns
+// of 7000 cycles in which two waves a SIMD convert codes (1150 cycles a block and
+// wave), multiply (1024) and take exponentials (600), one after the other for
+// each wave; 64 rows a wave convert half as often but leave one wave a SIMD: 34.
+// 2 x 13 queries, 8 heads over one of 256, 5131 keys (14.6 us and 3 of join): one
+// turn a wave; seven row tiles read the same keys through the L2s, 4 MB each.
+// One workgroup's call (1 query, 317 keys) takes 6 us: arguments, lens, table,
+// keys and the join wait for each other.
 #include "cache.h"
 #include "cache_attention_plan.h"
 #include "device_common.h"
@@ -475,6 +489,14 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
 // sum of half a block passes kMost (or there is no m yet) the maximum is looked
 // for and the probabilities are taken again; p is at most kMost, l at least
 // 2^kManyUp then.
+//
+// What bounds it.  A frame of 2 x 1560 queries, 16 heads of 128, 12480 keys: 319
+// GFLOP in 352 to 358 us, 0.9 PFLOP/s (a large library product: 1.4).  Of the
+// 352, products alone take 202, fragment reads add 27, softmax 75, conversions
+// 24, loads 16; matrix and vector units are each busy half the time, and 224 of
+// 256 CUs have a tile.  64 rows a wave and 4 waves: 393 to 403; two blocks a
+// barrier: 364.  One wave a SIMD (D = 256) where the queries and sums of 32 rows
+// take the registers of two.
 // ---------------------------------------------------------------------------
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
@@ -896,7 +918,9 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
 }
 
 // Joins the parts of a row: kJoin groups of D / 4 lanes a row take every kJoin-th
-// part, four in flight, 16 bytes of each a lane, and meet in LDS.
+// part, four in flight, 16 bytes of each a lane, and meet in LDS.  A launch and
+// two dependent loads: 2.8 us for 16 parts of 208 rows of 256 (one group a row:
+// 4.8).
 constexpr int kJoin = 4;
 template <int D>
 __global__ void __launch_bounds__(256) cache_join_kernel(Args p) {

@@ -10,6 +10,12 @@
 // head, so that tokens which follow each other in a page are written, and read,
 // in whole lines, while a token's head is D * 2 bytes side by side on the other
 // end.
+//
+// Bound by memory: 12480 tokens of 16 heads of 128, bf16 (102 MB and 29 MB of
+// cache), append in 23.4 us (5.6 TB/s, part of it from the last-level cache) and
+// read in 28.1 (4.7); a workgroup per token, all its heads, took 72 in all.  One
+// token of each of 64 sequences is a launch, the slot, the row and the
+// quotients: 3.5 us each.
 #include "cache.h"
 #include "device_common.h"
 #include "divisor.h"
