@@ -155,12 +155,15 @@ def test_an_operand_elsewhere_is_refused(ops, fn, name):
 @needs_library
 def test_another_device_than_the_current_one_is_refused(ops, monkeypatch):
     class There:
-        is_cuda, device = True, torch.device("cuda", 1)
+        device = torch.device("cuda", 1)
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(ops, "_current_device", lambda: 0)
     with pytest.raises(ValueError, match="current device"):
         ops._stream_for(There(), _NoStream())
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(ops, "_current_device", lambda: 1)
     assert ops._stream_for(There(), _NoStream()) == 0
 
 

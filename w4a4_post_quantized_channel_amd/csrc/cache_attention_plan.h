@@ -23,19 +23,22 @@ struct CacheAttnShape {
 };
 constexpr int kCacheShapes = 4;
 constexpr CacheAttnShape kCacheAttnShapes[3][kCacheShapes] = {
-    {{16, 4, 1.6}, {16, 8, 1.3}, {32, 8, 2.2}, {256, 8, 1.1}},      // D = 64 (estimates)
+    {{16, 4, 1.6}, {16, 8, 1.3}, {32, 8, 2.2}, {256, 8, 1.1}},      // D = 64
     {{16, 4, 2.6}, {16, 8, 2.0}, {32, 8, 3.4}, {256, 8, 1.85}},     // D = 128
     {{16, 4, 5.0}, {16, 8, 4.6}, {32, 4, 4.5}, {128, 4, 2.0}}};     // D = 256
 constexpr int kCacheCUs = 256;
 
-// Microseconds, fitted to measurements of D = 128 and 256 (a chunk of 8 x 50,
-// 16 heads over 4, 2090 keys: 24 with 32 rows a workgroup, 29 with 16, 33 with
-// 256; 200 queries of 8 heads over 8192 keys: 25 with 32 rows, 33 with 256; 500
-// queries of 8 heads over one of width 256, 4096 keys: 79 with 32, 86 with 16,
-// 57 with 128): iterations, start and end of a workgroup, and the join's launch,
-// parts and bytes; never less than reading the caches.  A batch of unequal histories gains nothing from more parts
-// (64 sequences of 4096 to 8192 keys, 32 heads over 8: 85 us in one part, 89 in
-// two, 92 in three, each with its caches cold).
+// Microseconds, fitted to measurements (width 128, a chunk of 8 x 50, 16 heads
+// over 4, 2090 keys: 24 with 32 rows a workgroup, 29 with 16, 33 with 256; width
+// 64: 17, 19 and 23; width 128, 200 queries of 8 heads over 8192 keys: 25 with 32
+// rows, 33 with 256; width 256, 500 queries of 8 heads over one, 4096 keys: 79
+// with 32, 86 with 16, 57 with 128): iterations, start and end of a workgroup,
+// and the join's launch, parts and bytes; never less than reading the caches.  A
+// batch of unequal histories gains nothing from more parts (64 sequences of 4096
+// to 8192 keys, 32 heads over 8: 85 us in one part, 89 in two, 92 in three, each
+// with its caches cold).  Of 20 other shapes the choice was the fastest of those
+// tried or within 10%, but for single tokens of width 64 over 8192 keys (66 with
+// four waves, 60 with eight).
 inline CacheAttnPlan plan_cache_attention(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len,
                                           bool split) {
   const CacheAttnShape* shapes = kCacheAttnShapes[D == 64 ? 0 : D == 128 ? 1 : 2];

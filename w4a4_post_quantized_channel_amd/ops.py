@@ -468,6 +468,13 @@ def _together(names: str, first: torch.Tensor, *others) -> int:
     device.  An operand in host memory would fault the kernel: if ``first`` lies
     there the address is NULL, which the library refuses after its checks of
     sizes."""
+    index = first.get_device()
+    if index >= 0:
+        for t in others:
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            return first.data_ptr()
     device = first.device
     for t in others:
         if t is not None and t.device != device:
@@ -629,15 +636,16 @@ def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
 # These check that their operands lie on the current device, whose stream they
 # take.
 # ---------------------------------------------------------------------------
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # (there is a CUDA tensor by then)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the handle alone, without a Stream object
 
 
 def _stream_for(t, stream) -> int:
     """The stream of a call on ``t``'s device, which has to be the current one."""
-    if t.is_cuda:
-        index = t.device.index
-        if index != torch.cuda.current_device():
-            raise ValueError(f"the operands are on {t.device}, the current device is cuda:{torch.cuda.current_device()}: "
+    index = t.get_device()                       # -1 in host memory
+    if index >= 0:
+        if index != _current_device():
+            raise ValueError(f"the operands are on {t.device}, the current device is cuda:{_current_device()}: "
                              f"call under torch.cuda.device({index})")
         if stream is None and _raw_stream is not None:
             return _raw_stream(index)
@@ -672,7 +680,7 @@ class KVCache(_Fixed):
         self.n_pages, self.Hkv, self.page, self.D = n, H, page, 2 * half
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
-        self.device = k_codes.device
+        self.device, self._index = k_codes.device, k_codes.get_device()
         strides = []
         for name, width in (("k_codes", half), ("k_scales", half // 8), ("v_codes", half), ("v_scales", half // 8)):
             t = getattr(self, name)
@@ -687,6 +695,9 @@ class KVCache(_Fixed):
         at = [t.data_ptr() if t.is_cuda else 0 for t in (k_codes, k_scales, v_codes, v_scales)]
         self._packed = _KVCACHE.pack(n, page, H, 2 * half, self.k_scale, self.v_scale, at[0], strides[0], at[1], strides[1],
                                    at[2], strides[2], at[3], strides[3])
+
+    def get_device(self) -> int:
+        return self._index
 
 
 def make_kv_cache(n_pages: int, page: int, Hkv: int, D: int, k_scale: float = 1.0, v_scale: float = 1.0,
