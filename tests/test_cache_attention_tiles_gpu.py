@@ -185,3 +185,31 @@ def test_sequences_longer_than_their_cache(T, D):
     for L in (320, 300, 4000):
         out = ops.cache_attention(q, c, table, lens, causal=True, max_len=L)
         R._assert_attention(out, _reference(q, c, table, lens, True, D ** -0.5, L), 320, 6 * 2.0 ** 6 * c.v_scale)
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_shapes_drawn_at_random(seed):
+    import random
+    from w4a4_post_quantized_channel_amd import ops
+    r = random.Random(900 + seed)
+    D, page, Hkv = r.choice([64, 128, 256]), r.choice([16, 32, 64, 128, 256]), r.choice([1, 1, 2, 3, 5])
+    Hq, B = Hkv * r.choice([1, 2, 3, 5, 8]), r.choice([1, 2, 3, 7, 20])
+    T, L = r.choice([1, 2, int(2 ** r.uniform(0, 9))]), int(2 ** r.uniform(0, 12.5))
+    if B * T * Hq * L > 2 ** 26:
+        B, T = 1, max(1, min(T, 2 ** 26 // (Hq * L)))
+    causal, split, scale = r.random() < 0.5, r.random() < 0.7, r.choice([D ** -0.5, D ** -0.5, 0.3, -0.1])
+    pages = -(-L // page) + r.choice([0, 0, 1])
+    c = R._cache(ops, seed, B * pages + 2, page, Hkv, D, 2.0 ** -9 * r.choice([1.0, 1.3]), 0.0021)
+    g = torch.Generator().manual_seed(seed)
+    table = torch.randint(0, B * pages + 2, (B, pages), generator=g).int()   # pages that several hold
+    table[torch.rand(B, pages, generator=g) < r.choice([0.0, 0.0, 0.3])] = -1
+    lens = torch.randint(0, L + 1, (B,), generator=g).int()
+    lens[r.randrange(B)] = L
+    q = R._rand(seed + 5, B, T, Hq + 1, D).to(torch.bfloat16).to(DEV)[:, :, :Hq]
+    out = torch.full((B, Hq, T + 1, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    into = out.transpose(1, 2)[:, :T]                                    # [B, Hq, T, D] in memory
+    ws = ops.make_cache_attention_workspace(B, T, Hq, Hkv, D, L, device=DEV) if split else None
+    table, lens = table.to(DEV), lens.to(DEV)
+    ops.cache_attention(q, c, table, lens, causal=causal, scale=scale, max_len=L, out=into, workspace=ws)
+    R._assert_attention(into, _reference(q, c, table, lens, causal, scale, L), L + page, 6 * 2.0 ** 6 * c.v_scale)
+    assert bool(torch.isnan(out[:, :, T].float()).all())
