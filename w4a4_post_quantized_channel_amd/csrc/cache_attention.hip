@@ -413,8 +413,8 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
     asm volatile("" ::: "memory");
   }
 
-  // Join the waves: each leaves its (m, l) and its o, scaled to the common
-  // maximum, in LDS, and all threads sum them.
+  // Join the waves: each leaves its (m, l) and its o in LDS, and all threads sum
+  // them, scaled to the common maximum.
   float* red = reinterpret_cast<float*>(smem);
   float* ml = red + NW * R * C::PITCH;
   __syncthreads();
@@ -425,17 +425,9 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
       ml[(wave * R + x * 16 + lr) * 2] = m[x];
       ml[(wave * R + x * 16 + lr) * 2 + 1] = l[x];
     }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int x = 0; x < MT; ++x) {
-    float mx = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < NW; ++k) mx = fmaxf(mx, ml[(k * R + x * 16 + lr) * 2]);
-    const float f = __builtin_amdgcn_exp2f(m[x] - (mx == -INFINITY ? 0.f : mx));
 #pragma unroll
     for (int d = 0; d < DT; ++d)
-      *reinterpret_cast<v4f*>(&red[(wave * R + x * 16 + lr) * C::PITCH + 16 * d + 4 * lg]) = o[x][d] * f;
+      *reinterpret_cast<v4f*>(&red[(wave * R + x * 16 + lr) * C::PITCH + 16 * d + 4 * lg]) = o[x][d];
   }
   __syncthreads();
   for (int e = tid; e < nrows * (D / 4); e += 64 * NW) {
@@ -447,8 +439,9 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
     v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
-      L += ml[(k * R + rr) * 2 + 1] * __builtin_amdgcn_exp2f(ml[(k * R + rr) * 2] - ms);
-      acc += *reinterpret_cast<const v4f*>(&red[(k * R + rr) * C::PITCH + d]);
+      const float f = __builtin_amdgcn_exp2f(ml[(k * R + rr) * 2] - ms);
+      L += ml[(k * R + rr) * 2 + 1] * f;
+      acc += *reinterpret_cast<const v4f*>(&red[(k * R + rr) * C::PITCH + d]) * f;
     }
     const int row = r0 + rr;
     if (p.po) {
