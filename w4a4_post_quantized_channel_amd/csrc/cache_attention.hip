@@ -189,6 +189,17 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
   const w4a4_cache_attn& a = p.a;
   const int G = (int)p.g.d, page = 1 << p.lp;
 
+  // Table entries of a block's four groups of 16 keys, one a lane group, whether
+  // held or not (without a table any integer).  Neither this load nor those of a
+  // block is ever left out, so that waits can count the younger ones: past the
+  // end all lanes read the first bytes of page 0 (one request instead of one a
+  // line).
+  const int entries = (int)a.table_pages;
+  const int32_t* table = entries > 0 ? a.table + b * a.table_sb : a.lens;
+  auto load_pages = [&](int blk) { return table[max(min((blk * BN + 16 * lg) >> p.lp, entries - 1), 0)]; };
+  int pg = 0, pg1 = 0;
+  if (part == 0) pg = load_pages(wave), pg1 = load_pages(wave + NW);   // while lens is on its way
+
   const int r0 = tile * R, nrows = min(R, p.rows - r0);
   int rem;
   const Limit limit(p, b);
@@ -197,19 +208,8 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
   const int nblk = (max(last, 0) + BN - 1) / BN;
   const int per = (nblk + (int)p.parts.d - 1) / (int)p.parts.d;
   const int lo = min(part * per, nblk), hi = min(lo + per, nblk);
-  // (without keys there may be no table: any integer then)
-  const int32_t* table = hi > lo ? a.table + b * a.table_sb : a.lens;
+  if (part != 0) pg = load_pages(lo + wave), pg1 = load_pages(lo + wave + NW);
 
-  // pages of a block's four groups of 16 keys, one a lane group; -1: absent.
-  // Neither this load nor those of a block is ever left out, so that waits can
-  // count the younger ones: past the end they read entry 0, and all lanes the
-  // first bytes of page 0 (one request instead of one a line).
-  auto load_pages = [&](int blk) {
-    const int j = blk * BN + 16 * lg;
-    const bool in = blk < hi && j < last;
-    const int pg = table[in ? j >> p.lp : 0];
-    return in ? pg : -1;
-  };
   Words<C::CB> kw[4], vw[4];        // a block's codes and scales: K by tiles of 16 keys
   Words<C::CB / 8> ksw[4];
   Words<DT> vsw;
@@ -219,11 +219,13 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
   const uint8_t* vc = (const uint8_t*)c.v_codes + (int64_t)hk * page * (D / 2);
   const uint8_t* vs = (const uint8_t*)c.v_scales + (int64_t)hk * page * DT;
   const uint32_t kco = lr * (D / 2) + lg * C::CB, kso = lr * DT + lg * (DT / 4), vco = lane * C::CB;
-  auto held = [&](int pg) { return pg >= 0 && pg < c.n_pages ? pg : 0; };   // an absent page: any, its keys are excluded
+  // an entry of a block; -1: the page is absent, or past the end (page 0 is read then, its keys are excluded)
+  const int end = min(last, hi * BN);
+  auto held = [&](int blk, int pg) { return blk * BN + 16 * lg < end && (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1; };
   auto load_k = [&](int blk, int pg) {
-    const uint64_t x = __ballot(pg < 0 || pg >= c.n_pages);
+    const uint64_t x = __ballot(pg < 0);
     bad = (uint32_t)(x & 1) | (uint32_t)(x >> 15 & 2) | (uint32_t)(x >> 30 & 4) | (uint32_t)(x >> 45 & 8);
-    pg = held(pg);
+    pg = max(pg, 0);
     const bool in = blk < hi;
     const uint32_t ko = in ? kco : 0, so = in ? kso : 0;
 #pragma unroll
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
     }
   };
   auto load_v = [&](int blk, int pg) {
-    pg = held(pg);
+    pg = max(pg, 0);
     const bool in = blk < hi;
     const uint32_t vo = in ? vco : 0, so = in ? (((blk * BN + 16 * lg) & (page - 1)) + lr) * DT : 0;
 #pragma unroll
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
     vsw = load_words<DT>(vs + (pg * c.v_scales_sp) + so);
   };
 
-  int pg = load_pages(lo + wave), pg1 = load_pages(lo + wave + NW);
+  pg = held(lo + wave, pg);
   // loads stay in this order, so that a wait for the older ones leaves the younger in flight
   auto in_order = [] {
     asm volatile("" ::: "memory");
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
   for (int blk = lo + wave; blk < hi; blk += NW) {
     const int j0 = blk * BN;
     const uint32_t absent = bad;
-    pg = pg1;
+    pg = held(blk + NW, pg1);
     pg1 = load_pages(blk + 2 * NW);
 
     // V into LDS: piece t holds keys 16 t .. 16 t + 15, CB bytes a lane
