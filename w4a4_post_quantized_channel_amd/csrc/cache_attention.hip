@@ -38,14 +38,15 @@
 // 5.1).  There each key is read by one workgroup only, past the caches: 92 us
 // against 102 with ordinary loads (7% slower where the history fits the 256 MB
 // cache and is read again at once), and in one part: 85 against 89 in two and 92
-// in three.  A chunk of 8 x 50 queries, 16 heads over 4, 2090 keys (22 us): turns
+// in three.  A chunk of 8 x 50 queries, 16 heads over 4, 2090 keys (21 us): turns
 // of 7000 cycles in which two waves a SIMD convert codes (1150 cycles a block and
 // wave), multiply (1024) and take exponentials (600), one after the other for
 // each wave; 64 rows a wave convert half as often but leave one wave a SIMD: 34.
-// 2 x 13 queries, 8 heads over one of 256, 5131 keys (14.6 us and 3 of join): one
+// 2 x 13 queries, 8 heads over one of 256, 5131 keys (14.2 us and 3 of join): one
 // turn a wave; seven row tiles read the same keys through the L2s, 4 MB each.
-// One workgroup's call (1 query, 317 keys) takes 6 us: arguments, lens, table,
-// keys and the join wait for each other.
+// One workgroup's call (1 query, 317 keys) takes 5.5 to 6 us: arguments, lens and
+// table, keys and the join wait for each other (the table waiting for lens: 0.3
+// more; a second barrier in the join: 0.3 more).
 #include "cache.h"
 #include "cache_attention_plan.h"
 #include "device_common.h"
