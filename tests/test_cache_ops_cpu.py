@@ -193,3 +193,13 @@ def test_what_a_call_was_packed_from_is_fixed(ops):
         for name in names.split():
             with pytest.raises(AttributeError, match=name):
                 setattr(x, name, getattr(x, name))
+
+
+@needs_library
+def test_a_copied_cache_is_packed_from_its_own_tensors(ops):
+    import copy
+    c = _calls(ops)["cache_append"]["cache"]
+    d = copy.deepcopy(c)
+    assert d.k_codes.data_ptr() != c.k_codes.data_ptr() and (d.k_scale, d.v_scale, d.page) == (c.k_scale, c.v_scale, c.page)
+    make, args = c.__reduce__()
+    assert make is ops.KVCache and all(a is getattr(c, n) for a, n in zip(args, ("k_codes", "k_scales", "v_codes", "v_scales")))

@@ -701,3 +701,20 @@ def test_gated_norm_and_rotary_in_a_graph(ops):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want[n]) and torch.equal(pos, pos_before)
+
+
+def test_copies_of_a_cache(ops):
+    import copy
+    import io
+    c = _cache(ops, 40, 4, 16, 2, 64)
+    slots = torch.arange(40, dtype=torch.int32, device=DEV)
+    want = [t.clone() for t in ops.cache_read(c, slots)]
+    buf = io.BytesIO()
+    torch.save(c, buf)
+    buf.seek(0)
+    same, own, loaded = copy.copy(c), copy.deepcopy(c), torch.load(buf, weights_only=False)   # (written two lines above)
+    c.k_codes.zero_()
+    for d, shared in ((same, True), (own, False), (loaded, False)):
+        k, v = ops.cache_read(d, slots)
+        assert torch.equal(v, want[1]) and torch.equal(k, torch.zeros_like(k) if shared else want[0])
+        assert (d.k_codes.data_ptr() == c.k_codes.data_ptr()) == shared

@@ -696,6 +696,9 @@ class KVCache(_Fixed):
         self._packed = _KVCACHE.pack(n, page, H, 2 * half, self.k_scale, self.v_scale, at[0], strides[0], at[1], strides[1],
                                    at[2], strides[2], at[3], strides[3])
 
+    def __reduce__(self):                        # a copy is packed from its own tensors
+        return KVCache, (self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.k_scale, self.v_scale)
+
     def get_device(self) -> int:
         return self._index
 
