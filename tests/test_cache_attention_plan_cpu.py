@@ -28,7 +28,7 @@ int main() {
 }
 """
 TILES = {64: [(16, 4), (16, 8), (32, 8), (256, 8)], 128: [(16, 4), (16, 8), (32, 8), (256, 8)],
-         256: [(16, 4), (16, 8), (32, 4), (128, 4)]}
+         256: [(16, 4), (16, 8), (128, 4)]}
 
 
 @pytest.fixture(scope="module")

@@ -18,8 +18,9 @@ SHAPES = {
     (128, 16, 4, False, False): (257, 1, 1, 1, 33, True),
     (128, 16, 4, False, True): (1, 523, 8, 1, 66, True),
     (128, 16, 4, True, False): (13, 1, 10, 5, 1557, True),
+    (128, 16, 4, True, True): (11, 17, 3, 3, 1767, True),
     (128, 16, 8, False, False): (1, 4, 4, 1, 700, False),
-    (128, 16, 8, False, True): (1, 23, 1, 1, 32, True),
+    (128, 16, 8, False, True): (1, 8, 3, 1, 257, False),
     (128, 16, 8, True, False): (1, 1, 9, 1, 1562, True),
     (128, 16, 8, True, True): (1, 18, 1, 1, 1639, True),
     (128, 256, 8, False, None): (6, 400, 4, 2, 300, False),
@@ -28,27 +29,24 @@ SHAPES = {
     (128, 32, 8, False, True): (1, 1447, 3, 3, 264, False),
     (128, 32, 8, True, False): (13, 4, 5, 1, 4642, True),
     (128, 32, 8, True, True): (1, 181, 4, 1, 2603, True),
-    (256, 128, 4, False, None): (1, 50, 5, 1, 70, False),
-    (256, 128, 4, True, None): (1, 7, 5, 1, 555, True),
+    (256, 128, 4, False, None): (1, 347, 25, 5, 32, False),
+    (256, 128, 4, True, None): (4, 724, 3, 1, 580, True),
     (256, 16, 4, False, False): (129, 1, 6, 2, 32, False),
     (256, 16, 4, False, True): (10, 162, 5, 1, 141, True),
     (256, 16, 4, True, False): (22, 1, 4, 4, 1026, True),
     (256, 16, 4, True, True): (1, 116, 6, 3, 2652, True),
-    (256, 16, 8, False, False): (1, 2, 3, 1, 200, False),
+    (256, 16, 8, False, False): (1, 1, 2, 1, 257, False),
     (256, 16, 8, False, True): (1, 10, 2, 1, 266, False),
-    (256, 16, 8, True, False): (1, 1, 4, 1, 537, True),
-    (256, 16, 8, True, True): (1, 9, 2, 1, 582, True),
-    (256, 32, 4, False, False): (1, 10, 2, 1, 32, True),
-    (256, 32, 4, False, True): (1, 33, 1, 1, 135, False),
-    (256, 32, 4, True, False): (9, 4, 25, 5, 1038, True),
-    (256, 32, 4, True, True): (1, 183, 8, 1, 1122, True),
+    (256, 16, 8, True, False): (1, 1, 2, 1, 10569, True),
+    (256, 16, 8, True, True): (1, 3, 8, 1, 10055, True),
     (64, 16, 4, False, False): (129, 1, 2, 2, 32, True),
     (64, 16, 4, False, True): (33, 6, 12, 4, 32, True),
     (64, 16, 4, True, False): (22, 1, 2, 2, 2683, True),
-    (64, 16, 8, False, False): (1, 3, 5, 1, 150, False),
-    (64, 16, 8, False, True): (1, 6, 4, 1, 33, True),
-    (64, 16, 8, True, False): (1, 2, 7, 1, 2056, True),
-    (64, 16, 8, True, True): (1, 5, 4, 1, 2259, True),
+    (64, 16, 4, True, True): (1, 5, 5, 1, 1068, True),
+    (64, 16, 8, False, False): (1, 1, 1, 1, 258, True),
+    (64, 16, 8, False, True): (1, 9, 2, 1, 272, False),
+    (64, 16, 8, True, False): (1, 1, 1, 1, 5009, True),
+    (64, 16, 8, True, True): (1, 17, 1, 1, 4919, True),
     (64, 256, 8, False, None): (4, 600, 4, 2, 330, False),
     (64, 256, 8, True, None): (1, 1365, 6, 3, 654, True),
     (64, 32, 8, False, False): (44, 7, 9, 3, 269, False),

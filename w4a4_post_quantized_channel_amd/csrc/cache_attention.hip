@@ -1029,7 +1029,6 @@ hipError_t launch_cache_attention(const w4a4_kvcache& c, const w4a4_cache_attn& 
     else launch_many<Many<128, 8, 1>>(p, st);
   } else {
     if (pl.rows == 16) four ? launch_few<256, 1, 4>(p, st) : launch_few<256, 1, 8>(p, st);
-    else if (pl.rows == 32) launch_few<256, 2, 4>(p, st);
     else launch_many<Many<256, 4, 1>>(p, st);
   }
   hipError_t e = hipGetLastError();
