@@ -462,16 +462,14 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: a workgroup of four waves, NS sets of 32 rows each, shares every
-// block of keys, converted to fp16 once and kept in LDS.
+// Many rows: a workgroup of W waves (eight; four at D = 256) of 32 rows each
+// shares every block of keys, converted to fp16 once and kept in LDS.
 //
 // Products.  S^T = K Q^T and O^T = V^T P^T with v_mfma_f32_32x32x16_f16: a lane
 // has one query (lane % 32) and of 32 keys the scores of keys 8 (i / 4) +
 // 4 (lane / 32) + i % 4.  The second product takes its 16 keys per step in that
 // order, V^T comes from LDS through the transposing read (4 keys x 16 channels
-// per 16 lanes), and P never moves between lanes.  A fragment read from LDS
-// feeds NS products: with 32 rows a wave, reading fragments would take as long
-// as multiplying them.
+// per 16 lanes), and P never moves between lanes.
 //
 // A wave overlaps its own work as far as it can.  Keys go by halves of a
 // block: phase 1 of half u multiplies half u + 1 by the queries while it turns
@@ -500,9 +498,10 @@ typedef __attribute__((address_space(3))) v4i lds_v4i;
 
 constexpr float kMost = 32768.f, kManyUp = 5.f;
 
-template <int D_, int W_, int NS_>
+template <int D_, int W_>
 struct Many {
-  static constexpr int D = D_, W = W_, NS = NS_, R = W * 32 * NS;
+  static constexpr int D = D_, W = W_;
+  static constexpr int NS = 1, R = W * 32 * NS;         // sets of 32 rows of a wave (two sets: see above)
   static constexpr int RB = 2 * D, MAT = BN * RB;       // bytes of a row, of a block of K or V
   static constexpr int KC = D / 16, DB = D / 32;        // steps, channel blocks
   static constexpr int MATS = 8 / W;                    // W = 8: waves 0-3 convert K, 4-7 V; W = 4: each both
@@ -1022,14 +1021,14 @@ hipError_t launch_cache_attention(const w4a4_kvcache& c, const w4a4_cache_attn& 
   if (c.D == 64) {
     if (pl.rows == 16) four ? launch_few<64, 1, 4>(p, st) : launch_few<64, 1, 8>(p, st);
     else if (pl.rows == 32) launch_few<64, 2, 8>(p, st);
-    else launch_many<Many<64, 8, 1>>(p, st);
+    else launch_many<Many<64, 8>>(p, st);
   } else if (c.D == 128) {
     if (pl.rows == 16) four ? launch_few<128, 1, 4>(p, st) : launch_few<128, 1, 8>(p, st);
     else if (pl.rows == 32) launch_few<128, 2, 8>(p, st);
-    else launch_many<Many<128, 8, 1>>(p, st);
+    else launch_many<Many<128, 8>>(p, st);
   } else {
     if (pl.rows == 16) four ? launch_few<256, 1, 4>(p, st) : launch_few<256, 1, 8>(p, st);
-    else launch_many<Many<256, 4, 1>>(p, st);
+    else launch_many<Many<256, 4>>(p, st);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.parts == 1) return e;
