@@ -634,7 +634,9 @@ def group_norm_act(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] 
 # Operators around a 4-bit key/value cache
 #
 # These check that their operands lie on the current device, whose stream they
-# take.
+# take.  With ``stream`` (a torch.cuda.Stream) the outputs that a call makes come
+# from that stream's memory; the caller orders it with the streams that wrote the
+# operands and that read the outputs.
 # ---------------------------------------------------------------------------
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # (there is a CUDA tensor by then)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the handle alone, without a Stream object
@@ -650,6 +652,17 @@ def _stream_for(t, stream) -> int:
         if stream is None and _raw_stream is not None:
             return _raw_stream(index)
     return _stream(stream)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output of a call on ``stream``, from that stream's memory: work that other streams have queued may still
+    use what they freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):        # (something with a handle alone)
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class _Fixed:
@@ -749,9 +762,9 @@ def cache_read(cache: KVCache, slots: torch.Tensor, *, k: Optional[torch.Tensor]
     M = _check_slots(slots)
     shape = (M, cache.Hkv, cache.D)
     if k is None:
-        k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=slots.device)
+        k = _empty(shape, dtype if v is None else v.dtype, slots.device, stream)
     if v is None:
-        v = torch.empty(shape, dtype=k.dtype, device=slots.device)
+        v = _empty(shape, k.dtype, slots.device, stream)
     km, kh, _ = _cache_rows("k", k, shape, k.dtype)
     vm, vh, _ = _cache_rows("v", v, shape, k.dtype)
     kp = _together("v slots cache", k, v, slots, cache)
@@ -786,7 +799,7 @@ def cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     if D != cache.D:
         raise ValueError(f"q has head width {D}, the cache {cache.D}")
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, T, Hq, D), torch.bfloat16, q.device, stream)
     qb, qt, qh, _ = _attn_operand("q", q, (B, T, Hq, D))
     ob, ot, oh, _ = _attn_operand("out", out, (B, T, Hq, D))
     if table.dtype is not torch.int32 or table.dim() != 2 or table.shape[0] != B or (
@@ -842,7 +855,7 @@ def rotary_axes(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, t
     shape, dtype = q.shape, q.dtype
     M, Hq, D = shape
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+        q_out = _empty(shape, dtype, q.device, stream)
     qm, qh, _ = _cache_rows("q", q, shape, dtype)
     qom, qoh, _ = _cache_rows("q_out", q_out, shape, dtype)
     Hk = kp = km = kh = kop = kom = koh = 0
@@ -850,7 +863,7 @@ def rotary_axes(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, t
         Hk = k.shape[1]
         kshape = (M, Hk, D)
         if k_out is None:
-            k_out = torch.empty(kshape, dtype=dtype, device=q.device)
+            k_out = _empty(kshape, dtype, q.device, stream)
         km, kh, _ = _cache_rows("k", k, kshape, dtype)
         kom, koh, _ = _cache_rows("k_out", k_out, kshape, dtype)
         kp, kop = k.data_ptr(), k_out.data_ptr()
@@ -916,9 +929,9 @@ def gated_norm(x: torch.Tensor, h: Optional[torch.Tensor] = None, *, gate: Optio
     shape = x.shape
     M, C, ldx = _matrix("x", x)
     if x_out is None and h is not None:
-        x_out = torch.empty((M, C), dtype=x.dtype, device=x.device)
+        x_out = _empty((M, C), x.dtype, x.device, stream)
     if y is None and norm:
-        y = torch.empty((M, C), dtype=y_dtype, device=x.device)
+        y = _empty((M, C), y_dtype, x.device, stream)
     hp = ldh = xop = ldxo = yp = ldy = 0
     if h is not None:
         hp, ldh = _like("h", h, shape)
