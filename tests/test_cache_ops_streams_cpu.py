@@ -63,3 +63,22 @@ def test_outputs_are_made_on_the_stream_of_the_call(ops, fn):
     with pytest.raises(ops.W4A4Error, match="NULL"):
         getattr(ops, fn)(**kw, stream=side)
     assert len(ops.made) == n and all(s is side for s in ops.made)
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    from w4a4_post_quantized_channel_amd import ops
+
+    class There:
+        device = torch.device("cuda", 1)
+
+        def get_device(self):
+            return 1
+
+    class On(_Side):
+        def __init__(self, index):
+            self.device_index = index
+
+    monkeypatch.setattr(ops, "_current_device", lambda: 1)
+    assert ops._stream_for(There(), On(1)) == 0
+    with pytest.raises(ValueError, match="stream"):
+        ops._stream_for(There(), On(0))

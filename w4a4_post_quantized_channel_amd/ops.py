@@ -649,8 +649,11 @@ def _stream_for(t, stream) -> int:
         if index != _current_device():
             raise ValueError(f"the operands are on {t.device}, the current device is cuda:{_current_device()}: "
                              f"call under torch.cuda.device({index})")
-        if stream is None and _raw_stream is not None:
-            return _raw_stream(index)
+        if stream is None:
+            if _raw_stream is not None:
+                return _raw_stream(index)
+        elif getattr(stream, "device_index", index) != index:    # it would read this device's addresses on its own
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the operands are on {t.device}")
     return _stream(stream)
 
 
