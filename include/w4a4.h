@@ -623,7 +623,9 @@ typedef struct w4a4_cache_attn {
 int w4a4_cache_attention(const w4a4_kvcache* c, const w4a4_cache_attn* a, void* workspace, size_t workspace_bytes,
                          void* stream);
 
-/* Bytes of workspace w4a4_cache_attention uses for these sizes (0: none). */
+/* Bytes of workspace w4a4_cache_attention uses for these sizes and max_len or
+ * any smaller one, so that a program keeps one workspace for its longest
+ * history (0: none).  Without a workspace a call does not split its keys. */
 size_t w4a4_cache_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len);
 
 /* w4a4_rotary_axes -- rotary positions with one to four axes (time, height

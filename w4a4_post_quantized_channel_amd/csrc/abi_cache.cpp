@@ -7,6 +7,7 @@
 #include "../../include/w4a4.h"
 #include "abi_util.h"
 #include "cache.h"
+#include "cache_attention_plan.h"
 
 using w4a4::aligned;
 using w4a4::fail;
@@ -211,7 +212,14 @@ int w4a4_cache_attention(const w4a4_kvcache* c, const w4a4_cache_attn* desc, voi
 size_t w4a4_cache_attention_workspace(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len) {
   if (check_attn_sizes("w4a4_cache_attention_workspace", B, T, Hq, Hkv, D, max_len) != W4A4_OK || B == 0 || T == 0)
     return 0;
-  return w4a4::cache_attention_workspace(B, T, Hq, Hkv, D, max_len);
+  // A shorter history can need more: its keys go into more parts.
+  size_t most = 0;
+  const int64_t blocks = w4a4::plan_blocks(max_len);
+  for (int64_t n = 1; n <= blocks; n += w4a4::plan_step(n)) {
+    const size_t need = w4a4::cache_attention_workspace(B, T, Hq, Hkv, D, n * w4a4::kCacheBlock);
+    if (need > most) most = need;
+  }
+  return most;
 }
 
 int w4a4_rotary_axes(const w4a4_rotary* desc, void* stream) {

@@ -14,6 +14,19 @@ struct CacheAttnPlan {
 
 constexpr int kCacheBlock = 64;   // keys of a block
 
+// Blocks that a plan is made for: those of max_len keys; from 1024 on in 64
+// steps an octave, so that all plans up to a length can be looked at.
+constexpr int64_t kEveryBlock = 1024;
+inline int64_t plan_step(int64_t blocks) {                   // from ``blocks`` to the next
+  int64_t step = 1;
+  for (int64_t n = kEveryBlock; n <= blocks; n *= 2) step = step == 1 ? kEveryBlock / 64 : 2 * step;
+  return step;
+}
+inline int64_t plan_blocks(int64_t max_len) {
+  const int64_t blocks = (max_len + kCacheBlock - 1) / kCacheBlock, step = plan_step(blocks - 1);
+  return (blocks + step - 1) / step * step;
+}
+
 // The kernels of a head width.  16 and 32 rows: every wave takes key blocks of
 // its own, so an iteration covers ``waves`` blocks; more rows: the waves share a
 // block.  fit: workgroups of a CU at once.  Microseconds: us, an iteration with
@@ -49,7 +62,7 @@ inline CacheAttnPlan plan_cache_attention(int64_t B, int64_t T, int64_t Hq, int6
                                           bool split) {
   const CacheAttnShape* shapes = kCacheAttnShapes[D == 64 ? 0 : D == 128 ? 1 : 2];
   if (B * T * Hq > 1 << 22) split = false;                   // (the join, too, has fewer than 2^32 threads)
-  const int64_t rows = T * (Hq / Hkv), blocks = (max_len + kCacheBlock - 1) / kCacheBlock;
+  const int64_t rows = T * (Hq / Hkv), blocks = plan_blocks(max_len);
   const double read = (double)B * Hkv * blocks * kCacheBlock * D * 1.125 / 5.3e6;   // the caches' bytes, once
   CacheAttnPlan best{};
   double best_cost = 1e300;

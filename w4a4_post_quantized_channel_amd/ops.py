@@ -8,6 +8,7 @@ no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -778,7 +779,10 @@ def cache_read(cache: KVCache, slots: torch.Tensor, *, k: Optional[torch.Tensor]
     return k, v
 
 
+@functools.lru_cache(maxsize=256)
 def cache_attention_workspace_size(B: int, T: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
+    """Bytes that cache_attention uses with these sizes for histories of up to max_len keys (the host looks at the
+    plan of every length: 0.1 ms)."""
     return int(LIB.w4a4_cache_attention_workspace(B, T, Hq, Hkv, D, max_len))
 
 
@@ -795,8 +799,10 @@ def cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     table int32 [B, pages] lists a sequence's pages (an entry outside the cache is an
     absent page, whose keys nobody sees), lens int32[B] its keys; causal: the T queries
     are its last T positions.  max_len (default: the table's reach) is a bound of lens
-    that the host knows; pass workspace=make_cache_attention_workspace(...) for the
-    same max_len.  scale defaults to 1 / sqrt(D).  See include/w4a4.h.
+    that the host knows.  Pass workspace=make_cache_attention_workspace(...) for the
+    same max_len or a larger one: without, the keys are not split, and few queries over
+    a long history take several times as long.  scale defaults to 1 / sqrt(D).  See
+    include/w4a4.h.
     """
     B, T, Hq, D = q.shape
     if D != cache.D:
