@@ -1,6 +1,8 @@
 """Attention over the 4-bit cache at the ends of what its arguments may be: scales
 near the ends of fp32's range, small probabilities in every kernel, one workspace
 for histories of every length.  References in 64 bits."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -32,3 +34,27 @@ def test_one_workspace_serves_shorter_histories(ops, B, T, Hq, Hkv, D):
         R._assert_attention(out, _reference(q, c, table, lens, False, D ** -0.5, L), L, 6 * 2.0 ** 6 * c.v_scale)
         own = ops.make_cache_attention_workspace(B, T, Hq, Hkv, D, L, device=DEV)
         assert torch.equal(out, ops.cache_attention(q, c, table, lens, max_len=L, workspace=own))
+
+
+PEAKS = [  # T, Hq, D, split, rows of a workgroup
+    (1, 2, 128, True, 16), (1300, 4, 128, True, 256), (4000, 8, 64, False, 256), (700, 4, 256, True, 128),
+    (3000, 8, 256, False, 128),
+]
+
+
+@pytest.mark.parametrize("T,Hq,D,split,rows", PEAKS)
+def test_small_weights_beside_a_peak(ops, T, Hq, D, split, rows):
+    """One key ahead of 2^17 - 1 of 2^-20.7 of its weight, which together make 7 percent: subnormal fp16 numbers in
+    the product and in the sum of the kernels for many rows."""
+    L, page = 2 ** 17, 256
+    c = R._cache(ops, 7, L // page, page, 1, D, 1.0, 1.0)
+    for t, byte in ((c.k_codes, 0), (c.k_scales, 0x38), (c.v_codes, 0x22), (c.v_scales, 0x38)):
+        t.fill_(byte)
+    c.k_codes[0, 0, 0], c.v_codes[0, 0, 0] = 0x22, 0   # key 0: ones, its value zeros; the others: the reverse
+    table = torch.arange(L // page, dtype=torch.int32, device=DEV).view(1, -1)
+    lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+    q = torch.ones(1, T, Hq, D, dtype=BF, device=DEV)
+    scale = 20.7 * math.log(2.0) / D
+    ref = [r.expand(1, T, Hq, -1) for r in _reference(q[:, :1, :1], c, table, lens, False, scale, L)]
+    ws = ops.make_cache_attention_workspace(1, T, Hq, 1, D, L, device=DEV) if split else None
+    R._assert_attention(ops.cache_attention(q, c, table, lens, scale=scale, workspace=ws), ref, L, 1.0)

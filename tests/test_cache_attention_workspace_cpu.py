@@ -44,3 +44,11 @@ def test_it_is_no_larger_than_some_shorter_history_needs(plans):  # noqa: F811
         needs = {p["parts"] * B * T * Hq * (D + 2) * 4 if p["parts"] > 1 else 0
                  for p in plans([(*size, 64 * n, True) for n in range(1, 513)])}
         assert ops.cache_attention_workspace_size(*size, 64 * 512) == max(needs)
+
+
+def test_the_range_tests_meet_the_kernels_they_name(plans):  # noqa: F811
+    from test_cache_attention_range_gpu import PEAKS
+    shapes = []
+    shapes += [((1, T, Hq, 1, D, 2 ** 17, split), rows) for T, Hq, D, split, rows in PEAKS]
+    for (s, rows), p in zip(shapes, plans([s for s, _ in shapes])):
+        assert p["rows"] == rows and (p["parts"] > 1) == s[-1], (s, p)
