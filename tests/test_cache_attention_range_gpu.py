@@ -58,3 +58,25 @@ def test_small_weights_beside_a_peak(ops, T, Hq, D, split, rows):
     ref = [r.expand(1, T, Hq, -1) for r in _reference(q[:, :1, :1], c, table, lens, False, scale, L)]
     ws = ops.make_cache_attention_workspace(1, T, Hq, 1, D, L, device=DEV) if split else None
     R._assert_attention(ops.cache_attention(q, c, table, lens, scale=scale, workspace=ws), ref, L, 1.0)
+VALUES = [  # T, Hq, D, keys, split, rows of a workgroup
+    (1, 2, 128, 2 ** 15, True, 16), (1, 2, 64, 2 ** 15, False, 16), (4096, 8, 128, 2 ** 12, False, 256),
+    (404, 8, 128, 2 ** 14, True, 256),
+]
+
+
+@pytest.mark.parametrize("T,Hq,D,L,split,rows", VALUES)
+@pytest.mark.parametrize("v_scale", [2.0 ** -122, 2.0 ** 110])
+def test_value_scales_near_the_ends(ops, T, Hq, D, L, split, rows, v_scale):
+    """The outputs are the same numbers, scaled: sums of 2^12 weights and more, 2^5 or 2^7 each, do not cost them bits."""
+    page = 128
+    c = R._cache(ops, 5, L // page, page, 1, D, 2.0 ** -12, v_scale)
+    plain = ops.KVCache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.k_scale, 1.0)
+    table = torch.arange(L // page, dtype=torch.int32, device=DEV).view(1, -1)
+    lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+    q = R._rand(6, 1, T, Hq, D).to(BF).to(DEV)
+    ws = ops.make_cache_attention_workspace(1, T, Hq, 1, D, L, device=DEV) if split else None
+    out, want = (ops.cache_attention(q, x, table, lens, workspace=ws).double() for x in (c, plain))
+    want = want * v_scale                              # exact
+    # below bf16's normal numbers: half of their step, and of what ``want`` had beyond it
+    err, tol = (out - want).abs(), (2.0 ** -134 + 2.0 ** -135) * 1.01 * (want.abs() <= 2.0 ** -126)
+    assert bool((err <= tol).all()), float((err / want.abs().clamp(min=2.0 ** -126)).max())

@@ -71,6 +71,7 @@ struct Args {
   Divisor g, tiles, heads, parts;
   float c2;              // > 0
   float qmul;            // 1, -1 (scale < 0) or 0 (scale of zero: c2 is 1)
+  float v, vpost;        // v_scale = v * vpost: v over a sum of weights is no subnormal number
   float* po;             // parts > 1: [part][b][head][row][D], else null
   float* pml;            // [part][b][head][row][2]
 };
@@ -136,6 +137,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){a, b}, v2h));
+}
+
+// Four outputs as bf16.
+__device__ __forceinline__ uint2 pack_out(const Args& p, v4f x) {
+  x *= p.vpost;
+  return make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
 
 // The factor 2^(13 - floor(log2 amax)) of a query row, and its inverse.  Rows
@@ -452,11 +459,11 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
       *reinterpret_cast<v4f*>(p.po + x * D + d) = acc;
       if (d == 0) *reinterpret_cast<v2f*>(p.pml + x * 2) = (v2f){M, L};
     } else {
-      const float inv = L == 0.f ? 0.f : c.v_scale / L;
+      const float inv = L == 0.f ? 0.f : p.v / L;
       int g;
       const int t = div_by(row, p.g, g);
       uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * G + g) * a.o_sh + d;
-      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+      *reinterpret_cast<uint2*>(out) = pack_out(p, acc * inv);
     }
   }
 }
@@ -897,7 +904,7 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
               (v4f){o[x][d][4 * i], o[x][d][4 * i + 1], o[x][d][4 * i + 2], o[x][d][4 * i + 3]};
       if (h == 0) *reinterpret_cast<v2f*>(p.pml + at * 2) = (v2f){m[x], l[x]};
     } else {
-      const float inv = l[x] == 0.f ? 0.f : c.v_scale / l[x];
+      const float inv = l[x] == 0.f ? 0.f : p.v / l[x];
       int g;
       const int t = div_by(row, p.g, g);
       uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * G + g) * a.o_sh;
@@ -906,8 +913,7 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<uint2*>(out + 32 * d + 8 * i + 4 * h) =
-              make_uint2(pack_bf16(o[x][d][4 * i] * inv, o[x][d][4 * i + 1] * inv),
-                         pack_bf16(o[x][d][4 * i + 2] * inv, o[x][d][4 * i + 3] * inv));
+              pack_out(p, (v4f){o[x][d][4 * i], o[x][d][4 * i + 1], o[x][d][4 * i + 2], o[x][d][4 * i + 3]} * inv);
     }
   }
 }
@@ -971,12 +977,12 @@ __global__ void __launch_bounds__(256) cache_join_kernel(Args p) {
     L += mls[group + i][1] * e;
     acc += accs[group + i][x] * e;
   }
-  const float inv = L == 0.f ? 0.f : p.c.v_scale / L;
+  const float inv = L == 0.f ? 0.f : p.v / L;
   const int row = (int)(gr % p.rows), bh = (int)(gr / p.rows);
   int hk, g;
   const int b = div_by(bh, p.heads, hk), t = div_by(row, p.g, g);
   uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * (int)p.g.d + g) * a.o_sh + 4 * x;
-  *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+  *reinterpret_cast<uint2*>(out) = pack_out(p, acc * inv);
 }
 
 template <int D, int MT, int NW>
@@ -1013,6 +1019,9 @@ hipError_t launch_cache_attention(const w4a4_kvcache& c, const w4a4_cache_attn& 
   const double c2 = (double)a.scale * c.k_scale * 1.4426950408889634;
   p.qmul = c2 > 0 ? 1.f : c2 < 0 ? -1.f : 0.f;
   p.c2 = c2 == 0 ? 1.f : (float)(c2 < 0 ? -c2 : c2);
+  const bool tiny = c.v_scale < 0x1p-63f;                    // (weights, 2^15 at most, of 2^30 keys sum to 2^45)
+  p.v = tiny ? c.v_scale * 0x1p96f : c.v_scale;
+  p.vpost = tiny ? 0x1p-96f : 1.f;
   if (pl.parts > 1) {
     p.po = (float*)workspace;
     p.pml = p.po + (size_t)pl.parts * a.B * a.T * a.Hq * c.D;
