@@ -80,3 +80,40 @@ def test_value_scales_near_the_ends(ops, T, Hq, D, L, split, rows, v_scale):
     # below bf16's normal numbers: half of their step, and of what ``want`` had beyond it
     err, tol = (out - want).abs(), (2.0 ** -134 + 2.0 ** -135) * 1.01 * (want.abs() <= 2.0 ** -126)
     assert bool((err <= tol).all()), float((err / want.abs().clamp(min=2.0 ** -126)).max())
+
+
+KEYS = [(5, 16), (6000, 256)]   # T, rows of a workgroup
+
+
+@pytest.mark.parametrize("T,rows", KEYS)
+@pytest.mark.parametrize("gain", [2.0 ** 112, 2.0 ** 125])
+def test_keys_of_the_smallest_scales(ops, T, rows, gain):
+    """Queries near bf16's largest over keys whose scale is a subnormal number: the scores are the same."""
+    q, c, table, lens = R._attention_case(ops, 51, 1, T, 4, 2, 128, 16, 30, [470])
+    q = q.clamp(-7, 7)
+    small = ops.KVCache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.k_scale / gain, c.v_scale)
+    out = ops.cache_attention((q.float() * gain).to(BF), small, table, lens, max_len=480)
+    assert torch.equal(out, ops.cache_attention(q, c, table, lens, max_len=480))
+
+
+@pytest.mark.parametrize("T,rows", KEYS)
+def test_scores_of_nothing_under_the_largest_scales(ops, T, rows):
+    """Queries of zero make scores of zero, however large scale * k_scale: the mean of the values."""
+    q, c, table, lens = R._attention_case(ops, 53, 1, T, 4, 2, 128, 16, 30, [470])
+    big = ops.KVCache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, 2.0 ** 127, c.v_scale)
+    zero = torch.zeros_like(q)
+    assert torch.equal(ops.cache_attention(zero, big, table, lens, scale=1e30, max_len=480),
+                       ops.cache_attention(zero, c, table, lens, max_len=480))
+
+
+@pytest.mark.parametrize("T,rows", KEYS)
+def test_large_scores_under_a_small_scale(ops, T, rows):
+    """Scores of 2^40 and more are still numbers: the largest takes all the weight, under either scale of the keys."""
+    q, c, table, lens = R._attention_case(ops, 54, 1, T, 4, 2, 128, 16, 30, [470])
+    q = q.clamp(-7, 7)
+    gain = 2.0 ** 124
+    big = ops.KVCache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, 2.0 ** 30, c.v_scale)
+    small = ops.KVCache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, 2.0 ** 30 / gain, c.v_scale)
+    out = ops.cache_attention((q.float() * gain).to(BF), small, table, lens, max_len=480)
+    assert torch.equal(out, ops.cache_attention(q, big, table, lens, max_len=480))
+    assert bool(torch.isfinite(out.float()).all())

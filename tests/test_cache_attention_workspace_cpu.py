@@ -47,9 +47,10 @@ def test_it_is_no_larger_than_some_shorter_history_needs(plans):  # noqa: F811
 
 
 def test_the_range_tests_meet_the_kernels_they_name(plans):  # noqa: F811
-    from test_cache_attention_range_gpu import PEAKS, VALUES
+    from test_cache_attention_range_gpu import KEYS, PEAKS, VALUES
     shapes = []
     shapes += [((1, T, Hq, 1, D, 2 ** 17, split), rows) for T, Hq, D, split, rows in PEAKS]
     shapes += [((1, T, Hq, 1, D, L, split), rows) for T, Hq, D, L, split, rows in VALUES]
+    shapes += [((1, T, 4, 2, 128, 480, False), rows) for T, rows in KEYS]
     for (s, rows), p in zip(shapes, plans([s for s, _ in shapes])):
         assert p["rows"] == rows and (p["parts"] > 1) == s[-1], (s, p)

@@ -69,7 +69,7 @@ struct Args {
   int rows;              // T G rows of a sequence and KV head
   int lp;                // log2 of the page
   Divisor g, tiles, heads, parts;
-  float c2;              // > 0
+  float c2, cpost;       // > 0: |scale| log2 e k_scale = c2 * cpost
   float qmul;            // 1, -1 (scale < 0) or 0 (scale of zero: c2 is 1)
   float v, vpost;        // v_scale = v * vpost: v over a sum of weights is no subnormal number
   float* po;             // parts > 1: [part][b][head][row][D], else null
@@ -152,6 +152,12 @@ __device__ __forceinline__ float row_factor(float amax, float& inverse) {
   e = e < 14 ? 14 : e > 254 ? 254 : e;
   inverse = __uint_as_float((uint32_t)(e - 13) << 23);
   return __uint_as_float((uint32_t)(267 - e) << 23);
+}
+
+// What turns a row's scores into units of exp2.  Never zero (-inf, which is
+// excluded, times it stays -inf) and never infinite (zero times it stays zero).
+__device__ __forceinline__ float score_factor(const Args& p, float inverse) {
+  return fminf(fmaxf(p.c2 * inverse * p.cpost, 1.17549435e-38f), 3.40282347e38f);
 }
 
 template <int D_, int MT_, int NW_, bool ONCE_>
@@ -293,7 +299,7 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
     }
     float inv;
     const float fac = row_factor(group_max(amax), inv) * p.qmul;
-    cr[x] = fmaxf(p.c2 * inv, 1.17549435e-38f);          // never zero: -inf (excluded) times it stays -inf
+    cr[x] = score_factor(p, inv);
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -668,7 +674,7 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
     }
     float inv;
     const float fac = row_factor(half_max(amax), inv) * p.qmul;
-    cr[x] = fmaxf(p.c2 * inv, 1.17549435e-38f);          // never zero: -inf (excluded) times it stays -inf
+    cr[x] = score_factor(p, inv);
 #pragma unroll
     for (int s = 0; s < KC; ++s) {
       const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
@@ -1018,7 +1024,10 @@ hipError_t launch_cache_attention(const w4a4_kvcache& c, const w4a4_cache_attn& 
   p.parts = divisor(pl.parts);
   const double c2 = (double)a.scale * c.k_scale * 1.4426950408889634;
   p.qmul = c2 > 0 ? 1.f : c2 < 0 ? -1.f : 0.f;
-  p.c2 = c2 == 0 ? 1.f : (float)(c2 < 0 ? -c2 : c2);
+  // as a product, which meets the queries' factors where fp32 alone has no bits left for it, or no number
+  const double mag = c2 == 0 ? 1.0 : c2 < 0 ? -c2 : c2;
+  p.cpost = mag < 0x1p-64 ? 0x1p-64f : mag > 0x1p64 ? 0x1p64f : 1.f;
+  p.c2 = (float)(mag / p.cpost);
   const bool tiny = c.v_scale < 0x1p-63f;                    // (weights, 2^15 at most, of 2^30 keys sum to 2^45)
   p.v = tiny ? c.v_scale * 0x1p96f : c.v_scale;
   p.vpost = tiny ? 0x1p-96f : 1.f;
