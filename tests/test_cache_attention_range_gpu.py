@@ -117,3 +117,74 @@ def test_large_scores_under_a_small_scale(ops, T, rows):
     out = ops.cache_attention((q.float() * gain).to(BF), small, table, lens, max_len=480)
     assert torch.equal(out, ops.cache_attention(q, big, table, lens, max_len=480))
     assert bool(torch.isfinite(out.float()).all())
+
+
+@pytest.mark.parametrize("T,rows", KEYS)
+@pytest.mark.parametrize("log2", [8, 11, 13, 14, 15, 16, 17, 18, 19, 20, 22, 26, 40, 70, 100])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_of_any_size(ops, T, rows, log2, sign):
+    """A key ahead of the others takes all the weight, also where a step of the scores is more than the whole range
+    of the weights.  A score is off by (D / 2 2^-24 + 2^-22) smax (see _assert_attention): rows with a second key
+    within twice that and 40 are not compared."""
+    q, c, table, lens = R._attention_case(ops, 55, 1, T, 4, 2, 128, 16, 30, [470])
+    big = ops.KVCache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, 2.0 ** log2, c.v_scale)
+    out = ops.cache_attention(q, big, table, lens, scale=sign * 128 ** -0.5, max_len=480)
+    assert bool(torch.isfinite(out.float()).all())
+    kv, _ = R._values(c.k_codes, c.k_scales, 1.0)
+    vv, _ = R._values(c.v_codes, c.v_scales, 1.0)
+    at = table[0].cpu().long()
+    clear = 0
+    for h in range(4):
+        k = kv[at, h // 2].reshape(480, 128)[:470].to(DEV) * 2.0 ** log2 * sign * 128 ** -0.5
+        v = vv[at, h // 2].reshape(480, 128)[:470].to(DEV) * c.v_scale
+        x = q[0, :, h].double()
+        s = x @ k.t().contiguous()
+        smax = (x.abs() @ k.abs().t().contiguous()).amax(-1)
+        top = s.topk(2, dim=-1)
+        gap = top.values[:, 0] - top.values[:, 1]
+        far = gap > 2.02 * (64 * 2.0 ** -24 + 2.0 ** -22) * smax + 40
+        clear += int(far.sum())
+        want = v[top.indices[:, 0]]
+        err = (out[0, :, h].double() - want).abs()[far]
+        assert bool((err <= 2.0 ** -8 * want.abs()[far] + 2.0 ** -30).all()), float(err.max())
+    assert clear > 3 * T
+
+
+SHIFTED = [  # T, Hq, D, keys, split, rows of a workgroup
+    (5, 8, 128, 480, False, 16), (5, 8, 64, 1920, True, 16), (5, 8, 256, 480, False, 16), (3000, 8, 64, 480, False, 256),
+    (3000, 8, 128, 480, False, 256), (3000, 8, 256, 480, False, 128), (404, 8, 128, 2 ** 14, True, 256),
+]
+
+
+@pytest.mark.parametrize("T,Hq,D,L,split,rows", SHIFTED)
+@pytest.mark.parametrize("gain", [2.0 ** 9, 2.0 ** 10, 2.0 ** 12])
+@pytest.mark.parametrize("shift", ["up", "down", "up then none", "down then none then up", "none then up", "by keys", "by blocks"])
+def test_scores_beside_each_other_far_from_zero(ops, T, Hq, D, L, split, rows, gain, shift):
+    """Scores of a few units on top of plus or minus 2^19, 2^20 or 2^22 in one channel.  They are multiples of 1 / 8
+    (quarters times halves): beside 2^20 exact in fp32, whose last place there is 1 / 8.  Beside 2^22 it is 1 / 2: each
+    score is off by half of that, d = 1 / 4, a weight by a factor of e^d at most and its sum too, the output by
+    (e^(2 d) - 1) A < 0.65 A."""
+    page = 16
+    c = R._cache(ops, 61, L // page, page, 1, D, 1.0, 2.0 ** -9)
+    g = torch.Generator().manual_seed(62)
+    codes = torch.zeros(L, D, dtype=torch.uint8)
+    codes[:, 16] = torch.randint(0, 16, (L,), generator=g)               # -6 to 6
+    n, j = L // 3, torch.arange(L)
+    up = {"up": j >= 0, "down": j < 0, "up then none": j < n, "down then none then up": j >= 2 * n, "none then up": j >= n,
+          "by keys": j % 2 == 0, "by blocks": j // 64 % 3 == 1}[shift]
+    down = {"down": j >= 0, "down then none then up": j < n, "by blocks": j // 64 % 3 == 0}.get(shift, j < 0)
+    codes[up, 0], codes[down, 0] = 6, 14                                 # 4 and -4 times a scale of 256
+    c.k_codes.copy_((codes[:, 0::2] | codes[:, 1::2] << 4).view(L // page, 1, page, D // 2))
+    c.k_scales.fill_(0x38)
+    c.k_scales[..., 0] = 0x78
+    table = torch.arange(L // page, dtype=torch.int32, device=DEV).view(1, -1)
+    lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+    q = torch.zeros(1, T, Hq, D, dtype=BF, device=DEV)
+    q[..., 0] = gain
+    q[..., 16] = (torch.randint(-4, 5, (1, T, Hq), generator=g) / 4).to(BF).to(DEV)
+    ws = ops.make_cache_attention_workspace(1, T, Hq, 1, D, L, device=DEV) if split else None
+    out = ops.cache_attention(q, c, table, lens, scale=1.0, max_len=L, workspace=ws)
+    ref, A, smax = _reference(q, c, table, lens, False, 1.0, L)
+    # (where scores are exact, so are their differences: an error like that of scores of a few units)
+    smax.fill_(16.0 if gain < 2.0 ** 11 else 0.325 / (D / 2 * 2.0 ** -24 + 2.0 ** -22))
+    R._assert_attention(out, (ref, A, smax), L, 6 * 2.0 ** 6 * c.v_scale)

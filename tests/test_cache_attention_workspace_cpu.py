@@ -47,8 +47,8 @@ def test_it_is_no_larger_than_some_shorter_history_needs(plans):  # noqa: F811
 
 
 def test_the_range_tests_meet_the_kernels_they_name(plans):  # noqa: F811
-    from test_cache_attention_range_gpu import KEYS, PEAKS, VALUES
-    shapes = []
+    from test_cache_attention_range_gpu import KEYS, PEAKS, SHIFTED, VALUES
+    shapes = [((1, T, Hq, 1, D, L, split), rows) for T, Hq, D, L, split, rows in SHIFTED]
     shapes += [((1, T, Hq, 1, D, 2 ** 17, split), rows) for T, Hq, D, split, rows in PEAKS]
     shapes += [((1, T, Hq, 1, D, L, split), rows) for T, Hq, D, L, split, rows in VALUES]
     shapes += [((1, T, 4, 2, 128, 480, False), rows) for T, rows in KEYS]

@@ -61,6 +61,13 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) v2i lds_v2i;
 
 constexpr float kLazy = 8.f, kFewUp = 7.f;   // p < 2^15
+// Where |m| reaches this its last place, an eighth and more, is no small part of
+// what p may grow by (from 2^24 on p passed fp16, or all of a row's were lost).
+// Such a row's scores are summed from minus a base on, the score that m stands
+// for.  The kernel for many rows always starts its sums there (no time at width 128,
+// 2% at 64); the one for few takes its keys once more, with bases, where a
+// row turns out to need one: in the loop they cost 2 to 7% there.
+constexpr float kFar = 1048576.f;
 constexpr int BN = kCacheBlock;
 
 struct Args {
@@ -158,6 +165,32 @@ __device__ __forceinline__ float row_factor(float amax, float& inverse) {
 // excluded, times it stays -inf) and never infinite (zero times it stays zero).
 __device__ __forceinline__ float score_factor(const Args& p, float inverse) {
   return fminf(fmaxf(p.c2 * inverse * p.cpost, 1.17549435e-38f), 3.40282347e38f);
+}
+
+// The next m of a row that moves to its scores' maximum ``most``, and what its
+// scores, taken relative to minus ``from``, change by.  Beside a base m is what
+// that was rounded by, or, where this is far as well, left out.
+__device__ __forceinline__ float rebase(bool moves, float most, float factor, float& m, float from) {
+  if (!moves) return 0.f;
+  const float top = most - from, full = top * factor;
+  if (__builtin_fabsf(full) < kFar) {
+    m = full;
+    return -from;
+  }
+  const float step = -top - from, rest = (most + step) * factor;
+  const bool far = __builtin_fabsf(rest) >= kFar;
+  m = far ? 0.f : rest;
+  return far ? -most : step;
+}
+// At the end: m as other sums of the row know it, rounded, and the factor that
+// what was taken relative to the exact one gets for that (a last place of 60 and
+// more is left as it is: scores that differ by less than it differ by their own
+// rounding).
+__device__ __forceinline__ float to_m(float from, float factor, float& m) {
+  if (from == 0.f) return 1.f;
+  const float rest = m;
+  m = __builtin_fmaf(-from, factor, rest);
+  return __builtin_amdgcn_exp2f(fminf(fmaxf(__builtin_fmaf(-from, factor, -m) + rest, -30.f), 30.f));
 }
 
 template <int D_, int MT_, int NW_, bool ONCE_>
@@ -322,111 +355,161 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
   const int trow = 16 * (lr >> 2) + 4 * lg + (lr & 3);
   const uint32_t tbase = (uint32_t)(trow * (D / 2)), tswz = chunk(trow);
 
+  bool far = false;                                      // some m was too large to go without a base
+  float from[MT];                                        // with bases: minus them, what sums of scores start from
   // The next block's values are loaded when this one's are in LDS, its keys when
   // this one's are multiplied: into the registers that those leave.
-  for (int blk = lo + wave; blk < hi; blk += NW) {
-    const int j0 = blk * BN;
-    const uint32_t absent = bad;
-    pg = held(blk + NW, pg1);
-    pg1 = load_pages(blk + 2 * NW);
+  auto walk = [&](auto based_) {
+    constexpr bool based = based_();
+    for (int blk = lo + wave; blk < hi; blk += NW) {
+      const int j0 = blk * BN;
+      const uint32_t absent = bad;
+      pg = held(blk + NW, pg1);
+      pg1 = load_pages(blk + 2 * NW);
 
-    // V into LDS: piece t holds keys 16 t .. 16 t + 15, CB bytes a lane
+      // V into LDS: piece t holds keys 16 t .. 16 t + 15, CB bytes a lane
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int row = 16 * t + lane / (D / 2 / C::CB), ch = lane % (D / 2 / C::CB) * (C::CB / 8), z = chunk(row);
+      for (int t = 0; t < 4; ++t) {
+        const int row = 16 * t + lane / (D / 2 / C::CB), ch = lane % (D / 2 / C::CB) * (C::CB / 8), z = chunk(row);
 #pragma unroll
-      for (int i = 0; i < C::CB / 8; ++i)
-        *reinterpret_cast<uint2*>(vl + row * (D / 2) + ((ch + i) ^ z) * 8) = make_uint2(vw[t].w[2 * i], vw[t].w[2 * i + 1]);
-    }
-    // scales of key 16 lg + lr, in the order of the second product: t = lg, (g, i) from lr
-    {
-      const int at = (lr >> 2) * 16 + lg * 4 + (lr & 3);
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-        *reinterpret_cast<uint16_t*>(sl + (d * BN + at) * 2) = (uint16_t)scale_bits(vsw.w[d / 4] >> (8 * (d & 3)));
-    }
-
-    in_order();
-    load_v(blk + NW, pg);
-    in_order();
-
-    v4f s[MT][4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int x = 0; x < MT; ++x) s[x][t] = (v4f){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const v2h sc = both(scale_bits(ksw[t].w[0] >> (8 * (k / 2))));
-        const v8h kf = decode8(kw[t].w[k], sc, sc, sc, sc);
-#pragma unroll
-        for (int x = 0; x < MT; ++x) s[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[x][k], s[x][t], 0, 0, 0);
+        for (int i = 0; i < C::CB / 8; ++i)
+          *reinterpret_cast<uint2*>(vl + row * (D / 2) + ((ch + i) ^ z) * 8) =
+              make_uint2(vw[t].w[2 * i], vw[t].w[2 * i + 1]);
       }
-    }
-    in_order();
-    load_k(blk + NW, pg);
-    in_order();
-    if (absent || j0 + BN > first) {
+      // scales of key 16 lg + lr, in the order of the second product: t = lg, (g, i) from lr
+      {
+        const int at = (lr >> 2) * 16 + lg * 4 + (lr & 3);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+          *reinterpret_cast<uint16_t*>(sl + (d * BN + at) * 2) = (uint16_t)scale_bits(vsw.w[d / 4] >> (8 * (d & 3)));
+      }
+
+      in_order();
+      load_v(blk + NW, pg);
+      in_order();
+
+      v4f s[MT][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int x = 0; x < MT; ++x) {
+          const float z = based ? from[x] : 0.f;
+          s[x][t] = (v4f){z, z, z, z};
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const v2h sc = both(scale_bits(ksw[t].w[0] >> (8 * (k / 2))));
+          const v8h kf = decode8(kw[t].w[k], sc, sc, sc, sc);
+#pragma unroll
+          for (int x = 0; x < MT; ++x) s[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[x][k], s[x][t], 0, 0, 0);
+        }
+      }
+      in_order();
+      load_k(blk + NW, pg);
+      in_order();
+      if (absent || j0 + BN > first) {
+#pragma unroll
+        for (int x = 0; x < MT; ++x) {
+          const int vis = lim[x] - j0 - 4 * lg;
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[x][t][i] = 16 * t + i < vis && !(absent >> t & 1) ? s[x][t][i] : -INFINITY;
+        }
+      }
+      v8h pf[MT][2];
 #pragma unroll
       for (int x = 0; x < MT; ++x) {
-        const int vis = lim[x] - j0 - 4 * lg;
+        float tm = s[x][0][0];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[x][t][i] = 16 * t + i < vis && !(absent >> t & 1) ? s[x][t][i] : -INFINITY;
+          for (int i = 0; i < 4; ++i) tm = fmaxf(tm, s[x][t][i]);
+        const float most = group_max(tm);
+        tm = most * cr[x];
+        if (__any(tm > m[x] + kLazy)) {
+          const float mn = tm > m[x] + kLazy ? tm : m[x];   // only the rows that need it move
+          const float f = __builtin_amdgcn_exp2f(m[x] - (mn == -INFINITY ? 0.f : mn));
+          l[x] *= f;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[x][d] *= f;
+          if constexpr (based) {
+            const float step = rebase(tm > m[x] + kLazy, most, cr[x], m[x], from[x]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) s[x][t] += step;
+            from[x] += step;
+          } else {
+            far |= __any(__builtin_fabsf(mn) >= kFar && mn != -INFINITY);
+            m[x] = mn;
+          }
+        }
+        const float nm = m[x] == -INFINITY ? 0.f : kFewUp - m[x];
+        uint32_t w[8];
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], cr[x], nm));
+            const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i + 1], cr[x], nm));
+            l0 += e0;
+            l1 += e1;
+            w[2 * t + i / 2] = pack_f16(e0, e1);   // the second product takes p with 11 significant bits; l keeps 24
+          }
+        l[x] += l0 + l1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          pf[x][h] = __builtin_bit_cast(v8h, (v4i){(int)w[4 * h], (int)w[4 * h + 1], (int)w[4 * h + 2], (int)w[4 * h + 3]});
       }
+      // A wave's LDS accesses keep their order; the compiler has to keep it too.
+      asm volatile("" ::: "memory");
+      v2i vcd[DT];
+      uint4 vsc[DT][2];
+      auto read_v = [&](int d) {
+        vcd[d] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i*)(vl + tbase + ((d ^ tswz) * 8)));
+        const uint4* sp = reinterpret_cast<const uint4*>(sl + (d * BN + lg * 16) * 2);
+        vsc[d][0] = sp[0], vsc[d][1] = sp[1];
+      };
+      read_v(0);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        if (d + 1 < DT) read_v(d + 1);
+        __builtin_amdgcn_sched_barrier(0);   // else, short of registers, reads wait right before their products
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 q4 = vsc[d][h];
+          const v8h vf = decode8((uint32_t)vcd[d][h], __builtin_bit_cast(v2h, q4.x), __builtin_bit_cast(v2h, q4.y),
+                                 __builtin_bit_cast(v2h, q4.z), __builtin_bit_cast(v2h, q4.w));
+#pragma unroll
+          for (int x = 0; x < MT; ++x) o[x][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[x][h], o[x][d], 0, 0, 0);
+        }
+      }
+      asm volatile("" ::: "memory");
     }
-    v8h pf[MT][2];
+  };
+  struct Without { constexpr bool operator()() const { return false; } };
+  struct With { constexpr bool operator()() const { return true; } };
+  walk(Without());
+  if (__builtin_expect(far, 0)) {                        // once more, from the start
+    pg = held(lo + wave, load_pages(lo + wave));
+    pg1 = load_pages(lo + wave + NW);
+    load_v(lo + wave, pg);
+    load_k(lo + wave, pg);
 #pragma unroll
     for (int x = 0; x < MT; ++x) {
-      float tm = s[x][0][0];
+      m[x] = -INFINITY;
+      l[x] = from[x] = 0.f;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tm = fmaxf(tm, s[x][t][i]);
-      tm = group_max(tm) * cr[x];
-      if (__any(tm > m[x] + kLazy)) {
-        const float mn = tm > m[x] + kLazy ? tm : m[x];   // only the rows that need it move
-        const float f = __builtin_amdgcn_exp2f(m[x] - (mn == -INFINITY ? 0.f : mn));
-        m[x] = mn;
-        l[x] *= f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[x][d] *= f;
-      }
-      const float nm = m[x] == -INFINITY ? 0.f : kFewUp - m[x];
-      uint32_t w[8];
-      float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], cr[x], nm));
-          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i + 1], cr[x], nm));
-          l0 += e0;
-          l1 += e1;
-          w[2 * t + i / 2] = pack_f16(e0, e1);   // the second product takes p with 11 significant bits; l keeps 24
-        }
-      l[x] += l0 + l1;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        pf[x][h] = __builtin_bit_cast(v8h, (v4i){(int)w[4 * h], (int)w[4 * h + 1], (int)w[4 * h + 2], (int)w[4 * h + 3]});
+      for (int d = 0; d < DT; ++d) o[x][d] = (v4f){0.f, 0.f, 0.f, 0.f};
     }
-    // A wave's LDS accesses keep their order; the compiler has to keep it too.
-    asm volatile("" ::: "memory");
+    walk(With());
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      const v2i w = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i*)(vl + tbase + ((d ^ tswz) * 8)));
-      const uint4* sp = reinterpret_cast<const uint4*>(sl + (d * BN + lg * 16) * 2);
+    for (int x = 0; x < MT; ++x) {
+      const float f = to_m(from[x], cr[x], m[x]);
+      l[x] *= f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 q4 = sp[h];
-        const v8h vf = decode8((uint32_t)w[h], __builtin_bit_cast(v2h, q4.x), __builtin_bit_cast(v2h, q4.y),
-                               __builtin_bit_cast(v2h, q4.z), __builtin_bit_cast(v2h, q4.w));
-#pragma unroll
-        for (int x = 0; x < MT; ++x) o[x][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[x][h], o[x][d], 0, 0, 0);
-      }
+      for (int d = 0; d < DT; ++d) o[x][d] *= f;
     }
-    asm volatile("" ::: "memory");
   }
 
   // Join the waves: each leaves its (m, l) and its o in LDS, and all threads sum
@@ -746,9 +829,14 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  const v16f zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  v16f from[NS];                                          // minus the row's base: what sums of scores start from
+#pragma unroll
+  for (int x = 0; x < NS; ++x) {
+    from[x] = (v16f){0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    asm volatile("" : "+v"(from[x]));                     // (registers of its own, not copies of one for every sum)
+  }
   auto qk = [&](Scores& s, int x, int t, const v8h& f) {
-    s[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, qf[x][t], t == 0 ? zero : s[x], 0, 0, 0);
+    s[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, qf[x][t], t == 0 ? from[x] : s[x], 0, 0, 0);
   };
 
   // Phase 1: scores `s` to probabilities, products of K's half `half` to `next`.
@@ -782,19 +870,26 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
         float tm = s[x][0];
 #pragma unroll
         for (int e = 1; e < 16; ++e) tm = fmaxf(tm, s[x][e]);
+        const float most = half_max(tm);
+        tm = most * cr[x];
         // only the rows that need it move: no row's result depends on its neighbours
-        const bool moves = half_max(lb[x]) > kMost || m[x] == -INFINITY;
-        const float mn = moves ? fmaxf(m[x], half_max(tm) * cr[x]) : m[x];
-        const float f = __builtin_amdgcn_exp2f(m[x] - (mn == -INFINITY ? 0.f : mn));
-        m[x] = mn;
+        const bool moves = (half_max(lb[x]) > kMost || m[x] == -INFINITY) && tm > m[x];
+        const float f = __builtin_amdgcn_exp2f(m[x] - (moves ? tm : m[x] == -INFINITY ? 0.f : m[x]));
         l[x] *= f;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[x][d][e] *= f;
+        const float step = rebase(moves, most, cr[x], m[x], from[x][0]);
+        if (__any(step != 0.f)) {
+          s[x] += step;
+          next[x] += step;
+          from[x] += step;
+          asm volatile("" : "+v"(from[x]));
+        }
         lb[x] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) prob(s, x, w, mn == -INFINITY ? 0.f : kManyUp - mn);
+        for (int w = 0; w < 8; ++w) prob(s, x, w, m[x] == -INFINITY ? 0.f : kManyUp - m[x]);
       }
     }
 #pragma unroll
@@ -901,14 +996,15 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
     const int rl = (wave * NS + x) * 32 + lr, row = r0 + rl;
     if (rl >= nrows) continue;
     if (p.po) {
+      const float f = to_m(from[x][0], cr[x], m[x]);
       const int64_t at = (((int64_t)part * a.B + b) * c.Hkv + hk) * p.rows + row;
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<v4f*>(p.po + at * D + 32 * d + 8 * i + 4 * h) =
-              (v4f){o[x][d][4 * i], o[x][d][4 * i + 1], o[x][d][4 * i + 2], o[x][d][4 * i + 3]};
-      if (h == 0) *reinterpret_cast<v2f*>(p.pml + at * 2) = (v2f){m[x], l[x]};
+              (v4f){o[x][d][4 * i], o[x][d][4 * i + 1], o[x][d][4 * i + 2], o[x][d][4 * i + 3]} * f;
+      if (h == 0) *reinterpret_cast<v2f*>(p.pml + at * 2) = (v2f){m[x], l[x] * f};
     } else {
       const float inv = l[x] == 0.f ? 0.f : p.v / l[x];
       int g;
