@@ -36,7 +36,7 @@
 // What bounds it.  One token each of 64 sequences, 32 heads over 8 of 128, 4096
 // to 8192 keys: the caches' 463 MB at 5.4 TB/s, 85 us (a device copy reaches
 // 5.1).  There each key is read by one workgroup only, past the caches: 92 us
-// against 102 with ordinary loads (7% slower where the history fits the 256 MB
+// against 102 with ordinary loads (widths 128 and 256; 7% slower where the history fits the 256 MB
 // cache and is read again at once), and in one part: 85 against 89 in two and 92
 // in three.  A chunk of 8 x 50 queries, 16 heads over 4, 2090 keys (21 us): turns
 // of 7000 cycles in which two waves a SIMD convert codes (1150 cycles a block and
@@ -90,7 +90,8 @@ struct Words {
   uint32_t w[N];
 };
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-// ONCE: no other workgroup reads them, and they leave the caches first.
+// ONCE: no other workgroup reads them, and they leave the caches first (16 bytes
+// or more; width 64 takes 8 and reads them in the ordinary way).
 template <int BYTES, bool ONCE = false>
 __device__ __forceinline__ Words<BYTES> load_words(const uint8_t* p) {
   Words<BYTES> r;
@@ -220,7 +221,7 @@ struct Limit {
 };
 
 template <typename C>
-__global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 ? 2 : 1) attn_few_kernel(Args p) {
+__global__ void __launch_bounds__(64 * C::NW, 2) attn_few_kernel(Args p) {
   constexpr int D = C::D, MT = C::MT, NW = C::NW, R = C::R, KS = C::KS, DT = C::DT;
   __shared__ __attribute__((aligned(16))) uint8_t smem[C::LDS];
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
@@ -597,7 +598,7 @@ constexpr float kMost = 32768.f, kManyUp = 5.f;
 template <int D_, int W_>
 struct Many {
   static constexpr int D = D_, W = W_;
-  static constexpr int NS = 1, R = W * 32 * NS;         // sets of 32 rows of a wave (two sets: see above)
+  static constexpr int R = W * 32;
   static constexpr int RB = 2 * D, MAT = BN * RB;       // bytes of a row, of a block of K or V
   static constexpr int KC = D / 16, DB = D / 32;        // steps, channel blocks
   static constexpr int MATS = 8 / W;                    // W = 8: waves 0-3 convert K, 4-7 V; W = 4: each both
@@ -636,7 +637,7 @@ __device__ __forceinline__ float half_sum(float x) {
 
 template <typename C>
 __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) {
-  constexpr int D = C::D, NS = C::NS, R = C::R, MATS = C::MATS, KC = C::KC, DB = C::DB, AHEAD = C::AHEAD;
+  constexpr int D = C::D, R = C::R, MATS = C::MATS, KC = C::KC, DB = C::DB, AHEAD = C::AHEAD;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];   // K of even and odd blocks, V of them
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
   int rem;
   const Limit limit(p, b);
   const int last = limit(div_by(r0 + nrows - 1, p.g, rem));
-  const int first = limit(div_by(r0 + min(wave * 32 * NS, nrows - 1), p.g, rem));   // of this wave
+  const int first = limit(div_by(r0 + min(wave * 32, nrows - 1), p.g, rem));   // of this wave
   const int nblk = (max(last, 0) + BN - 1) / BN;
   const int per = (nblk + (int)p.parts.d - 1) / (int)p.parts.d;
   const int lo = min(part * per, nblk), n = min(lo + per, nblk) - lo;
@@ -734,15 +735,14 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
   for (int x = 0; x < 2; ++x) early[x] = load_raw(mat[0], x * BN, pg[x]);
 
   // queries: row tile r0, wave, set, lane
-  v8h qf[NS][KC];
-  float cr[NS], m[NS], l[NS];
-  int lim[NS];
-#pragma unroll
-  for (int x = 0; x < NS; ++x) {
-    const int row = r0 + min((wave * NS + x) * 32 + lr, nrows - 1);   // rows past the end repeat the last
+  v8h qf[KC];
+  float cr, m = -INFINITY, l = 0.f;                       // l: this half's keys only
+  int lim;
+  {
+    const int row = r0 + min(wave * 32 + lr, nrows - 1);   // rows past the end repeat the last
     int g;
     const int t = div_by(row, p.g, g);
-    lim[x] = limit(t);
+    lim = limit(t);
     const uint16_t* q = (const uint16_t*)a.q + b * a.q_sb + t * a.q_st + (int64_t)(hk * G + g) * a.q_sh + h * 8;
     uint4 v[KC];
     float amax = 0.f;
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
     }
     float inv;
     const float fac = row_factor(half_max(amax), inv) * p.qmul;
-    cr[x] = score_factor(p, inv);
+    cr = score_factor(p, inv);
 #pragma unroll
     for (int s = 0; s < KC; ++s) {
       const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
@@ -765,20 +765,16 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         f[i] = (int)pack_f16(__uint_as_float(w[i] << 16) * fac, __uint_as_float(w[i] & 0xFFFF0000u) * fac);
-      qf[x][s] = __builtin_bit_cast(v8h, f);
+      qf[s] = __builtin_bit_cast(v8h, f);
       // with one wave a SIMD it stays in accumulation registers, from where the products take it
-      if constexpr (C::W == 4) asm volatile("" : "+a"(qf[x][s]));
+      if constexpr (C::W == 4) asm volatile("" : "+a"(qf[s]));
     }
-    m[x] = -INFINITY;
-    l[x] = 0.f;                                          // this half's keys only
   }
-  v16f o[NS][DB];
+  v16f o[DB];
 #pragma unroll
-  for (int x = 0; x < NS; ++x)
+  for (int d = 0; d < DB; ++d)
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[x][d][i] = 0.f;
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
 
   // addresses of the fragment reads in the buffers that are read next
   const uint32_t ka = lds0 + lr * C::RB + ((h ^ swz_k<D>(lr)) << 4);
@@ -802,98 +798,78 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
     const v4s v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(vad[1][t % DB] + off));
     frag[t % AHEAD] = __builtin_bit_cast(v4i, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  typedef v16f Scores[NS];     // of 32 keys
-  uint32_t pk[NS][8];
-  float lb[NS];
+  typedef v16f Scores;     // of 32 keys
+  uint32_t pk[8];
+  float lb;
   const v2h one = {(_Float16)1.f, (_Float16)1.f};
-  auto prob = [&](const Scores& s, int x, int w, float nm) {   // probabilities 2 w and 2 w + 1 of a set
-    const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][2 * w], cr[x], nm));
-    const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][2 * w + 1], cr[x], nm));
-    pk[x][w] = pack_f16(e0, e1);   // the second product takes p with 11 significant bits, and so does the sum
-    lb[x] = __builtin_amdgcn_fdot2(__builtin_bit_cast(v2h, pk[x][w]), one, lb[x], false);
+  auto prob = [&](const Scores& s, int w, float nm) {   // probabilities 2 w and 2 w + 1
+    const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * w], cr, nm));
+    const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * w + 1], cr, nm));
+    pk[w] = pack_f16(e0, e1);   // the second product takes p with 11 significant bits, and so does the sum
+    lb = __builtin_amdgcn_fdot2(__builtin_bit_cast(v2h, pk[w]), one, lb, false);
   };
   // scores of keys from j0 (of the part) on that a row does not see; bad: absent groups of 16
   auto exclude = [&](Scores& s, int j0, uint32_t bad) {
     j0 += lo * BN;
     if ((bad & 3) == 0 && j0 + 32 <= first) return;
+    const int vis = lim - j0 - 4 * h;
 #pragma unroll
-    for (int x = 0; x < NS; ++x) {
-      const int vis = lim[x] - j0 - 4 * h;
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        s[x][e] = 8 * (e >> 2) + (e & 3) < vis && !(bad >> (e >> 3) & 1) ? s[x][e] : -INFINITY;
-    }
+    for (int e = 0; e < 16; ++e)
+      s[e] = 8 * (e >> 2) + (e & 3) < vis && !(bad >> (e >> 3) & 1) ? s[e] : -INFINITY;
   };
   auto sync = [&]() {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  v16f from[NS];                                          // minus the row's base: what sums of scores start from
-#pragma unroll
-  for (int x = 0; x < NS; ++x) {
-    from[x] = (v16f){0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    asm volatile("" : "+v"(from[x]));                     // (registers of its own, not copies of one for every sum)
-  }
-  auto qk = [&](Scores& s, int x, int t, const v8h& f) {
-    s[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, qf[x][t], t == 0 ? from[x] : s[x], 0, 0, 0);
+  // minus the row's base: what sums of scores start from
+  v16f from = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  asm volatile("" : "+v"(from));                          // (registers of its own, not copies of one for every sum)
+  auto qk = [&](Scores& s, int t, const v8h& f) {
+    s = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, qf[t], t == 0 ? from : s, 0, 0, 0);
   };
 
   // Phase 1: scores `s` to probabilities, products of K's half `half` to `next`.
   auto phase1 = [&](Scores& s, Scores& next, auto half_, auto then_, auto&& extra) {
     constexpr int half = half_(), then = then_();    // then: the half of V whose fragments come next, or -1
-    float nm[NS];
-#pragma unroll
-    for (int x = 0; x < NS; ++x) {
-      nm[x] = m[x] == -INFINITY ? 0.f : kManyUp - m[x];
-      lb[x] = 0.f;
-    }
+    const float nm = m == -INFINITY ? 0.f : kManyUp - m;
+    lb = 0.f;
 #pragma unroll
     for (int t = 0; t < KC; ++t) {
       const v8h f = __builtin_bit_cast(v8h, frag[t % AHEAD]);
+      qk(next, t, f);
 #pragma unroll
-      for (int x = 0; x < NS; ++x) {
-        qk(next, x, t, f);
-#pragma unroll
-        for (int w = t * 8 / KC; w < (t + 1) * 8 / KC; ++w) prob(s, x, w, nm[x]);
-      }
+      for (int w = t * 8 / KC; w < (t + 1) * 8 / KC; ++w) prob(s, w, nm);
       extra(t);
       if (t + AHEAD < KC) fetch_k(t + AHEAD, half);
       else if constexpr (then >= 0) fetch_v(t + AHEAD - KC, then);
     }
-    bool again = false;
+    if (__any(!(lb <= kMost) || m == -INFINITY)) {
+      float tm = s[0];
 #pragma unroll
-    for (int x = 0; x < NS; ++x) again |= !(lb[x] <= kMost) || m[x] == -INFINITY;
-    if (__any(again)) {
+      for (int e = 1; e < 16; ++e) tm = fmaxf(tm, s[e]);
+      const float most = half_max(tm);
+      tm = most * cr;
+      // only the rows that need it move: no row's result depends on its neighbours
+      const bool moves = (half_max(lb) > kMost || m == -INFINITY) && tm > m;
+      const float f = __builtin_amdgcn_exp2f(m - (moves ? tm : m == -INFINITY ? 0.f : m));
+      l *= f;
 #pragma unroll
-      for (int x = 0; x < NS; ++x) {
-        float tm = s[x][0];
+      for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int e = 1; e < 16; ++e) tm = fmaxf(tm, s[x][e]);
-        const float most = half_max(tm);
-        tm = most * cr[x];
-        // only the rows that need it move: no row's result depends on its neighbours
-        const bool moves = (half_max(lb[x]) > kMost || m[x] == -INFINITY) && tm > m[x];
-        const float f = __builtin_amdgcn_exp2f(m[x] - (moves ? tm : m[x] == -INFINITY ? 0.f : m[x]));
-        l[x] *= f;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[x][d][e] *= f;
-        const float step = rebase(moves, most, cr[x], m[x], from[x][0]);
-        if (__any(step != 0.f)) {
-          s[x] += step;
-          next[x] += step;
-          from[x] += step;
-          asm volatile("" : "+v"(from[x]));
-        }
-        lb[x] = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) prob(s, x, w, m[x] == -INFINITY ? 0.f : kManyUp - m[x]);
+        for (int e = 0; e < 16; ++e) o[d][e] *= f;
+      const float step = rebase(moves, most, cr, m, from[0]);
+      if (__any(step != 0.f)) {
+        s += step;
+        next += step;
+        from += step;
+        asm volatile("" : "+v"(from));
       }
-    }
+      lb = 0.f;
 #pragma unroll
-    for (int x = 0; x < NS; ++x) l[x] += lb[x];
+      for (int w = 0; w < 8; ++w) prob(s, w, m == -INFINITY ? 0.f : kManyUp - m);
+    }
+    l += lb;
   };
   // Phase 2: the probabilities by V's half `half`; convert(t) is called in every step.
   auto phase2 = [&](auto half_, auto then_, auto&& convert) {
@@ -902,12 +878,9 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
     for (int t = 0; t < KC; ++t) {
       convert(t);
       const v8h f = __builtin_bit_cast(v8h, frag[t % AHEAD]);
-#pragma unroll
-      for (int x = 0; x < NS; ++x) {
-        const uint32_t* w = &pk[x][t / DB * 4];
-        const v4i pv = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-        o[x][t % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, __builtin_bit_cast(v8h, pv), o[x][t % DB], 0, 0, 0);
-      }
+      const uint32_t* w = &pk[t / DB * 4];
+      const v4i pv = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+      o[t % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, __builtin_bit_cast(v8h, pv), o[t % DB], 0, 0, 0);
       if (t + AHEAD < KC) fetch_v(t + AHEAD, half);
       else fetch_k(t + AHEAD - KC, then);
     }
@@ -941,8 +914,7 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
 #pragma unroll
     for (int t = 0; t < KC; ++t) {
       fetch_k(t, 0);
-#pragma unroll
-      for (int x = 0; x < NS; ++x) qk(s0, x, t, __builtin_bit_cast(v8h, frag[t % AHEAD]));
+      qk(s0, t, __builtin_bit_cast(v8h, frag[t % AHEAD]));
     }
 #pragma unroll
     for (int t = 0; t < AHEAD; ++t) fetch_k(t, 1);
@@ -990,33 +962,30 @@ __global__ void __launch_bounds__(64 * C::W, C::W / 4) attn_many_kernel(Args p) 
     }
   }
 
+  l = half_sum(l);
+  const int rl = wave * 32 + lr, row = r0 + rl;
+  if (rl >= nrows) return;
+  if (p.po) {
+    const float f = to_m(from[0], cr, m);
+    const int64_t at = (((int64_t)part * a.B + b) * c.Hkv + hk) * p.rows + row;
 #pragma unroll
-  for (int x = 0; x < NS; ++x) {
-    l[x] = half_sum(l[x]);
-    const int rl = (wave * NS + x) * 32 + lr, row = r0 + rl;
-    if (rl >= nrows) continue;
-    if (p.po) {
-      const float f = to_m(from[x][0], cr[x], m[x]);
-      const int64_t at = (((int64_t)part * a.B + b) * c.Hkv + hk) * p.rows + row;
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<v4f*>(p.po + at * D + 32 * d + 8 * i + 4 * h) =
+            (v4f){o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]} * f;
+    if (h == 0) *reinterpret_cast<v2f*>(p.pml + at * 2) = (v2f){m, l * f};
+  } else {
+    const float inv = l == 0.f ? 0.f : p.v / l;
+    int g;
+    const int t = div_by(row, p.g, g);
+    uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * G + g) * a.o_sh;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<v4f*>(p.po + at * D + 32 * d + 8 * i + 4 * h) =
-              (v4f){o[x][d][4 * i], o[x][d][4 * i + 1], o[x][d][4 * i + 2], o[x][d][4 * i + 3]} * f;
-      if (h == 0) *reinterpret_cast<v2f*>(p.pml + at * 2) = (v2f){m[x], l[x] * f};
-    } else {
-      const float inv = l[x] == 0.f ? 0.f : p.v / l[x];
-      int g;
-      const int t = div_by(row, p.g, g);
-      uint16_t* out = (uint16_t*)a.out + b * a.o_sb + t * a.o_st + (int64_t)(hk * G + g) * a.o_sh;
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint2*>(out + 32 * d + 8 * i + 4 * h) =
-              pack_out(p, (v4f){o[x][d][4 * i], o[x][d][4 * i + 1], o[x][d][4 * i + 2], o[x][d][4 * i + 3]} * inv);
-    }
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint2*>(out + 32 * d + 8 * i + 4 * h) =
+            pack_out(p, (v4f){o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]} * inv);
   }
 }
 
@@ -1090,7 +1059,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(Args p) {
 template <int D, int MT, int NW>
 void launch_few(const Args& p, hipStream_t st) {
   const unsigned grid = (unsigned)(p.a.B * p.c.Hkv * p.tiles.d * p.parts.d);
-  if (p.tiles.d == 1) attn_few_kernel<Few<D, MT, NW, true>><<<grid, 64 * NW, 0, st>>>(p);
+  if (D > 64 && p.tiles.d == 1) attn_few_kernel<Few<D, MT, NW, D != 64>><<<grid, 64 * NW, 0, st>>>(p);
   else attn_few_kernel<Few<D, MT, NW, false>><<<grid, 64 * NW, 0, st>>>(p);
 }
 
