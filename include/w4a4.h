@@ -596,7 +596,8 @@ int w4a4_cache_read(const w4a4_kvcache* c, const int32_t* slots, int64_t M, void
  * h reads KV head h / (Hq / Hkv).  A row that sees no key is zero.
  * Keys and values enter the products exactly as the cache holds them (fp16),
  * queries as fp16 after a power of two per row, probabilities as fp16; scores,
- * softmax sums and outputs accumulate in fp32; one rounding to bf16.
+ * softmax sums and outputs accumulate in fp32; one rounding to bf16.  A score
+ * beyond fp32's range may make its row NaN.
  *  q, out    bf16 [B, T, Hq, D], channels contiguous; the other strides are
  *            in elements, multiples of 8, at most 2^30 (batch: 2^38); those of
  *            a dimension of one are not used.  Pointers 16-byte aligned.  out

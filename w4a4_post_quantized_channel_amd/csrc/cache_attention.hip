@@ -16,7 +16,8 @@
 // and v_scale enter c and the last division.  A query row is multiplied by the
 // power of two that puts its largest channel at 2^13: bf16's eight bits then
 // fit fp16 for every channel down to 2^-27 of the largest.  Probabilities are
-// rounded to fp16 (off by 2^-11 of them, an eighth of the output's own rounding).
+// rounded to fp16 (off by 2^-11 of them, an eighth of the output's own rounding:
+// in fp32 or as two fp16 numbers the second product would take twice as long).
 //
 // A wave works alone on every NW-th block of its workgroup's part, for
 // 16 MT rows at once:
@@ -34,15 +35,18 @@
 // by a second kernel.
 //
 // What bounds it.  One token each of 64 sequences, 32 heads over 8 of 128, 4096
-// to 8192 keys: the caches' 463 MB at 5.4 TB/s, 85 us (a device copy reaches
-// 5.1).  There each key is read by one workgroup only, past the caches: 92 us
-// against 102 with ordinary loads (widths 128 and 256; 7% slower where the history fits the 256 MB
-// cache and is read again at once), and in one part: 85 against 89 in two and 92
-// in three.  A chunk of 8 x 50 queries, 16 heads over 4, 2090 keys (21 us): turns
+// to 8192 keys: the caches' 463 MB at 5.5 TB/s, 84 us (a device copy reaches
+// 5.1).  There each key is read by one workgroup only, past the caches (at widths
+// 128 and 256): 92 us against 102 with ordinary loads (7% slower where the
+// history fits the 256 MB cache and is read again at once), and in one part: 85
+// against 89 in two and 92 in three.  Parts follow max_len: where one sequence of
+// a batch is far longer than the rest, its workgroups walk it alone.  A chunk of
+// 8 x 50 queries, 16 heads over 4, 2090 keys (21 us): turns
 // of 7000 cycles in which two waves a SIMD convert codes (1150 cycles a block and
 // wave), multiply (1024) and take exponentials (600), one after the other for
 // each wave; 64 rows a wave convert half as often but leave one wave a SIMD: 34.
-// 2 x 13 queries, 8 heads over one of 256, 5131 keys (14.2 us and 3 of join): one
+// Blocks of absent pages take the time of others.  2 x 13 queries, 8 heads over
+// one of 256, 5131 keys (14.4 us and 2.8 of join): one
 // turn a wave; seven row tiles read the same keys through the L2s, 4 MB each.
 // One workgroup's call (1 query, 317 keys) takes 5.5 to 6 us: arguments, lens and
 // table, keys and the join wait for each other (the table waiting for lens: 0.3
@@ -64,9 +68,9 @@ constexpr float kLazy = 8.f, kFewUp = 7.f;   // p < 2^15
 // Where |m| reaches this its last place, an eighth and more, is no small part of
 // what p may grow by (from 2^24 on p passed fp16, or all of a row's were lost).
 // Such a row's scores are summed from minus a base on, the score that m stands
-// for.  The kernel for many rows always starts its sums there (no time at width 128,
-// 2% at 64); the one for few takes its keys once more, with bases, where a
-// row turns out to need one: in the loop they cost 2 to 7% there.
+// for.  The kernel for many rows always starts its sums there (no time at width
+// 128, 2% at 64); the one for few takes its keys once more, with bases, where a
+// row turns out to need one: in its loop they cost 2 to 7%.
 constexpr float kFar = 1048576.f;
 constexpr int BN = kCacheBlock;
 

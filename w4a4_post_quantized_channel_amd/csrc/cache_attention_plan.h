@@ -29,9 +29,10 @@ inline int64_t plan_blocks(int64_t max_len) {
 
 // The kernels of a head width.  16 and 32 rows: every wave takes key blocks of
 // its own, so an iteration covers ``waves`` blocks; more rows: the waves share a
-// block.  fit: workgroups of a CU at once.  Microseconds: us, an iteration with
-// all CUs full; start, a workgroup's start and end; next, what those of the
-// workgroups behind it add (which overlap where two fit).
+// block.  Fitted numbers, no residencies: fit, workgroups of a CU that ``us`` is
+// for (four of {16, 4} have room at width 64, three at 128, two at 256).
+// Microseconds: us, an iteration with that many on all CUs; start, a workgroup's
+// start and end; next, what those of the workgroups behind it add.
 struct CacheAttnShape {
   int rows, waves, fit;
   double us, start, next;
@@ -54,7 +55,14 @@ constexpr int kCacheCUs = 256;
 //             four, 41 with 128 rows;  2 x 300, 4 over 4, 1500: 22, 23 and 30;
 //             16 x 16, 32 over 4, 4096: 91, 79 and 58 (32 rows: never the fastest)
 // Iterations (0.65 of their time where a CU holds one workgroup of two), starts,
-// and the join's launch, parts and bytes; never less than reading the caches.  A
+// and the join's launch, parts and bytes (fitted with the rest: 8 TB/s, where a
+// copy reaches 5.1); never less than reading the caches.  Against every tile in
+// 1, 2, 4 .. 64 parts, 40 shapes drawn at random and eight single tokens with 600
+// to 1200 units: 1.04 times the fastest in the geometric mean, within 5% of it in
+// 38 and 20% in 44 of 48 (all eight of the latter within 3%).  The farthest: 38 x
+// 1, 32 over 8 of width 128, 10541 keys: 106 for 74 in four parts; 54 x 40, 7
+// over 1 of width 256, 116 keys: 24 for 17 with 128 rows; 7 x 1, 28 over 4 of
+// width 128, 1528 keys: 12.6 for 9.7 with four waves in eight parts.  A
 // batch of unequal histories gains nothing from more parts (64 sequences of 4096
 // to 8192 keys, 32 heads over 8 of width 128: 85 in one part, 89 in two, 92 in
 // three, each with its caches cold).

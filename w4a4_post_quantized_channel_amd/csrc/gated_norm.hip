@@ -5,12 +5,15 @@
 // accuracy), and y.  Sums go over a thread's values, the lanes of a wave and
 // the waves, all in fp32.
 //
-// A row stays in registers: each input is read once, each output written once.
-// Rows of up to 512 channels belong to one wave, four rows a workgroup; longer
-// ones to a workgroup of one thread per eight channels (two or three times eight
-// beyond 8192).  Where the width is no multiple of eight, the channels behind
-// the last eight are a thread's each: loads of single channels by one thread,
-// one after the other, cost 777 rows of 1155 channels 4.4 us of 10.2.
+// A row of up to 8192 channels stays in registers: each input is read once, each
+// output written once.  Rows of up to 512 channels belong to one wave, four rows a
+// workgroup; longer ones to a workgroup of one thread per eight channels (two or
+// three times eight beyond 8192, which 128 registers do not hold: a multiple of
+// eight keeps 12 of a thread's in scratch memory, 4096 rows of 16384 in bf16 take
+// 116 us, 4.6 TB/s, and of 8192 57; another width 164, rows of 16383 take 311).
+// Where the width is no multiple of eight, the channels behind the last eight are
+// a thread's each: loads of single channels by one thread, one after the other,
+// cost 777 rows of 1155 channels 4.4 us of 10.2.
 // Rows that follow each other belong to the same workgroup, which keeps its
 // channels' gate, scale and shift while they stay the same (read for every row
 // they would be two thirds of what a compute unit loads at 5120 channels), and
@@ -19,7 +22,8 @@
 // Bound by memory for many rows: 12480 of 5120 channels, fp32 stream, bf16 h and
 // y (767 MB), take 155 us, 4.9 TB/s (a thread per channel took 985, a workgroup
 // per row 237).  For few rows it is a launch and the chain of a row: loads, two
-// or three sums and the store, 4.1 us for 64 rows of 2048, 5.8 for the 777.
+// or three sums, each with the weights that are loaded behind it, and the store,
+// 4.1 us for 64 rows of 2048, 5.8 for the 777.
 #include "cache.h"
 #include "device_common.h"
 #include "divisor.h"
@@ -243,7 +247,9 @@ __global__ void __launch_bounds__(1024) gated_norm_kernel(w4a4_gated a, int rows
 
 hipError_t launch_gated_norm(const w4a4_gated& g, hipStream_t st) {
   const int C = (int)g.C;
-  // One row a workgroup (or wave) until the card is full, then runs of rows.
+  // One row a workgroup (or wave) up to 2048 threads a CU, then runs of rows.
+  // (Registers let 20 waves of a CU run at once, 16 where a wave has a row: 12480
+  // rows of 5120 are 735 workgroups of ten waves, two of them a CU.)
   const int items = C / 8 + C % 8;
   const bool wave = items <= 64, tail = C % 8 != 0;
   const unsigned threads = wave ? 256 : items <= 1024 ? (unsigned)((items + 63) / 64 * 64) : 1024;

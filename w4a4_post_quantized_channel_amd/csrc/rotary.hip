@@ -15,9 +15,12 @@
 // thread.
 //
 // Bound by memory: 12480 tokens of 16 + 16 heads of 128 in bf16 (204 MB) take 42
-// us, 4.9 TB/s; a thread per pair took 96.  One token's call is a launch: 400
-// tokens of 16 + 4 heads take 6 us, three dependent loads (positions, table and
-// rows) and the sines.
+// us, 4.9 TB/s; a thread per pair took 96.  Heads of 72 with all 36 pairs in
+// halves, which no eight pairs split, go by one pair a thread: 36 us, 3.2 TB/s,
+// where adjacent pairs of the same width take 24.  Few tokens: 400 of 16 + 4 heads
+// take 6 us, most of it the table entries and positions of a thread's eight pairs
+// (four of adjacent ones), which are loaded under each pair's condition, one pair
+// after the other.
 #include "cache.h"
 #include "device_common.h"
 #include "divisor.h"
