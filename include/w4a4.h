@@ -430,7 +430,8 @@ size_t w4a4_workspace_size(int64_t M, int64_t N, int64_t K, int32_t fmt);
  * queries are the sequence's last T positions).  Query head h reads KV head
  * h / (Hq / Hkv).  A row that sees no key is zero.  Scores, softmax sums and
  * outputs accumulate in fp32; the probabilities enter the second product
- * as bf16; one rounding to bf16 at the end.
+ * as bf16; one rounding to bf16 at the end.  Scores of more than 2^26 in
+ * magnitude may make their row NaN or zero (fp32 holds them to 4 at best).
  *  q, out    bf16 [B, T, Hq, D];  k_prefix, v_prefix  bf16 [P, Hkv, D];
  *            k_own, v_own  bf16 [B, S, Hkv, D].  The last dimension is
  *            contiguous; the other strides are in elements, multiples of 8,
